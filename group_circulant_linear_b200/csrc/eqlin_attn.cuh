@@ -1,0 +1,99 @@
+// eqlin_attn.cuh -- what the attention kernels share: the call's parameters,
+// the documents, and the score function.
+//
+// Tokens lie in one packed sequence [N]; a document is a contiguous range of
+// them, and a token attends to the tokens of its document.  With u = scale
+// q_i.k_j (natural units throughout, base-2 inside the kernels):
+//
+//   c = cap tanh(u / cap)   (cap > 0),   c = u   (cap = 0)
+//   s = c - slope_h sum_a |pos[i, a] - pos[j, a]|
+//   lse_i = log sum_j exp s_ij,   P = exp(s - lse),   o_i = sum_j P_ij v_j
+//
+//   dv_j = sum_i P_ij do_i,   dP = do.v,   delta_i = do_i.o_i
+//   ds = P (dP - delta),      du = ds (1 - tanh^2(u / cap))
+//   dq_i = scale sum_j du k_j,   dk_j = scale sum_i du q_i
+//
+// Rows outside every document get o = 0, lse = 0 and zero gradients.
+#pragma once
+
+#include "eqlin_internal.cuh"
+
+namespace eqlin {
+namespace attn {
+
+constexpr int kMaxAxes = 3;
+constexpr int kMaxHeadDim = 128;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+struct Params {
+  const void* q;
+  const void* k;
+  const void* v;
+  const void* go;
+  void* o;                // read by the backward
+  void* dq;
+  void* dk;
+  void* dv;
+  float* lse;             // [H][N]
+  float* delta;           // [H][N]
+  int64_t qs, ks, vs, os, gos, dqs, dks, dvs;   // elements per token
+  int64_t N;
+  const int32_t* offsets; // [docs + 1], or null: documents of `len` tokens
+  int64_t docs, len;
+  const float* pos;       // [N][axes]
+  const float* slopes;    // [H]
+  int axes;               // 0: no bias
+  int H, K, D;
+  int hint;               // blocks per (document, head); each walks the tiles hint apart
+  float scale, cap;
+  int* err;               // error record (eqlin_wait.cuh), or null
+  uint32_t wait_limit;
+};
+
+// The block's document, head and first tile: tiles vary fastest, so that
+// blocks which share keys run together.
+struct Work {
+  int64_t doc;
+  int head, tile;
+};
+__device__ __forceinline__ Work work_of(const Params& p, int heads) {
+  const uint32_t b = blockIdx.x;
+  const uint32_t rest = b / (uint32_t)p.hint;
+  Work w;
+  w.tile = (int)(b - rest * (uint32_t)p.hint);
+  const uint32_t d = rest / (uint32_t)heads;
+  w.head = (int)(rest - d * (uint32_t)heads);
+  w.doc = d;
+  return w;
+}
+
+// A document's tokens [lo, hi).  Offsets are forced into [0, N] and into
+// order, so that wrong ones cannot lead out of the tensors.
+__device__ __forceinline__ void doc_range(const Params& p, int64_t doc, int64_t& lo, int64_t& hi) {
+  if (!p.offsets) {
+    lo = doc * p.len;
+    hi = lo + p.len;
+    return;
+  }
+  lo = min(max((int64_t)p.offsets[doc], (int64_t)0), p.N);
+  hi = min(max((int64_t)p.offsets[doc + 1], lo), p.N);
+}
+
+// Blocks whose document index is `docs` (packed calls only) clear the rows
+// outside all documents: [0, first offset) and [last offset, N).
+template <typename F>
+__device__ __forceinline__ void outside_rows(const Params& p, int tile, F&& clear) {
+  const int64_t a = min(max((int64_t)p.offsets[0], (int64_t)0), p.N);
+  const int64_t b = min(max((int64_t)p.offsets[p.docs], a), p.N);
+  for (int64_t r = tile; r < a; r += p.hint) clear(r);
+  for (int64_t r = b + tile; r < p.N; r += p.hint) clear(r);
+}
+
+}  // namespace attn
+
+// f32 (and the reference for the other types): CUDA cores.
+cudaError_t launch_attn_simt_forward(const attn::Params& p, eqlin_dtype_t dt, cudaStream_t st);
+cudaError_t launch_attn_simt_backward(const attn::Params& p, eqlin_dtype_t dt, cudaStream_t st);
+
+}  // namespace eqlin

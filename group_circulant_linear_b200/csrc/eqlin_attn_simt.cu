@@ -1,0 +1,485 @@
+// eqlin_attn_simt.cu -- document attention on the CUDA cores, in FP32.
+//
+// One block owns 64 rows of one head of one document and walks the other
+// side in tiles of 64, with one pass over it: the forward keeps each row's
+// running maximum and sum and rescales its output when the maximum grows.
+// The backward is two kernels of the same shape, so no sum needs atomics and
+// results do not depend on the order in which blocks run: one owns query rows
+// (dq, and delta on the way), the other key rows (dk, dv, over all query
+// heads that share them).
+//
+// 256 threads form a 16 x 16 grid; thread (ty, tx) owns rows 4ty .. 4ty+3
+// and, of a 64 x 64 product, columns tx + 16j: reads of the moving operand are
+// then 16 rows apart by D + 4 floats, free of bank conflicts, and those of the
+// rows broadcast.  Per four feature steps that is 8 16-byte shared loads for
+// 64 FMAs, which bounds the kernels (shared-memory issue, not FFMA).
+#include "eqlin_attn.cuh"
+
+namespace eqlin {
+namespace attn_simt {
+
+using namespace attn;
+
+constexpr int B = 64;                     // rows and columns of a tile
+constexpr int kThreads = 256;
+constexpr int LDP = B + 4;
+
+template <int DP> struct Cfg {
+  static constexpr int LD = DP + 4;
+  static constexpr int TILE = B * LD;     // floats
+  static constexpr int DC = (DP + 63) / 64;   // float4 groups of a thread's output columns
+};
+
+// Rows [r0, r0 + 64) of a head as FP32, zero past `hi` and past D.
+template <int DP, typename E>
+__device__ __forceinline__ void load_tile(float* dst, const void* src, int64_t stride, int64_t head_off, int64_t r0,
+                                          int64_t hi, int D, float mul) {
+  constexpr int V = 16 / sizeof(E);
+  for (int i = threadIdx.x; i < B * (DP / V); i += kThreads) {
+    const int r = i / (DP / V), c = (i - r * (DP / V)) * V;
+    float f[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = 0.f;
+    if (r0 + r < hi && c < D) {
+      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const E*>(src) + (r0 + r) * stride + head_off + c);
+      const E* e = reinterpret_cast<const E*>(&u);
+#pragma unroll
+      for (int k = 0; k < V; ++k) f[k] = Elem<E>::to_f(e[k]) * mul;
+    }
+#pragma unroll
+    for (int k = 0; k < V; k += 4)
+      *reinterpret_cast<float4*>(dst + r * Cfg<DP>::LD + c + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+  }
+}
+
+// acc[i][j] = A[row 4ty+i] . Bm[row tx+16j] over DP features
+template <int DP>
+__device__ __forceinline__ void mm_nt(const float* A, const float* Bm, float (&acc)[4][4]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+#pragma unroll 4
+  for (int d = 0; d < DP; d += 4) {
+    float4 a[4], b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * Cfg<DP>::LD + d);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(Bm + (tx + 16 * j) * Cfg<DP>::LD + d);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
+        acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
+        acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
+        acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
+      }
+  }
+}
+
+// out[i][c] += sum_j P[4ty+i][j] M[j][4tx + 64c ..]
+template <int DP>
+__device__ __forceinline__ void mm_nn(const float* P, const float* M, float (&out)[4][Cfg<DP>::DC][4]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  if (4 * tx >= DP) return;
+#pragma unroll 2
+  for (int j = 0; j < B; j += 4) {
+    float4 a[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(P + (4 * ty + i) * LDP + j);
+#pragma unroll
+    for (int jj = 0; jj < 4; ++jj)
+#pragma unroll
+      for (int c = 0; c < Cfg<DP>::DC; ++c) {
+        const float4 m = *reinterpret_cast<const float4*>(M + (j + jj) * Cfg<DP>::LD + 4 * tx + 64 * c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const float w = jj == 0 ? a[i].x : jj == 1 ? a[i].y : jj == 2 ? a[i].z : a[i].w;
+          out[i][c][0] = fmaf(w, m.x, out[i][c][0]);
+          out[i][c][1] = fmaf(w, m.y, out[i][c][1]);
+          out[i][c][2] = fmaf(w, m.z, out[i][c][2]);
+          out[i][c][3] = fmaf(w, m.w, out[i][c][3]);
+        }
+      }
+  }
+}
+
+template <int DP, typename E>
+__device__ __forceinline__ void store_rows(void* dst, int64_t stride, int64_t head_off, int64_t r0, int64_t hi, int D,
+                                           const float (&v)[4][Cfg<DP>::DC][4]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int64_t r = r0 + 4 * ty + i;
+    if (r >= hi) continue;
+#pragma unroll
+    for (int c = 0; c < Cfg<DP>::DC; ++c) {
+      const int d = 4 * tx + 64 * c;
+      if (d >= D) continue;               // D is a multiple of 4
+      E* o = static_cast<E*>(dst) + r * stride + head_off + d;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = Elem<E>::from_f(v[i][c][k]);
+    }
+  }
+}
+
+template <typename E>
+__device__ __forceinline__ void clear_row(void* dst, int64_t stride, int64_t head_off, int64_t r, int D) {
+  for (int d = threadIdx.x; d < D; d += kThreads)
+    static_cast<E*>(dst)[r * stride + head_off + d] = Elem<E>::from_f(0.f);
+}
+
+// Positions of tile rows: [axes][64].
+__device__ __forceinline__ void load_pos(float* dst, const Params& p, int64_t r0, int64_t hi) {
+  for (int i = threadIdx.x; i < B * p.axes; i += kThreads) {
+    const int a = i / B, r = i - a * B;
+    dst[i] = r0 + r < hi ? p.pos[(r0 + r) * p.axes + a] : 0.f;
+  }
+}
+__device__ __forceinline__ float distance(const float* pr, int r, const float* pc, int c, int axes) {
+  float d = 0.f;
+  for (int a = 0; a < axes; ++a) d += fabsf(pr[a * B + r] - pc[a * B + c]);
+  return d;
+}
+
+// ------------------------------------------------------------------ forward
+
+template <int DP, typename E>
+__global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(16) float sm[];
+  float* Q = sm;
+  float* K = Q + Cfg<DP>::TILE;
+  float* V = K + Cfg<DP>::TILE;
+  float* P = V + Cfg<DP>::TILE;
+  float* pq = P + B * LDP;
+  float* pk = pq + kMaxAxes * B;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  grid_dep_launch();
+  grid_dep_wait();
+  const Work w = work_of(p, p.H);
+  const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)(w.head / (p.H / p.K)) * p.D;
+  if (w.doc == p.docs) {
+    outside_rows(p, w.tile, [&](int64_t r) {
+      clear_row<E>(p.o, p.os, qh, r, p.D);
+      if (threadIdx.x == 0) p.lse[(int64_t)w.head * p.N + r] = 0.f;
+    });
+    return;
+  }
+  int64_t lo, hi;
+  doc_range(p, w.doc, lo, hi);
+  const float slope = p.axes ? p.slopes[w.head] : 0.f;
+  const float icap = p.cap > 0.f ? 1.f / p.cap : 0.f;
+  for (int64_t r0 = lo + (int64_t)w.tile * B; r0 < hi; r0 += (int64_t)p.hint * B) {
+    __syncthreads();
+    load_tile<DP, E>(Q, p.q, p.qs, qh, r0, hi, p.D, p.scale);
+    load_pos(pq, p, r0, hi);
+    float m[4], l[4], o[4][Cfg<DP>::DC][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      m[i] = -INFINITY;
+      l[i] = 0.f;
+#pragma unroll
+      for (int c = 0; c < Cfg<DP>::DC; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][c][k] = 0.f;
+    }
+    for (int64_t c0 = lo; c0 < hi; c0 += B) {
+      __syncthreads();
+      load_tile<DP, E>(K, p.k, p.ks, kh, c0, hi, p.D, 1.f);
+      load_tile<DP, E>(V, p.v, p.vs, kh, c0, hi, p.D, 1.f);
+      load_pos(pk, p, c0, hi);
+      __syncthreads();
+      float s[4][4];
+      mm_nt<DP>(Q, K, s);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float top = m[i];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (p.cap > 0.f) s[i][j] = p.cap * tanhf(s[i][j] * icap);
+          if (p.axes) s[i][j] -= slope * distance(pq, 4 * ty + i, pk, tx + 16 * j, p.axes);
+          if (c0 + tx + 16 * j >= hi) s[i][j] = -INFINITY;
+          top = fmaxf(top, s[i][j]);
+        }
+#pragma unroll
+        for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float base = top == -INFINITY ? 0.f : top;
+        const float fix = expf(m[i] - base);
+        m[i] = top;
+        float sum = 0.f;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          s[i][j] = expf(s[i][j] - base);
+          sum += s[i][j];
+          P[(4 * ty + i) * LDP + tx + 16 * j] = s[i][j];
+        }
+        l[i] = l[i] * fix + sum;          // this thread's columns; joined at the end
+#pragma unroll
+        for (int c = 0; c < Cfg<DP>::DC; ++c)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) o[i][c][k] *= fix;
+      }
+      __syncthreads();
+      mm_nn<DP>(P, V, o);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
+      const float inv = 1.f / l[i];
+#pragma unroll
+      for (int c = 0; c < Cfg<DP>::DC; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) o[i][c][k] *= inv;
+      const int64_t r = r0 + 4 * ty + i;
+      if (tx == 0 && r < hi) p.lse[(int64_t)w.head * p.N + r] = m[i] + logf(l[i]);
+    }
+    store_rows<DP, E>(p.o, p.os, qh, r0, hi, p.D, o);
+  }
+}
+
+// ----------------------------------------------------------------- backward
+
+// P and du of one 64 x 64 tile from its raw products u (rows and columns as in
+// mm_nt), dP, and the softmax statistics of the query side.
+__device__ __forceinline__ void tile_grad(const Params& p, float u, float dp, float dist, float lse, float delta,
+                                          bool on, float icap, float slope, float& prob, float& du) {
+  float slope_u = 1.f, s = u;
+  if (p.cap > 0.f) {
+    const float t = tanhf(u * icap);
+    s = p.cap * t;
+    slope_u = 1.f - t * t;
+  }
+  if (p.axes) s -= slope * dist;
+  prob = on ? expf(s - lse) : 0.f;
+  du = on ? prob * (dp - delta) * slope_u : 0.f;
+}
+
+template <int DP, typename E>
+__global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(16) float sm[];
+  float* Q = sm;
+  float* G = Q + Cfg<DP>::TILE;
+  float* K = G + Cfg<DP>::TILE;
+  float* V = K + Cfg<DP>::TILE;
+  float* P = V + Cfg<DP>::TILE;
+  float* pq = P + B * LDP;
+  float* pk = pq + kMaxAxes * B;
+  float* dl = pk + kMaxAxes * B;
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  grid_dep_launch();
+  grid_dep_wait();
+  const Work w = work_of(p, p.H);
+  const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)(w.head / (p.H / p.K)) * p.D;
+  if (w.doc == p.docs) {
+    outside_rows(p, w.tile, [&](int64_t r) { clear_row<E>(p.dq, p.dqs, qh, r, p.D); });
+    return;
+  }
+  int64_t lo, hi;
+  doc_range(p, w.doc, lo, hi);
+  const float slope = p.axes ? p.slopes[w.head] : 0.f;
+  const float icap = p.cap > 0.f ? 1.f / p.cap : 0.f;
+  for (int64_t r0 = lo + (int64_t)w.tile * B; r0 < hi; r0 += (int64_t)p.hint * B) {
+    __syncthreads();
+    load_tile<DP, E>(K, p.o, p.os, qh, r0, hi, p.D, 1.f);   // o, for delta
+    load_tile<DP, E>(G, p.go, p.gos, qh, r0, hi, p.D, 1.f);
+    load_tile<DP, E>(Q, p.q, p.qs, qh, r0, hi, p.D, p.scale);
+    load_pos(pq, p, r0, hi);
+    __syncthreads();
+    {   // delta of row t / 4, four threads a row
+      const int r = threadIdx.x >> 2;
+      float d = 0.f;
+      for (int c = (threadIdx.x & 3); c < DP; c += 4) d = fmaf(G[r * Cfg<DP>::LD + c], K[r * Cfg<DP>::LD + c], d);
+      d += __shfl_xor_sync(0xffffffffu, d, 1);
+      d += __shfl_xor_sync(0xffffffffu, d, 2);
+      if ((threadIdx.x & 3) == 0) {
+        dl[r] = d;
+        if (r0 + r < hi) p.delta[(int64_t)w.head * p.N + r0 + r] = d;
+      }
+    }
+    __syncthreads();
+    float lse[4], delta[4], acc[4][Cfg<DP>::DC][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t r = r0 + 4 * ty + i;
+      lse[i] = r < hi ? p.lse[(int64_t)w.head * p.N + r] : 0.f;
+      delta[i] = dl[4 * ty + i];
+#pragma unroll
+      for (int c = 0; c < Cfg<DP>::DC; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][c][k] = 0.f;
+    }
+    for (int64_t c0 = lo; c0 < hi; c0 += B) {
+      __syncthreads();
+      load_tile<DP, E>(K, p.k, p.ks, kh, c0, hi, p.D, 1.f);
+      load_tile<DP, E>(V, p.v, p.vs, kh, c0, hi, p.D, 1.f);
+      load_pos(pk, p, c0, hi);
+      __syncthreads();
+      float u[4][4], dp[4][4];
+      mm_nt<DP>(Q, K, u);
+      mm_nt<DP>(G, V, dp);
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int c = tx + 16 * j, r = 4 * ty + i;
+          float prob, du;
+          tile_grad(p, u[i][j], dp[i][j], distance(pq, r, pk, c, p.axes), lse[i], delta[i],
+                    r0 + r < hi && c0 + c < hi, icap, slope, prob, du);
+          P[r * LDP + c] = du;
+        }
+      __syncthreads();
+      mm_nn<DP>(P, K, acc);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < Cfg<DP>::DC; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][c][k] *= p.scale;
+    store_rows<DP, E>(p.dq, p.dqs, qh, r0, hi, p.D, acc);
+  }
+}
+
+template <int DP, typename E>
+__global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(16) float sm[];
+  float* K = sm;
+  float* V = K + Cfg<DP>::TILE;
+  float* Q = V + Cfg<DP>::TILE;
+  float* G = Q + Cfg<DP>::TILE;
+  float* P = G + Cfg<DP>::TILE;
+  float* pq = P + B * LDP;
+  float* pk = pq + kMaxAxes * B;
+  float* stat = pk + kMaxAxes * B;         // lse [64], delta [64]
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  grid_dep_launch();
+  grid_dep_wait();
+  const Work w = work_of(p, p.K);
+  const int rep = p.H / p.K;
+  const int64_t kh = (int64_t)w.head * p.D;
+  if (w.doc == p.docs) {
+    outside_rows(p, w.tile, [&](int64_t r) {
+      clear_row<E>(p.dk, p.dks, kh, r, p.D);
+      clear_row<E>(p.dv, p.dvs, kh, r, p.D);
+    });
+    return;
+  }
+  int64_t lo, hi;
+  doc_range(p, w.doc, lo, hi);
+  const float icap = p.cap > 0.f ? 1.f / p.cap : 0.f;
+  for (int64_t r0 = lo + (int64_t)w.tile * B; r0 < hi; r0 += (int64_t)p.hint * B) {
+    __syncthreads();
+    load_tile<DP, E>(K, p.k, p.ks, kh, r0, hi, p.D, 1.f);
+    load_tile<DP, E>(V, p.v, p.vs, kh, r0, hi, p.D, 1.f);
+    load_pos(pk, p, r0, hi);
+    float dk[4][Cfg<DP>::DC][4], dv[4][Cfg<DP>::DC][4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int c = 0; c < Cfg<DP>::DC; ++c)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) dk[i][c][k] = dv[i][c][k] = 0.f;
+    for (int g = 0; g < rep; ++g) {
+      const int head = w.head * rep + g;
+      const int64_t qh = (int64_t)head * p.D;
+      const float slope = p.axes ? p.slopes[head] : 0.f;
+      for (int64_t c0 = lo; c0 < hi; c0 += B) {
+        __syncthreads();
+        load_tile<DP, E>(Q, p.q, p.qs, qh, c0, hi, p.D, p.scale);
+        load_tile<DP, E>(G, p.go, p.gos, qh, c0, hi, p.D, 1.f);
+        load_pos(pq, p, c0, hi);
+        if (threadIdx.x < B) {
+          const bool on = c0 + threadIdx.x < hi;
+          stat[threadIdx.x] = on ? p.lse[(int64_t)head * p.N + c0 + threadIdx.x] : 0.f;
+          stat[B + threadIdx.x] = on ? p.delta[(int64_t)head * p.N + c0 + threadIdx.x] : 0.f;
+        }
+        __syncthreads();
+        float u[4][4], dp[4][4];
+        mm_nt<DP>(K, Q, u);
+        mm_nt<DP>(V, G, dp);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const int c = tx + 16 * j, r = 4 * ty + i;
+            float prob, du;
+            tile_grad(p, u[i][j], dp[i][j], distance(pk, r, pq, c, p.axes), stat[c], stat[B + c],
+                      r0 + r < hi && c0 + c < hi, icap, slope, prob, du);
+            P[r * LDP + c] = prob;
+            dp[i][j] = du;
+          }
+        __syncthreads();
+        mm_nn<DP>(P, G, dv);
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int j = 0; j < 4; ++j) P[(4 * ty + i) * LDP + tx + 16 * j] = dp[i][j];
+        __syncthreads();
+        mm_nn<DP>(P, Q, dk);               // Q carries the scale
+      }
+    }
+    store_rows<DP, E>(p.dk, p.dks, kh, r0, hi, p.D, dk);
+    store_rows<DP, E>(p.dv, p.dvs, kh, r0, hi, p.D, dv);
+  }
+}
+
+// ------------------------------------------------------------------- launch
+
+template <int DP> constexpr int smem_bytes(int tiles) {
+  return (tiles * Cfg<DP>::TILE + B * LDP + 2 * kMaxAxes * B + 2 * B) * (int)sizeof(float);
+}
+
+cudaError_t run(void (*k)(Params), int smem, Params p, int heads, cudaStream_t st) {
+  const int64_t longest = p.len;           // the document length that sets the blocks per head
+  int64_t tiles = (longest + B - 1) / B;
+  if (tiles < 1) tiles = 1;
+  const int64_t items = (p.docs + (p.offsets ? 1 : 0)) * heads;
+  if (items == 0) return cudaSuccess;
+  if (items > 0x7fffffff) return cudaErrorInvalidValue;
+  const int64_t room = 0x7fffffff / items;
+  p.hint = (int)(tiles < room ? tiles : room);
+  cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(k), smem);
+  if (e == cudaSuccess) e = launch_pdl(k, dim3((unsigned)(items * p.hint)), dim3(kThreads), (size_t)smem, st, p);
+  if (e == cudaSuccess) count_launches(1);
+  return e;
+}
+
+template <int DP, typename E>
+cudaError_t forward(const Params& p, cudaStream_t st) {
+  return run(attn_simt_fwd_kernel<DP, E>, smem_bytes<DP>(3), p, p.H, st);
+}
+template <int DP, typename E>
+cudaError_t backward(const Params& p, cudaStream_t st) {
+  const cudaError_t e = run(attn_simt_dq_kernel<DP, E>, smem_bytes<DP>(4), p, p.H, st);
+  return e != cudaSuccess ? e : run(attn_simt_dkv_kernel<DP, E>, smem_bytes<DP>(4), p, p.K, st);
+}
+
+template <typename E>
+cudaError_t pick(const Params& p, bool bwd, cudaStream_t st) {
+  if (p.D <= 32) return bwd ? backward<32, E>(p, st) : forward<32, E>(p, st);
+  if (p.D <= 64) return bwd ? backward<64, E>(p, st) : forward<64, E>(p, st);
+  return bwd ? backward<128, E>(p, st) : forward<128, E>(p, st);
+}
+
+cudaError_t dispatch(const Params& p, eqlin_dtype_t dt, bool bwd, cudaStream_t st) {
+  switch (dt) {
+    case EQLIN_F32: return pick<float>(p, bwd, st);
+    case EQLIN_F16: return pick<__half>(p, bwd, st);
+    default: return pick<__nv_bfloat16>(p, bwd, st);
+  }
+}
+
+}  // namespace attn_simt
+
+cudaError_t launch_attn_simt_forward(const attn::Params& p, eqlin_dtype_t dt, cudaStream_t st) {
+  return attn_simt::dispatch(p, dt, false, st);
+}
+cudaError_t launch_attn_simt_backward(const attn::Params& p, eqlin_dtype_t dt, cudaStream_t st) {
+  return attn_simt::dispatch(p, dt, true, st);
+}
+
+}  // namespace eqlin

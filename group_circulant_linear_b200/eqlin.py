@@ -30,6 +30,17 @@ STATUS = {0: "EQLIN_OK", -1: "EQLIN_ERR_INVALID_ARG", -2: "EQLIN_ERR_UNSUPPORTED
 
 # Every entry point include/eqlin.h declares, with its ctypes signature.
 _vp, _i64, _int, _u32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_uint32
+_f32 = ctypes.c_float
+
+
+class AttentionDesc(ctypes.Structure):
+    """eqlin_attention_t."""
+    _fields_ = [("tokens", _i64), ("heads", _i64), ("kv_heads", _i64), ("head_dim", _i64),
+                ("q_stride", _i64), ("k_stride", _i64), ("v_stride", _i64), ("o_stride", _i64),
+                ("docs", _i64), ("offsets", _vp), ("max_len", _i64), ("pos", _vp), ("slopes", _vp),
+                ("axes", _int), ("scale", _f32), ("cap", _f32), ("err", _vp), ("wait_limit", _u32)]
+
+
 SIGNATURES = {
     "eqlin_create": ([_int, _i64, _i64, _int, ctypes.POINTER(_vp)], _int),
     "eqlin_create_group": ([_int, _int, _i64, _i64, _int, ctypes.POINTER(_vp)], _int),
@@ -52,6 +63,16 @@ SIGNATURES = {
     "eqlin_backward_dw_spectra": ([_vp, _vp, _vp, _vp, _vp, _i64, _vp], _int),
     "eqlin_backward": ([_vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp], _int),
     "eqlin_destroy": ([_vp], None),
+    "eqlin_norm_forward": ([_int, _i64, _int, _vp, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _i64, _vp], _int),
+    "eqlin_norm_workspace_bytes": ([_int, _i64, _i64], _i64),
+    "eqlin_norm_backward": ([_int, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp], _int),
+    "eqlin_rope_create": ([_int, _i64, _int, ctypes.POINTER(_i64), ctypes.POINTER(ctypes.c_double),
+                           ctypes.POINTER(_vp)], _int),
+    "eqlin_rope_destroy": ([_vp], None),
+    "eqlin_rope_apply": ([_vp, _int, _vp, _vp, _i64, _vp, _i64, _i64, _int, _i64, _vp], _int),
+    "eqlin_attention_forward": ([ctypes.POINTER(AttentionDesc), _int, _vp, _vp, _vp, _vp, _vp, _vp], _int),
+    "eqlin_attention_backward": ([ctypes.POINTER(AttentionDesc), _int, _vp, _i64, _vp, _vp, _vp, _vp, _vp, _vp, _i64,
+                                  _vp, _i64, _vp, _i64, _vp, _vp], _int),
 }
 
 _lib = None
@@ -307,6 +328,257 @@ def status_string(status: int) -> str:
 
 def destroy(h: Handle):
     h.close()
+
+
+# ------------------------------------------ norm, rotary positions, attention
+#
+# These calls belong to no handle.  They run on the tensors' device (all on one)
+# and, unless told otherwise, on its current stream.
+
+class _On:
+    """Make the tensors' device current for a call and find the stream."""
+
+    def __init__(self, t: torch.Tensor, stream):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError("expected a CUDA tensor")
+        self.device, self.stream = t.device, stream
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        self.prev = cur if cur != self.device.index else None
+        if self.prev is not None:
+            torch.cuda.set_device(self.device)
+        if self.stream is None:
+            return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
+        return _stream(self.stream)
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+        return False
+
+
+def _ptr(t, dtype, shape, name, device):
+    p = _dev_ptr(t, dtype, shape, name)
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    return p
+
+
+def _opt(t, dtype, shape, name, device):
+    return None if t is None else _ptr(t, dtype, shape, name, device)
+
+
+def _shape2(x, name):
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if x.dim() != 2:
+        raise ValueError(f"{name} must be [N, C'*T], got {tuple(x.shape)}")
+    if x.dtype not in _DT:
+        raise TypeError(f"{name} must be float32, float16 or bfloat16, got {x.dtype}")
+    return x.shape
+
+
+def norm_forward(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor, y: torch.Tensor, mean: torch.Tensor,
+                 rstd: torch.Tensor, T: int, eps: float = 1e-6, res: torch.Tensor | None = None,
+                 xsum: torch.Tensor | None = None, stream=None):
+    """Group layer norm of x (or of x + res, which xsum receives); see eqlin_norm_forward."""
+    N, F = _shape2(x, "x")
+    dt, dev, Cp = x.dtype, x.device, w.shape[0]
+    if Cp * T != F:
+        raise ValueError(f"x has {F} features, w {Cp} channels of {T}")
+    with _On(x, stream) as st:
+        _check(lib().eqlin_norm_forward(
+            T, Cp, _DT[dt], _ptr(x, dt, None, "x", dev), _opt(res, dt, (N, F), "res", dev),
+            _ptr(w, dt, (Cp,), "w", dev), _ptr(b, dt, (Cp,), "b", dev), eps, _opt(xsum, dt, (N, F), "xsum", dev),
+            _ptr(y, dt, (N, F), "y", dev), _ptr(mean, torch.float32, (N,), "mean", dev),
+            _ptr(rstd, torch.float32, (N,), "rstd", dev), N, st), "eqlin_norm_forward")
+
+
+def norm_workspace(T: int, Cp: int, N: int, device=None) -> torch.Tensor:
+    """A workspace for norm_backward on N rows."""
+    n = int(lib().eqlin_norm_workspace_bytes(int(T), int(Cp), int(N)))
+    if n < 0:
+        raise ValueError(f"no norm of {Cp} channels of {T} on {N} rows")
+    return torch.empty(n, dtype=torch.uint8, device=device or "cuda")
+
+
+def norm_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
+                  dx: torch.Tensor, dw: torch.Tensor, db: torch.Tensor, T: int, gsum: torch.Tensor | None = None,
+                  workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of the norm; x is what was normalised (x, or xsum); see eqlin_norm_backward."""
+    N, F = _shape2(gy, "gy")
+    dt, dev, Cp = gy.dtype, gy.device, w.shape[0]
+    if Cp * T != F:
+        raise ValueError(f"gy has {F} features, w {Cp} channels of {T}")
+    with _On(gy, stream) as st:
+        if workspace is None:
+            if stream is not None:
+                raise ValueError("pass a workspace along with a stream")
+            workspace = norm_workspace(T, Cp, N, dev)
+        need = lib().eqlin_norm_workspace_bytes(T, Cp, N)
+        if workspace.numel() * workspace.element_size() < need:
+            raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, needs {need}")
+        _check(lib().eqlin_norm_backward(
+            T, Cp, _DT[dt], _ptr(gy, dt, None, "gy", dev), _opt(gsum, dt, (N, F), "gsum", dev),
+            _ptr(x, dt, (N, F), "x", dev), _ptr(w, dt, (Cp,), "w", dev), _ptr(mean, torch.float32, (N,), "mean", dev),
+            _ptr(rstd, torch.float32, (N,), "rstd", dev), _ptr(dx, dt, (N, F), "dx", dev),
+            _ptr(dw, torch.float32, (Cp,), "dw", dev), _ptr(db, torch.float32, (Cp,), "db", dev),
+            _ptr(workspace, workspace.dtype, None, "workspace", dev), N, st), "eqlin_norm_backward")
+
+
+class Rope:
+    """A plan of rotary positions for heads of [Ch, T] features.
+
+    ``sections[a]`` channel pairs follow axis a of the positions; pair k of a
+    section of n turns by ``base ** (-k / n)`` radians per unit of position,
+    unless ``freqs`` gives one frequency for each pair of all sections."""
+
+    def __init__(self, T: int, Ch: int, sections, base: float = 100.0, freqs=None):
+        self.T, self.Ch, self.sections = int(T), int(Ch), tuple(int(n) for n in sections)
+        if not self.sections or min(self.sections) < 0:
+            raise ValueError("sections holds a number of channel pairs for each axis")
+        if freqs is None:
+            freqs = [float(base) ** (-k / n) for n in self.sections for k in range(n)]
+        self.freqs = tuple(float(f) for f in freqs)
+        if len(self.freqs) != sum(self.sections):
+            raise ValueError(f"{len(self.freqs)} frequencies for {sum(self.sections)} channel pairs")
+        out = ctypes.c_void_p()
+        self._r = None
+        _check(lib().eqlin_rope_create(self.T, self.Ch, self.axes, (_i64 * self.axes)(*self.sections),
+                                       (ctypes.c_double * max(1, len(self.freqs)))(*self.freqs), ctypes.byref(out)),
+               "eqlin_rope_create")
+        self._r = out
+
+    @property
+    def axes(self) -> int:
+        return len(self.sections)
+
+    @property
+    def ptr(self):
+        return self._r
+
+    def __del__(self):
+        try:
+            if self._r:
+                lib().eqlin_rope_destroy(self._r)
+                self._r = None
+        except Exception:
+            pass
+
+    def __copy__(self):
+        return self
+
+    def __deepcopy__(self, memo):
+        return self                # immutable, in host memory
+
+    def __reduce__(self):
+        return Rope, (self.T, self.Ch, self.sections, 1.0, self.freqs)
+
+
+def _heads(t, dtype, shape, name, device):
+    """A [N, heads, D] tensor whose heads lie one after the other: pointer and token stride."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    N, H, D = shape
+    s = t.stride()
+    if t.numel() and ((D > 1 and s[2] != 1) or (H > 1 and s[1] != D)):
+        raise ValueError(f"{name}: the heads of a token must lie one after the other")
+    # a single token has no next one: its stride says nothing
+    return ctypes.c_void_p(t.data_ptr()), (int(s[0]) if N > 1 else H * D)
+
+
+def rope(r: Rope, pos: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, inverse: bool = False, stream=None):
+    """Turn the heads src [N, heads, Ch*T] by their positions pos [N, axes] into
+    dst (which may be src); ``inverse`` turns back.  See eqlin_rope_apply."""
+    if not isinstance(src, torch.Tensor) or src.dim() != 3:
+        raise ValueError("src must be [N, heads, Ch*T]")
+    N, H, D = src.shape
+    if D != r.Ch * r.T:
+        raise ValueError(f"src has heads of {D} features, the plan {r.Ch} channels of {r.T}")
+    if src.dtype not in _DT:
+        raise TypeError(f"src must be float32, float16 or bfloat16, got {src.dtype}")
+    with _On(src, stream) as st:
+        ps, ss = _heads(src, src.dtype, (N, H, D), "src", src.device)
+        pd, ds = _heads(dst, src.dtype, (N, H, D), "dst", src.device)
+        _check(lib().eqlin_rope_apply(r.ptr, _DT[src.dtype], _ptr(pos, torch.float32, (N, r.axes), "pos", src.device),
+                                      ps, ss, pd, ds, H, 1 if inverse else 0, N, st), "eqlin_rope_apply")
+
+
+def _attention_desc(q, k, v, o, lse, docs, offsets, max_len, pos, slopes, scale, cap, err, wait_limit):
+    if not isinstance(q, torch.Tensor) or q.dim() != 3 or not isinstance(k, torch.Tensor) or k.dim() != 3:
+        raise ValueError("q, k and v must be [N, heads, D]")
+    if q.dtype not in _DT:
+        raise TypeError(f"q must be float32, float16 or bfloat16, got {q.dtype}")
+    N, H, D = q.shape
+    K = k.shape[1]
+    dev = q.device
+    if offsets is not None:
+        if offsets.dim() != 1 or offsets.numel() < 1:
+            raise ValueError("offsets must be [docs + 1]")
+        docs = offsets.numel() - 1
+    axes = 0
+    if (pos is None) != (slopes is None):
+        raise ValueError("pos and slopes go together")
+    if pos is not None:
+        if pos.dim() != 2 or pos.shape[1] < 1:
+            raise ValueError("pos must be [N, axes]")
+        axes = pos.shape[1]
+    ptrs, strides = zip(_heads(q, q.dtype, (N, H, D), "q", dev), _heads(k, q.dtype, (N, K, D), "k", dev),
+                        _heads(v, q.dtype, (N, K, D), "v", dev), _heads(o, q.dtype, (N, H, D), "o", dev))
+    desc = AttentionDesc(
+        tokens=N, heads=H, kv_heads=K, head_dim=D, q_stride=strides[0], k_stride=strides[1], v_stride=strides[2],
+        o_stride=strides[3], docs=int(docs), offsets=_opt(offsets, torch.int32, None, "offsets", dev),
+        max_len=int(max_len or 0), pos=_opt(pos, torch.float32, (N, axes), "pos", dev),
+        slopes=_opt(slopes, torch.float32, (H,), "slopes", dev), axes=axes,
+        scale=float(D ** -0.5 if scale is None else scale), cap=float(cap),
+        err=_opt(err, torch.int32, (4,), "err", dev), wait_limit=int(wait_limit))
+    return desc, ptrs, _ptr(lse, torch.float32, (H, N), "lse", dev)
+
+
+def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor, *,
+                      docs: int = 1, offsets: torch.Tensor | None = None, max_len: int | None = None,
+                      pos: torch.Tensor | None = None, slopes: torch.Tensor | None = None, scale: float | None = None,
+                      cap: float = 0.0, err: torch.Tensor | None = None, wait_limit: int = 0, stream=None):
+    """Attention within documents: q, o [N, heads, D], k, v [N, kv_heads, D],
+    lse [heads, N] float32.  ``docs`` documents of equal length, or ``offsets``
+    (int32 [docs + 1]) for packed ones; see eqlin_attention_forward."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a CUDA tensor")
+    with _On(q, stream) as st:
+        desc, (pq, pk, pv, po), pl = _attention_desc(q, k, v, o, lse, docs, offsets, max_len, pos, slopes, scale, cap,
+                                                     err, wait_limit)
+        _check(lib().eqlin_attention_forward(ctypes.byref(desc), _DT[q.dtype], pq, pk, pv, po, pl, st),
+               "eqlin_attention_forward")
+
+
+def attention_backward(go: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor,
+                       lse: torch.Tensor, dq: torch.Tensor, dk: torch.Tensor, dv: torch.Tensor, delta: torch.Tensor,
+                       *, docs: int = 1, offsets: torch.Tensor | None = None, max_len: int | None = None,
+                       pos: torch.Tensor | None = None, slopes: torch.Tensor | None = None,
+                       scale: float | None = None, cap: float = 0.0, err: torch.Tensor | None = None,
+                       wait_limit: int = 0, stream=None):
+    """Gradients of attention_forward into dq, dk and dv; delta [heads, N]
+    float32 is a workspace.  See eqlin_attention_backward."""
+    if not isinstance(q, torch.Tensor):
+        raise TypeError("q must be a CUDA tensor")
+    with _On(q, stream) as st:
+        desc, (pq, pk, pv, po), pl = _attention_desc(q, k, v, o, lse, docs, offsets, max_len, pos, slopes, scale, cap,
+                                                     err, wait_limit)
+        dev, dt = q.device, q.dtype
+        pg, sg = _heads(go, dt, q.shape, "go", dev)
+        pdq, sdq = _heads(dq, dt, q.shape, "dq", dev)
+        pdk, sdk = _heads(dk, dt, k.shape, "dk", dev)
+        pdv, sdv = _heads(dv, dt, k.shape, "dv", dev)
+        _check(lib().eqlin_attention_backward(
+            ctypes.byref(desc), _DT[dt], pg, sg, pq, pk, pv, po, pl, pdq, sdq, pdk, sdk, pdv, sdv,
+            _ptr(delta, torch.float32, (q.shape[1], q.shape[0]), "delta", dev), st), "eqlin_attention_backward")
 
 
 # ------------------------------------------------------- allocating helpers

@@ -267,6 +267,132 @@ EQLIN_API eqlin_status_t eqlin_backward_dw_noalloc(int T, int64_t Cp, int64_t Dp
                                                    int64_t N, void *stream);
 
 /*
+ * What stands between the layers of an equivariant transformer block
+ * ------------------------------------------------------------------
+ * The paper times its layer inside EQ-ViT and EQ-Swin blocks (technical
+ * summary, section "Resultados Experimentais", network level).  The calls
+ * below are those blocks' other operators: the norm, rotary positions and
+ * attention.  They belong to no handle: they take the shapes directly, run on
+ * the CURRENT device, allocate no device memory and keep nothing between
+ * calls, so calls on different streams may overlap as long as their buffers
+ * differ.  Features are [C', T] per token, index c*T + t, as above.
+ */
+
+/*
+ * Group layer norm: statistics over all F = C'*T features, affine parameters
+ * w, b [C'] shared along the group axis (so it commutes with a cyclic shift).
+ *
+ *   s = x + res,   mean = mean_f s,   rstd = (mean_f (s - mean)^2 + eps)^-1/2
+ *   y[n, c*T+t] = (s[n, c*T+t] - mean[n]) * rstd[n] * w[c] + b[c]
+ *
+ * x, res, sum, y [N, F] and w, b [C'] of the dtype, mean and rstd [N] float32.
+ * res and sum are both NULL (s = x) or both given: sum receives s rounded to
+ * the dtype (the residual stream), while y follows from the unrounded s.  sum
+ * may be x or res; y may be x when res is NULL.  1 <= T <= 16 (any order,
+ * dihedral ones included), F <= 8192, rows of a multiple of 16 bytes.
+ */
+EQLIN_API eqlin_status_t eqlin_norm_forward(int T, int64_t Cp, eqlin_dtype_t dtype, const void *x,
+                                            const void *res, const void *w, const void *b, float eps,
+                                            void *sum, void *y, float *mean, float *rstd, int64_t N,
+                                            void *stream);
+
+/* Bytes of the workspace that eqlin_norm_backward needs (-1 on bad arguments). */
+EQLIN_API int64_t eqlin_norm_workspace_bytes(int T, int64_t Cp, int64_t N);
+
+/*
+ * Its gradient: with x the normalised rows (x, or sum), xh = (x - mean) rstd
+ * and g = gy w,
+ *   dx = rstd (g - mean_f g - xh mean_f(g xh)) + gsum     (the gradient of x and of res)
+ *   dw[c] = sum_n sum_t gy xh,    db[c] = sum_n sum_t gy
+ * gsum [N, F], the gradient of sum, may be NULL.  dx may be gy or gsum.  dw
+ * and db [C'] are float32 and overwritten; sums run in a fixed order, without
+ * atomics.  workspace: eqlin_norm_workspace_bytes, 16-byte aligned; calls that
+ * may overlap on the GPU need one each.
+ */
+EQLIN_API eqlin_status_t eqlin_norm_backward(int T, int64_t Cp, eqlin_dtype_t dtype, const void *gy,
+                                             const void *gsum, const void *x, const void *w,
+                                             const float *mean, const float *rstd, void *dx, float *dw,
+                                             float *db, void *workspace, int64_t N, void *stream);
+
+typedef struct eqlin_rope *eqlin_rope_t;
+
+/*
+ * A plan of rotary positions for heads of [Ch, T] features (Ch even, at most
+ * 256; 1 <= T <= 16): channel i < Ch/2 pairs with channel i + Ch/2 at every
+ * group position and is turned by pos[axis_i] * freqs[i] radians.  The first
+ * sections[0] pairs follow axis 0, the next sections[1] axis 1, and so on
+ * (axes <= 4; time, height, width of a video, say); pairs past the last
+ * section are copied.  The plan lives in host memory, belongs to no device
+ * and may be used from several threads.
+ */
+EQLIN_API eqlin_status_t eqlin_rope_create(int T, int64_t Ch, int axes, const int64_t *sections,
+                                           const double *freqs, eqlin_rope_t *out);
+EQLIN_API void eqlin_rope_destroy(eqlin_rope_t r);
+
+/*
+ * Turn `heads` heads of each of N tokens: src and dst hold token n's heads one
+ * after the other from element n * stride (stride >= heads * Ch * T, in
+ * elements), pos [N, axes] is float32.  inverse != 0 turns back, which is also
+ * the gradient.  dst may be src (with the same stride); other overlaps are not
+ * allowed.  The angle is exact to about 1e-7 turns for far positions, too.
+ */
+EQLIN_API eqlin_status_t eqlin_rope_apply(eqlin_rope_t r, eqlin_dtype_t dtype, const float *pos,
+                                          const void *src, int64_t src_stride, void *dst,
+                                          int64_t dst_stride, int64_t heads, int inverse, int64_t N,
+                                          void *stream);
+
+/*
+ * Attention within documents.  Tokens lie in one packed sequence; a document
+ * (an image, a window, a clip) is a contiguous range of it, and a token
+ * attends to all tokens of its document.  Head h of q reads key head
+ * h / (heads / kv_heads).
+ *
+ *   u = scale * q_i . k_j
+ *   s = (cap > 0 ? cap * tanh(u / cap) : u) - slopes[h] * sum_a |pos[i, a] - pos[j, a]|
+ *   lse_i = log sum_j exp(s_ij),    o_i = sum_j exp(s_ij - lse_i) v_j
+ *
+ * The distance is the city-block one, which a quarter turn of an image leaves
+ * as it is.  Layouts: token n's heads lie one after the other from element
+ * n * stride, so q, k and v may be parts of one packed projection; strides and
+ * head_dim are multiples of 16 bytes, head_dim <= 128.  lse is [heads, tokens]
+ * float32.  Rows outside every document get o = 0, lse = 0 and zero gradients;
+ * what the inputs hold there is not looked at.
+ */
+typedef struct {
+    int64_t tokens, heads, kv_heads, head_dim;
+    int64_t q_stride, k_stride, v_stride, o_stride;   /* elements per token */
+    int64_t docs;             /* documents; without offsets they have tokens / docs tokens each */
+    const int32_t *offsets;   /* device, [docs + 1], ascending, 0 <= offsets <= tokens; or NULL */
+    int64_t max_len;          /* length of the longest document if known, else 0: it spreads the
+                                 work, and every value gives the same results */
+    const float *pos;         /* device, [tokens, axes], or NULL with axes = 0 */
+    const float *slopes;      /* device, [heads] */
+    int axes;                 /* 0 (no bias) to 3 */
+    float scale, cap;         /* cap = 0: scores are not capped */
+    int32_t *err;             /* device, 4 words as in eqlin_error_detail, zeroed by the caller: a
+                                 wait that ran out is recorded here (outputs are then undefined);
+                                 or NULL */
+    uint32_t wait_limit;      /* as in eqlin_set_wait_limit; 0 for the default */
+} eqlin_attention_t;
+
+EQLIN_API eqlin_status_t eqlin_attention_forward(const eqlin_attention_t *a, eqlin_dtype_t dtype,
+                                                 const void *q, const void *k, const void *v, void *o,
+                                                 float *lse, void *stream);
+
+/*
+ * Gradients of q, k and v from go, the gradient of o, and the forward's o and
+ * lse.  delta [heads, tokens] float32 is a workspace (calls that may overlap
+ * on the GPU need one each).  Two kernels, one over query rows and one over
+ * key rows: no atomics, so results do not vary from run to run.
+ */
+EQLIN_API eqlin_status_t eqlin_attention_backward(const eqlin_attention_t *a, eqlin_dtype_t dtype,
+                                                  const void *go, int64_t go_stride, const void *q,
+                                                  const void *k, const void *v, const void *o,
+                                                  const float *lse, void *dq, int64_t dq_stride,
+                                                  void *dk, int64_t dk_stride, void *dv,
+                                                  int64_t dv_stride, float *delta, void *stream);
+
+/*
  * Read and clear the handle's device-side error word.  Call after
  * synchronising the streams the handle's kernels ran on.  Returns EQLIN_OK,
  * EQLIN_ERR_TIMEOUT (a kernel's bounded wait ran out and the kernel returned

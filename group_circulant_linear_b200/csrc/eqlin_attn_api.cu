@@ -15,7 +15,7 @@ eqlin_status_t describe(const eqlin_attention_t* a, eqlin_dtype_t dtype, attn::P
   if (a->tokens < 0 || a->docs < 0 || a->max_len < 0 || a->heads < 1 || a->kv_heads < 1 || a->head_dim < 1)
     return EQLIN_ERR_INVALID_ARG;
   if (a->heads % a->kv_heads) return EQLIN_ERR_INVALID_ARG;
-  if (!isfinite(a->scale) || !isfinite(a->cap) || a->cap < 0.f) return EQLIN_ERR_INVALID_ARG;
+  if (!isfinite(a->scale) || !(a->scale > 0.f) || !isfinite(a->cap) || a->cap < 0.f) return EQLIN_ERR_INVALID_ARG;
   if (a->axes < 0 || (a->axes > 0 && !a->slopes)) return EQLIN_ERR_INVALID_ARG;
   if (a->axes > attn::kMaxAxes) return EQLIN_ERR_UNSUPPORTED;
   if (a->heads > 65536 || a->head_dim > attn::kMaxHeadDim || a->tokens > 0x7fffffff) return EQLIN_ERR_UNSUPPORTED;
@@ -80,7 +80,8 @@ extern "C" eqlin_status_t eqlin_attention_forward(const eqlin_attention_t* a, eq
   p.ks = a->k_stride;
   p.vs = a->v_stride;
   p.os = a->o_stride;
-  return done(launch_attn_simt_forward(p, dtype, static_cast<cudaStream_t>(stream)));
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  return done(dtype == EQLIN_F32 ? launch_attn_simt_forward(p, dtype, cs) : launch_attn_tc_forward(p, dtype, cs));
 }
 
 extern "C" eqlin_status_t eqlin_attention_backward(const eqlin_attention_t* a, eqlin_dtype_t dtype, const void* go,

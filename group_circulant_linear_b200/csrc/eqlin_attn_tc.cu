@@ -1,0 +1,361 @@
+// eqlin_attn_tc.cu -- document attention, forward, on the tensor cores.
+//
+// Per own tile of 128 queries, one pass over the document's keys in tiles of
+// up to 128 (trimmed to 16): S = Q K^T into TMEM, a thread per row reads its
+// scores, keeps the running maximum m and sum l in FP32, and writes
+// P = 2^(s - m) back as 16-bit pairs, which the tensor core takes from TMEM
+// for O += P V.  P's rounding to 16 bits is the operand type's own (half a
+// step of the inputs'); l sums the unrounded values.
+//
+// The output is rescaled only when a row's maximum grows by more than 2^8
+// (kLag): until then P is at most 256, far inside both types, and O and l
+// share the older m, so the quotient is the same.
+//
+// TMEM: 256 columns, so that two blocks share an SM and one's softmax runs
+// under the other's products: S [0, 128), then up to 64 features P [128, 192)
+// and O [192, 256) -- the next S is issued while P is still read -- and above
+// that P over S and O [128, 256).
+#include "eqlin_attn_tc.cuh"
+
+namespace eqlin {
+namespace attn_tc {
+
+constexpr float kLag = 8.f;
+
+template <int DP> struct FwdCfg {
+  static constexpr bool OVER = DP > 64;                       // P lies over S
+  static constexpr int TILE = DP / 64 * PANEL;
+  static constexpr int SLOTS = DP > 64 ? 2 : 4;               // K and V tiles in turn
+  static constexpr int NBAR = 2 + 2 * SLOTS + 5;
+  static constexpr int TMEM = 256;
+  static constexpr int P_COL = OVER ? 0 : 128, O_COL = OVER ? 128 : 192;
+  static constexpr int POS = (SLOTS / 2) * kMaxAxes * ROWS * 4;
+  static constexpr int SMEM = (1 + SLOTS) * TILE + POS + NBAR * 8 + 64 + 1024;
+};
+
+template <int DP, typename E, int AXES, bool CAP>
+__global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_constant__ Params p) {
+  using C = FwdCfg<DP>;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* ring = smem + C::TILE;
+  float* spos = reinterpret_cast<float*>(ring + C::SLOTS * C::TILE);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(spos) + C::POS);
+  uint64_t* q_full = bars;
+  uint64_t* q_empty = bars + 1;
+  uint64_t* kv_full = bars + 2;
+  uint64_t* kv_empty = kv_full + C::SLOTS;
+  uint64_t* s_full = kv_empty + C::SLOTS;
+  uint64_t* s_free = s_full + 1;
+  uint64_t* p_full = s_free + 1;
+  uint64_t* o_full = p_full + 1;
+  uint64_t* drain = o_full + 1;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
+  int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
+  int* local_err = abort_word + 1;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  grid_dep_wait();
+  const Work w = work_of(p, p.H);
+  const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)(w.head / (p.H / p.K)) * p.D;
+  if (w.doc == p.docs) {
+    outside_rows(p, w.tile, [&](int64_t r) {
+      for (int d = threadIdx.x; d < p.D; d += kThreads) static_cast<E*>(p.o)[r * p.os + qh + d] = Elem<E>::from_f(0.f);
+      if (threadIdx.x == 0) p.lse[(int64_t)w.head * p.N + r] = 0.f;
+    });
+    return;
+  }
+  int64_t lo, hi;
+  doc_range(p, w.doc, lo, hi);
+  if (lo + (int64_t)w.tile * ROWS >= hi) return;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 32);
+    mbar_init(q_empty, 1);
+    for (int i = 0; i < C::SLOTS; ++i) {
+      mbar_init(kv_full + i, 32);
+      mbar_init(kv_empty + i, 1);
+    }
+    mbar_init(s_full, 1);
+    mbar_init(s_free, 128);
+    mbar_init(p_full, 128);
+    mbar_init(o_full, 1);
+    mbar_init(drain, 1);
+    *abort_word = 0;
+    for (int i = 0; i < 4; ++i) local_err[i] = 0;
+    fence_barrier_init();
+  }
+  if (warp == MMA_WARP) {
+    tmem_alloc(tmem_slot, C::TMEM);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  // after the allocation: a dependent kernel's block that takes TMEM columns
+  // early must not be able to starve one of these
+  grid_dep_launch();
+  volatile int* abort_flag = abort_word;
+  int* err = p.err ? p.err : local_err;
+  const uint32_t limit = p.wait_limit;
+  const int d16 = (p.D + 15) / 16;                            // 16-feature steps
+
+  if (warp == LOAD_WARP) {
+    Pending pend;
+    uint32_t item = 0, tile_no = 0;
+    bool ok = true;
+    for (int64_t r0 = lo + (int64_t)w.tile * ROWS; ok && r0 < hi; r0 += (int64_t)p.hint * ROWS, ++tile_no) {
+      ok = claim(pend, q_empty, (tile_no & 1) ^ 1, limit, abort_flag, lane, err, site(K_ATTN_FWD, 2, 0), tile_no);
+      if (!ok) break;
+      load_rows<DP, E>(smem_u32(smem), p.q, p.qs, qh, r0, hi, ROWS, p.D, 2 * d16, lane);
+      cp_async_commit();
+      announce_later(pend, q_full);
+      for (int64_t c0 = lo; ok && c0 < hi; c0 += ROWS) {
+        const int nc = (int)(hi - c0 < ROWS ? hi - c0 : ROWS), rows = (nc + 15) & ~15;
+#pragma unroll 1
+        for (int kv = 0; kv < 2; ++kv, ++item) {
+          const int slot = item % C::SLOTS;
+          const uint32_t ph = (item / C::SLOTS) & 1;
+          ok = claim(pend, kv_empty + slot, ph ^ 1, limit, abort_flag, lane, err, site(K_ATTN_FWD, 2, 1), item);
+          if (!ok) break;
+          load_rows<DP, E>(smem_u32(ring + slot * C::TILE), kv ? p.v : p.k, kv ? p.vs : p.ks, kh, c0, hi, rows, p.D,
+                           2 * d16, lane);
+          // positions go with V: its slot is free once the softmax has used them
+          if (AXES && kv) load_positions(spos + (slot >> 1) * kMaxAxes * ROWS, p, c0, hi, (nc + 31) & ~31, lane);
+          cp_async_commit();
+          announce_later(pend, kv_full + slot);
+        }
+      }
+    }
+    announce_all(pend);
+    if (!ok && lane == 0) raise_abort(abort_flag, err);
+  } else if (warp == MMA_WARP) {
+    if (lane == 0) {
+      uint32_t item = 0, tile_no = 0, step = 0;               // step: key tiles since the start
+      bool ok = true;
+      const uint32_t q_addr = smem_u32(smem);
+      const uint32_t id_o = idesc_f16(Pair<E>::fmt, (uint32_t)(16 * d16)) | kBTransposed;
+      auto qk = [&](int64_t c0, uint32_t it, uint32_t n) -> bool {   // scores of key tile n, whose K is item `it`
+        const int slot = it % C::SLOTS;
+        if (!bwait(kv_full + slot, (it / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 1), it)) return false;
+        // S is free once every thread has read the previous scores (P over S: once P, and with it PV, is issued)
+        if (!C::OVER && !bwait(s_free, (n & 1) ^ 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 2), n)) return false;
+        tc_fence_after();
+        const int nc = (int)(hi - c0 < ROWS ? hi - c0 : ROWS);
+        const uint32_t id = idesc_f16(Pair<E>::fmt, (uint32_t)((nc + 15) & ~15));
+        const uint32_t k_addr = smem_u32(ring + slot * C::TILE);
+        for (int d = 0; d < d16; ++d) {
+          const uint32_t off = (d >> 2) * PANEL + (d & 3) * 32;
+          mma_f16_ss(tmem, smem_desc(q_addr + off, 128), smem_desc(k_addr + off, 128), id, d > 0);
+        }
+        mma_commit(s_full);
+        mma_commit(kv_empty + slot);
+        return true;
+      };
+      for (int64_t r0 = lo + (int64_t)w.tile * ROWS; ok && r0 < hi; r0 += (int64_t)p.hint * ROWS, ++tile_no) {
+        ok = bwait(q_full, tile_no & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 0), tile_no) && qk(lo, item, step);
+        for (int64_t c0 = lo; ok && c0 < hi; c0 += ROWS, item += 2, ++step) {
+          const bool more = c0 + ROWS < hi;
+          if (!C::OVER && more) ok = qk(c0 + ROWS, item + 2, step + 1);
+          if (!C::OVER && !more) mma_commit(q_empty);
+          const uint32_t vi = item + 1;
+          const int slot = vi % C::SLOTS;
+          ok = ok && bwait(kv_full + slot, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 1), vi) &&
+               bwait(p_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 3), step);
+          if (!ok) break;
+          tc_fence_after();
+          const int nc = (int)(hi - c0 < ROWS ? hi - c0 : ROWS), steps = (nc + 15) / 16;
+          const uint32_t v_addr = smem_u32(ring + slot * C::TILE);
+          for (int s = 0; s < steps; ++s)
+            mma_f16_ts(tmem + C::O_COL, tmem + C::P_COL + s * 8, smem_desc_mn(v_addr + s * 2048, PANEL, 1024), id_o,
+                       c0 > lo || s > 0);
+          mma_commit(o_full);
+          mma_commit(kv_empty + slot);
+          if (C::OVER && more) ok = qk(c0 + ROWS, item + 2, step + 1);
+          if (C::OVER && !more) mma_commit(q_empty);
+        }
+      }
+      if (!ok) raise_abort(abort_flag, err);
+      mma_commit(drain);
+      mbar_wait(drain, 0, kDefaultWaitLimit);
+    }
+    __syncwarp();
+  } else {
+    const uint32_t my = tmem + ((uint32_t)(warp * 32) << 16);
+    const Score sc = score_of(p, w.head);
+    uint32_t step = 0;
+    bool ok = true;
+    for (int64_t r0 = lo + (int64_t)w.tile * ROWS; ok && r0 < hi; r0 += (int64_t)p.hint * ROWS) {
+      const int64_t row = r0 + warp * 32 + lane;
+      const bool any = r0 + warp * 32 < hi;                   // does the warp have a row at all
+      float own[AXES ? AXES : 1];
+#pragma unroll
+      for (int a = 0; a < AXES; ++a) own[a] = row < hi ? p.pos[row * AXES + a] : 0.f;
+      float m = -INFINITY, l = 0.f;
+      for (int64_t c0 = lo; c0 < hi; c0 += ROWS, ++step) {
+        const int nc = (int)(hi - c0 < ROWS ? hi - c0 : ROWS);
+        ok = wwait(s_full, step & 1, limit, abort_flag, lane, err, site(K_ATTN_FWD, 0, 0), step);
+        if (AXES && ok) {
+          const uint32_t vi = 2 * step + 1;
+          ok = wwait_all(kv_full + vi % C::SLOTS, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 1), step);
+        }
+        if (!ok) break;
+        tc_fence_after();
+        uint32_t raw[ROWS];
+        float* s = reinterpret_cast<float*>(raw);
+        if (any) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+            if (c * 32 < nc) tmem_ld32(my + c * 32, raw + c * 32);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tie32(raw + c * 32);
+        }
+        if (!C::OVER) {
+          tc_fence_before();
+          mbar_arrive(s_free);
+        }
+        float top = -INFINITY;
+        if (any) {
+          const float* pos = spos + (((2 * step + 1) % C::SLOTS) >> 1) * kMaxAxes * ROWS;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c * 32 >= nc) continue;
+            if (CAP || AXES) {
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float d[4] = {0.f, 0.f, 0.f, 0.f};
+                if (AXES) distances<AXES>(pos, c * 32 + i, own, d);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                  float& v = s[c * 32 + i + k];
+                  v = CAP ? sc.cap2 * tanh_raw(v, sc) : v * sc.scale2;
+                  if (AXES) v = fmaf(-sc.slope2, d[k], v);
+                }
+              }
+            }
+            if (c * 32 + 32 > nc) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (c * 32 + i >= nc) s[c * 32 + i] = -INFINITY;
+            }
+            float t0 = s[c * 32], t1 = s[c * 32 + 1];
+#pragma unroll
+            for (int i = 2; i < 32; i += 2) {
+              t0 = fmaxf(t0, s[c * 32 + i]);
+              t1 = fmaxf(t1, s[c * 32 + i + 1]);
+            }
+            top = fmaxf(top, fmaxf(t0, t1));
+          }
+          if (!(CAP || AXES)) top *= sc.scale2;               // scale > 0
+        }
+        // P's columns, and O, are free once the previous product is done
+        if (c0 > lo) {
+          ok = wwait(o_full, (step - 1) & 1, limit, abort_flag, lane, err, site(K_ATTN_FWD, 0, 2), step);
+          if (!ok) break;
+          tc_fence_after();
+          const bool grow = top > m + kLag;
+          if (__any_sync(0xffffffffu, grow)) {
+            const float fix = grow ? ex2(m - top) : 1.f;
+            l *= fix;
+            if (grow) m = top;
+#pragma unroll
+            for (int c = 0; c < DP / 16; ++c) {
+              if (c >= d16) continue;
+              uint32_t o[16];
+              tmem_ld_32x32b_x16(my + C::O_COL + c * 16, o);
+              tmem_wait_ld();
+              tie16(o);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+              tmem_st_32x32b_x16(my + C::O_COL + c * 16, o);
+            }
+            tmem_wait_st();
+          }
+        } else {
+          m = top;
+        }
+        if (any) {
+          const float k2 = (CAP || AXES) ? 1.f : sc.scale2;
+          float l0 = 0.f, l1 = 0.f;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            if (c * 32 >= nc) continue;
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              const float a = ex2(fmaf(s[c * 32 + i], k2, -m)), b = ex2(fmaf(s[c * 32 + i + 1], k2, -m));
+              l0 += a;
+              l1 += b;
+              pk[i / 2] = Pair<E>::pack(a, b);
+            }
+            tmem_st_32x32b_x16(my + C::P_COL + c * 16, pk);
+          }
+          l += l0 + l1;
+          tmem_wait_st();
+        }
+        tc_fence_before();
+        mbar_arrive(p_full);
+      }
+      if (!ok) break;
+      ok = wwait(o_full, (step - 1) & 1, limit, abort_flag, lane, err, site(K_ATTN_FWD, 0, 3), step);
+      if (!ok) break;
+      tc_fence_after();
+      if (any) {
+        const float inv = 1.f / l;
+        E* out = static_cast<E*>(p.o) + row * p.os + qh;
+#pragma unroll
+        for (int c = 0; c < DP / 16; ++c) {
+          if (c >= d16) continue;
+          uint32_t o[16];
+          tmem_ld_32x32b_x16(my + C::O_COL + c * 16, o);
+          tmem_wait_ld();
+          tie16(o);
+          uint32_t pk[8];
+#pragma unroll
+          for (int i = 0; i < 16; i += 2)
+            pk[i / 2] = Pair<E>::pack(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+          if (row < hi) {
+            *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+            if (c * 16 + 8 < p.D) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          }
+        }
+        if (row < hi) p.lse[(int64_t)w.head * p.N + row] = (m + log2f(l)) * kLn2;
+      }
+      tc_fence_before();
+    }
+    if (!ok && lane == 0) raise_abort(abort_flag, err);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == MMA_WARP) tmem_dealloc(tmem, C::TMEM);
+}
+
+template <int DP, typename E, bool CAP>
+cudaError_t forward_axes(const Params& p, cudaStream_t st) {
+  constexpr int smem = FwdCfg<DP>::SMEM;
+  switch (p.axes) {
+    case 0: return launch_rows(attn_tc_fwd_kernel<DP, E, 0, CAP>, smem, p, p.H, st);
+    case 1: return launch_rows(attn_tc_fwd_kernel<DP, E, 1, CAP>, smem, p, p.H, st);
+    case 2: return launch_rows(attn_tc_fwd_kernel<DP, E, 2, CAP>, smem, p, p.H, st);
+    default: return launch_rows(attn_tc_fwd_kernel<DP, E, 3, CAP>, smem, p, p.H, st);
+  }
+}
+template <int DP, typename E>
+cudaError_t forward_cap(const Params& p, cudaStream_t st) {
+  return p.cap > 0.f ? forward_axes<DP, E, true>(p, st) : forward_axes<DP, E, false>(p, st);
+}
+template <typename E>
+cudaError_t forward_dim(const Params& p, cudaStream_t st) {
+  return p.D <= 64 ? forward_cap<64, E>(p, st) : forward_cap<128, E>(p, st);
+}
+
+}  // namespace attn_tc
+
+cudaError_t launch_attn_tc_forward(const attn::Params& p, eqlin_dtype_t dt, cudaStream_t st) {
+  return dt == EQLIN_F16 ? attn_tc::forward_dim<__half>(p, st) : attn_tc::forward_dim<__nv_bfloat16>(p, st);
+}
+
+}  // namespace eqlin

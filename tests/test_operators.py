@@ -570,7 +570,7 @@ def test_attention_refusals():
     assert L.eqlin_attention_forward(None, 2, one, one, one, one, one, None) == -1
     assert call(dt=7) == -1 and call(tokens=-1) == -1 and call(heads=0) == -1 and call(kv_heads=3) == -1
     assert call(docs=0) == -1 and call(docs=4) == -1 and call(docs=-1) == -1 and call(max_len=-1) == -1
-    assert call(scale=math.nan) == -1 and call(cap=-1.0) == -1 and call(cap=math.inf) == -1
+    assert call(scale=math.nan) == -1 and call(scale=0.0) == -1 and call(scale=-1.0) == -1 and call(cap=-1.0) == -1 and call(cap=math.inf) == -1
     assert call(axes=1) == -1 and call(axes=1, slopes=4096) == -1 and call(axes=4, slopes=4096, pos=4096) == -2
     assert call(head_dim=136, q_stride=1024, k_stride=1024, v_stride=1024, o_stride=1024) == -2
     assert call(head_dim=12) == -3 and call(head_dim=0) == -1

@@ -16,8 +16,8 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libeqlin.so")
 SOURCES = ["eqlin_api.cu", "eqlin_simt.cu", "eqlin_tc.cu", "eqlin_tc32.cu", "eqlin_tc32_dw.cu", "eqlin_tc_dw.cu", "eqlin_tc_dws.cu",
            "eqlin_dihedral.cu", "eqlin_noalloc.cu", "eqlin_norm.cu", "eqlin_rope.cu", "eqlin_attn_api.cu",
-           "eqlin_attn_simt.cu", "eqlin_attn_tc.cu"]
-HEADERS = ["eqlin_attn.cuh", "eqlin_attn_tc.cuh", "eqlin_internal.cuh", "eqlin_ptx.cuh", "eqlin_packed.cuh", "eqlin_wait.cuh"]
+           "eqlin_attn_simt.cu", "eqlin_attn_tc.cu", "eqlin_attn_tc_dq.cu", "eqlin_attn_tc_dkv.cu"]
+HEADERS = ["eqlin_attn.cuh", "eqlin_attn_tc.cuh", "eqlin_attn_tc_bwd.cuh", "eqlin_internal.cuh", "eqlin_ptx.cuh", "eqlin_packed.cuh", "eqlin_wait.cuh"]
 INCLUDE = os.path.join(os.path.dirname(HERE), "include")
 
 NVCC_FLAGS = [

@@ -98,5 +98,8 @@ cudaError_t launch_attn_simt_backward(const attn::Params& p, eqlin_dtype_t dt, c
 
 // f16 and bf16: tcgen05.
 cudaError_t launch_attn_tc_forward(const attn::Params& p, eqlin_dtype_t dt, cudaStream_t st);
+// dq and delta first, then dk and dv, which read delta.
+cudaError_t launch_attn_tc_dq(const attn::Params& p, eqlin_dtype_t dt, cudaStream_t st);
+cudaError_t launch_attn_tc_dkv(const attn::Params& p, eqlin_dtype_t dt, cudaStream_t st);
 
 }  // namespace eqlin

@@ -121,5 +121,8 @@ extern "C" eqlin_status_t eqlin_attention_backward(const eqlin_attention_t* a, e
   p.dqs = dq_stride;
   p.dks = dk_stride;
   p.dvs = dv_stride;
-  return done(launch_attn_simt_backward(p, dtype, static_cast<cudaStream_t>(stream)));
+  cudaStream_t cs = static_cast<cudaStream_t>(stream);
+  if (dtype == EQLIN_F32) return done(launch_attn_simt_backward(p, dtype, cs));
+  const cudaError_t e = launch_attn_tc_dq(p, dtype, cs);
+  return done(e != cudaSuccess ? e : launch_attn_tc_dkv(p, dtype, cs));
 }

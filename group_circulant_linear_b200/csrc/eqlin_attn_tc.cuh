@@ -103,23 +103,23 @@ template <int N> __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One warp copies `rows` rows (<= 128) from token r0 on of one head into the
+// One warp copies `rows` rows (<= TILE_ROWS) from token r0 on of one head into the
 // panels at dst; rows at or past `hi`, and features at or past D, read as zero.
 // chunks: 16-byte chunks of a row that any product reads (ceil(D / 16) * 2).
-template <int DP, typename E>
+template <int DP, typename E, int TILE_ROWS = ROWS>
 __device__ __forceinline__ void load_rows(uint32_t dst, const void* src, int64_t stride, int64_t head_off, int64_t r0,
                                           int64_t hi, int rows, int D, int chunks, int lane) {
   const int sub = lane >> 3, ch0 = lane & 7;
   const char* base = reinterpret_cast<const char*>(static_cast<const E*>(src) + head_off);
   const int64_t step = stride * (int64_t)sizeof(E);
-  const int left = (int)(hi - r0 < ROWS ? hi - r0 : ROWS);
+  const int left = (int)(hi - r0 < TILE_ROWS ? hi - r0 : TILE_ROWS);
 #pragma unroll
   for (int pn = 0; pn < DP / 64; ++pn) {
     const int ch = pn * 8 + ch0;
     if (ch >= chunks) continue;
     const bool live_ch = ch * 8 < D;
     const char* from = base + (r0 + sub) * step + ch * 16;
-    const uint32_t to = dst + pn * PANEL;
+    const uint32_t to = dst + pn * TILE_ROWS * 128;
 #pragma unroll 4
     for (int r = sub; r < rows; r += 4, from += 4 * step) {
       const bool on = live_ch && r < left;
@@ -218,7 +218,8 @@ __device__ __forceinline__ void distances(const float* pos, int c0, const float*
   }
 }
 
-inline cudaError_t launch_rows(void (*k)(Params), int smem, Params p, int heads, cudaStream_t st) {
+inline cudaError_t launch_rows(void (*k)(Params), int smem, Params p, int heads, cudaStream_t st,
+                               int threads = kThreads) {
   int64_t tiles = (p.len + ROWS - 1) / ROWS;
   if (tiles < 1) tiles = 1;
   const int64_t items = (p.docs + (p.offsets ? 1 : 0)) * heads;
@@ -227,7 +228,7 @@ inline cudaError_t launch_rows(void (*k)(Params), int smem, Params p, int heads,
   const int64_t room = 0x7fffffff / items;
   p.hint = (int)(tiles < room ? tiles : room);
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(k), smem);
-  if (e == cudaSuccess) e = launch_pdl(k, dim3((unsigned)(items * p.hint)), dim3(kThreads), (size_t)smem, st, p);
+  if (e == cudaSuccess) e = launch_pdl(k, dim3((unsigned)(items * p.hint)), dim3(threads), (size_t)smem, st, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

@@ -11,6 +11,10 @@
 //   ds = rstd (g - mean_f g - xh mean_f(g xh)) + gs       (gs: gradient of s itself, optional)
 //   dw[c] = sum_n sum_t gy xh,    db[c] = sum_n sum_t gy
 //
+// The backward forms s = x + r again from both, unrounded: reading the stored
+// sum instead would save one of its six tensors but put the sum's rounding
+// (half a step of the type, relative) into xh, and with it into dw.
+//
 // All sums are FP32; the variance is taken about the mean in a second pass
 // over registers, not as E[s^2] - mu^2, which cancels when |mu| >> sigma.
 //
@@ -67,6 +71,13 @@ __device__ __forceinline__ void unpack(const uint4& u, float* f) {
   const E* e = reinterpret_cast<const E*>(&u);
 #pragma unroll
   for (int i = 0; i < V; ++i) f[i] = Elem<E>::to_f(e[i]);
+}
+template <typename E>
+__device__ __forceinline__ void add(const uint4& u, float* f) {
+  constexpr int V = 16 / sizeof(E);
+  const E* e = reinterpret_cast<const E*>(&u);
+#pragma unroll
+  for (int i = 0; i < V; ++i) f[i] += Elem<E>::to_f(e[i]);
 }
 template <typename E>
 __device__ __forceinline__ uint4 pack(const float* f) {
@@ -200,7 +211,7 @@ norm_fwd_kernel(const __grid_constant__ Params p) {
   }
 }
 
-template <typename E, int VPT, int TT, bool BLOCK>
+template <typename E, int VPT, int TT, bool BLOCK, bool RES>
 __global__ void __launch_bounds__(BLOCK ? kBlockThreads<E> : kThreads)
 norm_bwd_kernel(const __grid_constant__ Params p) {
   constexpr int V = 16 / sizeof(E), CG = V / TT;
@@ -224,13 +235,14 @@ norm_bwd_kernel(const __grid_constant__ Params p) {
   const int64_t first = at.row - (BLOCK ? 0 : (threadIdx.x & 31) / p.lpr);
   for (int64_t base = first, row = at.row; base < p.N; base += at.step, row += at.step) {
     const bool live = row < p.N;
-    uint4 ux[VPT], ug[VPT];                // kept packed between the two passes over them
+    uint4 ug[VPT], ux[VPT], ur[VPT];       // kept packed between the two passes over them
     const float mu = live ? p.mean[row] : 0.f, rstd = live ? p.rstd[row] : 0.f;
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       const int vec = at.lane + j * p.lpr;
-      ux[j] = ug[j] = make_uint4(0, 0, 0, 0);
+      ux[j] = ug[j] = ur[j] = make_uint4(0, 0, 0, 0);
       if (live && vec < p.nvec) {
+        if (RES) ur[j] = ld_stream(static_cast<const uint4*>(p.res) + row * p.nvec + vec);
         ux[j] = ld_stream(static_cast<const uint4*>(p.x) + row * p.nvec + vec);
         ug[j] = ld_stream(static_cast<const uint4*>(p.gy) + row * p.nvec + vec);
       }
@@ -241,6 +253,7 @@ norm_bwd_kernel(const __grid_constant__ Params p) {
       if (!(live && at.lane + j * p.lpr < p.nvec)) continue;
       float x[V], g[V];
       unpack<E>(ux[j], x);
+      if (RES) add<E>(ur[j], x);
       unpack<E>(ug[j], g);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -260,6 +273,7 @@ norm_bwd_kernel(const __grid_constant__ Params p) {
       if (!(live && vec < p.nvec)) continue;
       float x[V], g[V];
       unpack<E>(ux[j], x);
+      if (RES) add<E>(ur[j], x);
       unpack<E>(ug[j], g);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
@@ -392,7 +406,10 @@ template <typename E, int TT, int VPT>
 cudaError_t launch_vpt(const Params& p, const Shape& s, bool bwd, int blocks, cudaStream_t st) {
   const int threads = s.block ? s.lpr : kThreads;
   const size_t smem = bwd ? (size_t)2 * (p.F / TT) * sizeof(float) : 0;
-  void (*k)(Params) = bwd ? (s.block ? norm_bwd_kernel<E, VPT, TT, true> : norm_bwd_kernel<E, VPT, TT, false>)
+  void (*k)(Params) = bwd ? (p.res ? (s.block ? norm_bwd_kernel<E, VPT, TT, true, true>
+                                              : norm_bwd_kernel<E, VPT, TT, false, true>)
+                                   : (s.block ? norm_bwd_kernel<E, VPT, TT, true, false>
+                                              : norm_bwd_kernel<E, VPT, TT, false, false>))
                           : (s.block ? norm_fwd_kernel<E, VPT, TT, true> : norm_fwd_kernel<E, VPT, TT, false>);
   if (smem > 40 * 1024) {
     const cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(k), 2 * kMaxF * (int)sizeof(float));
@@ -488,7 +505,7 @@ extern "C" int64_t eqlin_norm_workspace_bytes(int T, int64_t Cp, int64_t N) {
 }
 
 extern "C" eqlin_status_t eqlin_norm_backward(int T, int64_t Cp, eqlin_dtype_t dtype, const void* gy, const void* gsum,
-                                              const void* x, const void* w, const float* mean, const float* rstd,
+                                              const void* x, const void* res, const void* w, const float* mean, const float* rstd,
                                               void* dx, float* dw, float* db, void* workspace, int64_t N,
                                               void* stream) {
   const eqlin_status_t st = norm::check(T, Cp, dtype, N);
@@ -501,10 +518,11 @@ extern "C" eqlin_status_t eqlin_norm_backward(int T, int64_t Cp, eqlin_dtype_t d
     return e == cudaSuccess ? EQLIN_OK : EQLIN_ERR_CUDA;
   }
   if (!gy || !x || !mean || !rstd || !dx || !workspace) return EQLIN_ERR_INVALID_ARG;
-  if (norm::bad16(gy) || norm::bad16(gsum) || norm::bad16(x) || norm::bad16(dx) || norm::bad16(workspace))
+  if (norm::bad16(gy) || norm::bad16(gsum) || norm::bad16(x) || norm::bad16(res) || norm::bad16(dx) || norm::bad16(workspace))
     return EQLIN_ERR_MISALIGNED;
   norm::Params p = norm::describe(T, Cp, dtype, N);
   p.x = x;
+  p.res = res;
   p.gy = gy;
   p.gs = gsum;
   p.w = w;

@@ -65,7 +65,8 @@ SIGNATURES = {
     "eqlin_destroy": ([_vp], None),
     "eqlin_norm_forward": ([_int, _i64, _int, _vp, _vp, _vp, _vp, _f32, _vp, _vp, _vp, _vp, _i64, _vp], _int),
     "eqlin_norm_workspace_bytes": ([_int, _i64, _i64], _i64),
-    "eqlin_norm_backward": ([_int, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp], _int),
+    "eqlin_norm_backward": ([_int, _i64, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _i64, _vp],
+                            _int),
     "eqlin_rope_create": ([_int, _i64, _int, ctypes.POINTER(_i64), ctypes.POINTER(ctypes.c_double),
                            ctypes.POINTER(_vp)], _int),
     "eqlin_rope_destroy": ([_vp], None),
@@ -405,8 +406,8 @@ def norm_workspace(T: int, Cp: int, N: int, device=None) -> torch.Tensor:
 
 def norm_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
                   dx: torch.Tensor, dw: torch.Tensor, db: torch.Tensor, T: int, gsum: torch.Tensor | None = None,
-                  workspace: torch.Tensor | None = None, stream=None):
-    """Gradients of the norm; x is what was normalised (x, or xsum); see eqlin_norm_backward."""
+                  res: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
+    """Gradients of the norm of x (or of x + res); see eqlin_norm_backward."""
     N, F = _shape2(gy, "gy")
     dt, dev, Cp = gy.dtype, gy.device, w.shape[0]
     if Cp * T != F:
@@ -421,7 +422,8 @@ def norm_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, mean: torc
             raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, needs {need}")
         _check(lib().eqlin_norm_backward(
             T, Cp, _DT[dt], _ptr(gy, dt, None, "gy", dev), _opt(gsum, dt, (N, F), "gsum", dev),
-            _ptr(x, dt, (N, F), "x", dev), _ptr(w, dt, (Cp,), "w", dev), _ptr(mean, torch.float32, (N,), "mean", dev),
+            _ptr(x, dt, (N, F), "x", dev), _opt(res, dt, (N, F), "res", dev), _ptr(w, dt, (Cp,), "w", dev),
+            _ptr(mean, torch.float32, (N,), "mean", dev),
             _ptr(rstd, torch.float32, (N,), "rstd", dev), _ptr(dx, dt, (N, F), "dx", dev),
             _ptr(dw, torch.float32, (Cp,), "dw", dev), _ptr(db, torch.float32, (Cp,), "db", dev),
             _ptr(workspace, workspace.dtype, None, "workspace", dev), N, st), "eqlin_norm_backward")

@@ -300,17 +300,17 @@ EQLIN_API eqlin_status_t eqlin_norm_forward(int T, int64_t Cp, eqlin_dtype_t dty
 EQLIN_API int64_t eqlin_norm_workspace_bytes(int T, int64_t Cp, int64_t N);
 
 /*
- * Its gradient: with x the normalised rows (x, or sum), xh = (x - mean) rstd
+ * Its gradient: with s = x + res again (res NULL: s = x), xh = (s - mean) rstd
  * and g = gy w,
  *   dx = rstd (g - mean_f g - xh mean_f(g xh)) + gsum     (the gradient of x and of res)
  *   dw[c] = sum_n sum_t gy xh,    db[c] = sum_n sum_t gy
- * gsum [N, F], the gradient of sum, may be NULL.  dx may be gy or gsum.  dw
+ * gsum [N, F], the gradient of sum, may be NULL.  dx may be gy, gsum, x or res.  dw
  * and db [C'] are float32 and overwritten; sums run in a fixed order, without
  * atomics.  workspace: eqlin_norm_workspace_bytes, 16-byte aligned; calls that
  * may overlap on the GPU need one each.
  */
 EQLIN_API eqlin_status_t eqlin_norm_backward(int T, int64_t Cp, eqlin_dtype_t dtype, const void *gy,
-                                             const void *gsum, const void *x, const void *w,
+                                             const void *gsum, const void *x, const void *res, const void *w,
                                              const float *mean, const float *rstd, void *dx, float *dw,
                                              float *db, void *workspace, int64_t N, void *stream);
 

@@ -60,9 +60,7 @@ def norm_bounds(x, res, w, b, gy, gs, T, eps, dt):
     if res is not None:
         out["xsum"] = (s, u * s.abs() + z)
     if gy is not None:
-        # the backward reads the sum as stored: rounded to the type
-        es = u * s.abs() + z if res is not None else torch.zeros_like(s)
-        exh = es * rstd + c * mag                                  # error of xh
+        exh = c * mag                                              # error of xh
         g = gy.double()
         gw = g * wf
         m1, m2 = gw.mean(1, keepdim=True), (gw * xh).mean(1, keepdim=True)
@@ -112,8 +110,8 @@ def test_norm(N, Cp, T, with_res, dtype):
     xsum = torch.empty((N, F), dtype=dt, device="cuda") if with_res else None
     dw, db = torch.empty(Cp, device="cuda"), torch.empty(Cp, device="cuda")
     eqlin.norm_forward(d["x"], d["w"], d["b"], y[1:-1], mean, rstd, T, res=None if res is None else res.cuda(), xsum=xsum)
-    eqlin.norm_backward(d["gy"], xsum if with_res else d["x"], d["w"], mean, rstd, dx[1:-1], dw, db, T,
-                        gsum=None if gs is None else gs.cuda())
+    eqlin.norm_backward(d["gy"], d["x"], d["w"], mean, rstd, dx[1:-1], dw, db, T, gsum=None if gs is None else gs.cuda(),
+                        res=None if res is None else res.cuda())
     torch.cuda.synchronize()
     got = {"y": y[1:-1], "mean": mean, "rstd": rstd, "dx": dx[1:-1], "dw": dw, "db": db}
     if with_res:
@@ -512,12 +510,12 @@ def test_norm_refusals():
     assert fwd(mean=None) == -1 and fwd(rstd=None) == -1 and fwd(x=ctypes.c_void_p(4104)) == -3
     assert fwd(N=0) == 0
 
-    def bwd(T=4, Cp=8, dt=bf, gy=one, gs=None, x=one, w=one, mean=one, rstd=one, dx=one, dw=one, db=one, ws=one, N=3):
-        return L.eqlin_norm_backward(T, Cp, dt, gy, gs, x, w, mean, rstd, dx, dw, db, ws, N, None)
+    def bwd(T=4, Cp=8, dt=bf, gy=one, gs=None, x=one, res=None, w=one, mean=one, rstd=one, dx=one, dw=one, db=one, ws=one, N=3):
+        return L.eqlin_norm_backward(T, Cp, dt, gy, gs, x, res, w, mean, rstd, dx, dw, db, ws, N, None)
 
     for name in ("gy", "x", "w", "mean", "rstd", "dx", "dw", "db", "ws"):
         assert bwd(**{name: None}) == -1, name
-    for name in ("gy", "gs", "x", "dx", "ws"):
+    for name in ("gy", "gs", "x", "res", "dx", "ws"):
         assert bwd(**{name: ctypes.c_void_p(4100)}) == -3, name
     assert bwd(T=17) == -2 and bwd(Cp=3) == -3 and bwd(N=-2) == -1
     assert L.eqlin_norm_workspace_bytes(4, 8, 2) == 2 * 2 * 8 * 4

@@ -366,8 +366,8 @@ def _own_norm(st):
     if c["res"]:
         out["xsum"] = st["xsum"]
     if c["train"]:
-        eqlin.norm_backward(st["gy"], st["xsum"] if c["res"] else st["x"], st["w"], st["mean"], st["rstd"],
-                            st["dx"], st["dw"], st["db"], c["T"], gsum=st["gsum"], workspace=st["ws"])
+        eqlin.norm_backward(st["gy"], st["x"], st["w"], st["mean"], st["rstd"], st["dx"], st["dw"], st["db"], c["T"],
+                            gsum=st["gsum"], res=st["res"], workspace=st["ws"])
         out.update(dx=st["dx"], dw=st["dw"], db=st["db"])
     return out
 

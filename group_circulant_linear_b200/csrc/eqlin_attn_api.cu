@@ -18,7 +18,8 @@ eqlin_status_t describe(const eqlin_attention_t* a, eqlin_dtype_t dtype, attn::P
   if (!isfinite(a->scale) || !(a->scale > 0.f) || !isfinite(a->cap) || a->cap < 0.f) return EQLIN_ERR_INVALID_ARG;
   if (a->axes < 0 || (a->axes > 0 && !a->slopes)) return EQLIN_ERR_INVALID_ARG;
   if (a->axes > attn::kMaxAxes) return EQLIN_ERR_UNSUPPORTED;
-  if (a->heads > 65536 || a->head_dim > attn::kMaxHeadDim || a->tokens > 0x7fffffff) return EQLIN_ERR_UNSUPPORTED;
+  if (a->heads > 65536 || a->head_dim > attn::kMaxHeadDim || a->tokens > 0x7fffff00)   // a tile's end fits 32 bits
+    return EQLIN_ERR_UNSUPPORTED;
   const int64_t es = dtype == EQLIN_F32 ? 4 : 2;
   if (a->head_dim * es % 16) return EQLIN_ERR_MISALIGNED;
   if (!a->offsets) {

@@ -34,7 +34,8 @@ template <int DP> struct FwdCfg {
 };
 
 template <int DP, typename E, int AXES, bool CAP>
-__global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_constant__ Params p,
+                                                                 const __grid_constant__ Maps maps) {
   using C = FwdCfg<DP>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
@@ -57,7 +58,8 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
   const Work w = work_of(p, p.H);
-  const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)(w.head / (p.H / p.K)) * p.D;
+  const int kv_head = w.head / (p.H / p.K);
+  const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)kv_head * p.D;
   if (w.doc == p.docs) {
     outside_rows(p, w.tile, [&](int64_t r) {
       for (int d = threadIdx.x; d < p.D; d += kThreads) static_cast<E*>(p.o)[r * p.os + qh + d] = Elem<E>::from_f(0.f);
@@ -65,9 +67,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
     });
     return;
   }
-  int64_t lo, hi;
-  doc_range(p, w.doc, lo, hi);
-  if (lo + (int64_t)w.tile * ROWS >= hi) return;
+  int64_t lo64, hi64;
+  doc_range(p, w.doc, lo64, hi64);
+  if (lo64 + (int64_t)w.tile * ROWS >= hi64) return;
+  const int lo = (int)uniform((uint32_t)lo64), hi = (int)uniform((uint32_t)hi64);
+  const int first = lo + w.tile * ROWS;
+  // tokens are below 2^31, a tile's end may not be: loops count tiles
+  const int own_tiles = (int)(((int64_t)(hi - first) + (int64_t)p.hint * ROWS - 1) / ((int64_t)p.hint * ROWS));
+  const int key_tiles = (hi - lo - 1) / ROWS + 1;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 32);
@@ -92,7 +99,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   // after the allocation: a dependent kernel's block that takes TMEM columns
   // early must not be able to starve one of these
   grid_dep_launch();
@@ -103,99 +110,127 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
 
   if (warp == LOAD_WARP) {
     Pending pend;
-    uint32_t item = 0, tile_no = 0;
+    Side<AXES, false, ROWS> sidev;
+    uint32_t item = 0;
     bool ok = true;
-    for (int64_t r0 = lo + (int64_t)w.tile * ROWS; ok && r0 < hi; r0 += (int64_t)p.hint * ROWS, ++tile_no) {
-      ok = claim(pend, q_empty, (tile_no & 1) ^ 1, limit, abort_flag, lane, err, site(K_ATTN_FWD, 2, 0), tile_no);
+    if (AXES) sidev.fetch(p, w.head, lo, hi, lane);
+    for (int t = 0; ok && t < own_tiles; ++t) {
+      const int r0 = first + t * p.hint * ROWS;
+      ok = claim(pend, q_empty, (t & 1) ^ 1, limit, abort_flag, err, site(K_ATTN_FWD, 2, 0), t);
       if (!ok) break;
-      load_rows<DP, E>(smem_u32(smem), p.q, p.qs, qh, r0, hi, ROWS, p.D, 2 * d16, lane);
-      cp_async_commit();
-      announce_later(pend, q_full);
-      for (int64_t c0 = lo; ok && c0 < hi; c0 += ROWS) {
-        const int nc = (int)(hi - c0 < ROWS ? hi - c0 : ROWS), rows = (nc + 15) & ~15;
+      if (hi - r0 >= ROWS) {
+        if (lane == 0) {
+          expect_bytes(q_full, C::TILE);
+          tma_rows<DP, ROWS>(smem, &maps.m[0], w.head, r0, q_full);
+        }
+        mbar_arrive(q_full);
+      } else {
+        load_rows<DP, E>(smem_u32(smem), p.q, p.qs, qh, r0, hi, ROWS, p.D, 2 * d16, lane);
+        cp_async_commit();
+        announce_later(pend, q_full);
+      }
+      for (int j = 0; ok && j < key_tiles; ++j) {
+        const int c0 = lo + j * ROWS, nc = min(hi - c0, ROWS);
 #pragma unroll 1
         for (int kv = 0; kv < 2; ++kv, ++item) {
           const int slot = item % C::SLOTS;
-          const uint32_t ph = (item / C::SLOTS) & 1;
-          ok = claim(pend, kv_empty + slot, ph ^ 1, limit, abort_flag, lane, err, site(K_ATTN_FWD, 2, 1), item);
+          ok = claim(pend, kv_empty + slot, ((item / C::SLOTS) & 1) ^ 1, limit, abort_flag, err, site(K_ATTN_FWD, 2, 1),
+                     item);
           if (!ok) break;
-          load_rows<DP, E>(smem_u32(ring + slot * C::TILE), kv ? p.v : p.k, kv ? p.vs : p.ks, kh, c0, hi, rows, p.D,
-                           2 * d16, lane);
+          uint8_t* to = ring + slot * C::TILE;
+          if (nc == ROWS && lane == 0) {
+            expect_bytes(kv_full + slot, C::TILE);
+            tma_rows<DP, ROWS>(to, &maps.m[1 + kv], kv_head, c0, kv_full + slot);
+          }
           // positions go with V: its slot is free once the softmax has used them
-          if (AXES && kv) load_positions(spos + (slot >> 1) * kMaxAxes * ROWS, p, c0, hi, (nc + 31) & ~31, lane);
-          cp_async_commit();
-          announce_later(pend, kv_full + slot);
+          if (AXES && kv) {
+            sidev.store(spos + (slot >> 1) * kMaxAxes * ROWS, 0.f, 0.f, lane);
+            sidev.fetch(p, w.head, j + 1 < key_tiles ? c0 + ROWS : lo, hi, lane);
+          }
+          if (nc == ROWS) {
+            mbar_arrive(kv_full + slot);
+          } else {
+            load_rows<DP, E>(smem_u32(to), kv ? p.v : p.k, kv ? p.vs : p.ks, kh, c0, hi, (nc + 15) & ~15, p.D, 2 * d16,
+                             lane);
+            cp_async_commit();
+            announce_later(pend, kv_full + slot);
+          }
         }
       }
     }
     announce_all(pend);
     if (!ok && lane == 0) raise_abort(abort_flag, err);
   } else if (warp == MMA_WARP) {
-    if (lane == 0) {
-      uint32_t item = 0, tile_no = 0, step = 0;               // step: key tiles since the start
-      bool ok = true;
-      const uint32_t q_addr = smem_u32(smem);
-      const uint32_t id_o = idesc_f16(Pair<E>::fmt, (uint32_t)(16 * d16)) | kBTransposed;
-      auto qk = [&](int64_t c0, uint32_t it, uint32_t n) -> bool {   // scores of key tile n, whose K is item `it`
-        const int slot = it % C::SLOTS;
-        if (!bwait(kv_full + slot, (it / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 1), it)) return false;
-        // S is free once every thread has read the previous scores (P over S: once P, and with it PV, is issued)
-        if (!C::OVER && !bwait(s_free, (n & 1) ^ 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 2), n)) return false;
-        tc_fence_after();
-        const int nc = (int)(hi - c0 < ROWS ? hi - c0 : ROWS);
-        const uint32_t id = idesc_f16(Pair<E>::fmt, (uint32_t)((nc + 15) & ~15));
-        const uint32_t k_addr = smem_u32(ring + slot * C::TILE);
-        for (int d = 0; d < d16; ++d) {
+    const uint32_t leader = lane == 0;
+    uint32_t item = 0, step = 0;                              // step: key tiles since the start
+    bool ok = true;
+    const uint32_t q_addr = smem_u32(smem);
+    const uint32_t id_o = idesc_f16(Pair<E>::fmt, (uint32_t)(16 * d16)) | kBTransposed;
+    // scores of key tile j, step n, whose K is item `it`
+    auto qk = [&](int j, uint32_t it, uint32_t n) -> bool {
+      const int slot = it % C::SLOTS;
+      if (!wwait_all(kv_full + slot, (it / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 1), it)) return false;
+      // S is free once every thread has read the previous scores (P over S: once P, and with it PV, is issued)
+      if (!C::OVER && !wwait_all(s_free, (n & 1) ^ 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 2), n)) return false;
+      tc_fence_after();
+      const int nc = min(hi - lo - j * ROWS, ROWS);
+      const uint32_t id = idesc_f16(Pair<E>::fmt, (uint32_t)((nc + 15) & ~15));
+      const uint32_t k_addr = smem_u32(ring + slot * C::TILE);
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d)
+        if (d < d16) {
           const uint32_t off = (d >> 2) * PANEL + (d & 3) * 32;
-          mma_f16_ss(tmem, smem_desc(q_addr + off, 128), smem_desc(k_addr + off, 128), id, d > 0);
+          mma_ss(leader, tmem, smem_desc(q_addr + off, 128), smem_desc(k_addr + off, 128), id, d > 0);
         }
-        mma_commit(s_full);
-        mma_commit(kv_empty + slot);
-        return true;
-      };
-      for (int64_t r0 = lo + (int64_t)w.tile * ROWS; ok && r0 < hi; r0 += (int64_t)p.hint * ROWS, ++tile_no) {
-        ok = bwait(q_full, tile_no & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 0), tile_no) && qk(lo, item, step);
-        for (int64_t c0 = lo; ok && c0 < hi; c0 += ROWS, item += 2, ++step) {
-          const bool more = c0 + ROWS < hi;
-          if (!C::OVER && more) ok = qk(c0 + ROWS, item + 2, step + 1);
-          if (!C::OVER && !more) mma_commit(q_empty);
-          const uint32_t vi = item + 1;
-          const int slot = vi % C::SLOTS;
-          ok = ok && bwait(kv_full + slot, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 1), vi) &&
-               bwait(p_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 3), step);
-          if (!ok) break;
-          tc_fence_after();
-          const int nc = (int)(hi - c0 < ROWS ? hi - c0 : ROWS), steps = (nc + 15) / 16;
-          const uint32_t v_addr = smem_u32(ring + slot * C::TILE);
-          for (int s = 0; s < steps; ++s)
-            mma_f16_ts(tmem + C::O_COL, tmem + C::P_COL + s * 8, smem_desc_mn(v_addr + s * 2048, PANEL, 1024), id_o,
-                       c0 > lo || s > 0);
-          mma_commit(o_full);
-          mma_commit(kv_empty + slot);
-          if (C::OVER && more) ok = qk(c0 + ROWS, item + 2, step + 1);
-          if (C::OVER && !more) mma_commit(q_empty);
-        }
+      commit(leader, s_full);
+      commit(leader, kv_empty + slot);
+      return true;
+    };
+    for (int t = 0; ok && t < own_tiles; ++t) {
+      ok = wwait_all(q_full, t & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 0), t) && qk(0, item, step);
+      for (int j = 0; ok && j < key_tiles; ++j, item += 2, ++step) {
+        const bool more = j + 1 < key_tiles;
+        if (!C::OVER && more) ok = qk(j + 1, item + 2, step + 1);
+        if (!C::OVER && !more) commit(leader, q_empty);
+        const uint32_t vi = item + 1;
+        const int slot = vi % C::SLOTS;
+        ok = ok && wwait_all(kv_full + slot, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 1), vi) &&
+             wwait_all(p_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 3), step);
+        if (!ok) break;
+        tc_fence_after();
+        const int steps = (min(hi - lo - j * ROWS, ROWS) + 15) / 16;
+        const uint32_t v_addr = smem_u32(ring + slot * C::TILE);
+#pragma unroll
+        for (int s = 0; s < ROWS / 16; ++s)
+          if (s < steps)
+            mma_ts(leader, tmem + C::O_COL, tmem + C::P_COL + s * 8, smem_desc_mn(v_addr + s * 2048, PANEL, 1024), id_o,
+                   j > 0 || s > 0);
+        commit(leader, o_full);
+        commit(leader, kv_empty + slot);
+        if (C::OVER && more) ok = qk(j + 1, item + 2, step + 1);
+        if (C::OVER && !more) commit(leader, q_empty);
       }
-      if (!ok) raise_abort(abort_flag, err);
-      mma_commit(drain);
-      mbar_wait(drain, 0, kDefaultWaitLimit);
     }
+    if (!ok && lane == 0) raise_abort(abort_flag, err);
+    commit(leader, drain);
+    mbar_wait(drain, 0, kDefaultWaitLimit);
     __syncwarp();
   } else {
     const uint32_t my = tmem + ((uint32_t)(warp * 32) << 16);
     const Score sc = score_of(p, w.head);
     uint32_t step = 0;
     bool ok = true;
-    for (int64_t r0 = lo + (int64_t)w.tile * ROWS; ok && r0 < hi; r0 += (int64_t)p.hint * ROWS) {
-      const int64_t row = r0 + warp * 32 + lane;
-      const bool any = r0 + warp * 32 < hi;                   // does the warp have a row at all
+    for (int t = 0; ok && t < own_tiles; ++t) {
+      const int r0 = first + t * p.hint * ROWS + warp * 32;   // the warp's first row
+      const bool any = r0 < hi, live = lane < hi - r0;
+      const int64_t row = (int64_t)r0 + lane;
       float own[AXES ? AXES : 1];
 #pragma unroll
-      for (int a = 0; a < AXES; ++a) own[a] = row < hi ? p.pos[row * AXES + a] : 0.f;
-      float m = -INFINITY, l = 0.f;
-      for (int64_t c0 = lo; c0 < hi; c0 += ROWS, ++step) {
-        const int nc = (int)(hi - c0 < ROWS ? hi - c0 : ROWS);
-        ok = wwait(s_full, step & 1, limit, abort_flag, lane, err, site(K_ATTN_FWD, 0, 0), step);
+      for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
+      float m = -INFINITY, l = 0.f;                           // m in base-2 units
+      for (int j = 0; j < key_tiles; ++j, ++step) {
+        const int nc = min(hi - lo - j * ROWS, ROWS);
+        ok = wwait_all(s_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 0), step);
         if (AXES && ok) {
           const uint32_t vi = 2 * step + 1;
           ok = wwait_all(kv_full + vi % C::SLOTS, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 1), step);
@@ -222,37 +257,25 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             if (c * 32 >= nc) continue;
-            if (CAP || AXES) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                float d[4] = {0.f, 0.f, 0.f, 0.f};
-                if (AXES) distances<AXES>(pos, c * 32 + i, own, d);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  float& v = s[c * 32 + i + k];
-                  v = CAP ? sc.cap2 * tanh_raw(v, sc) : v * sc.scale2;
-                  if (AXES) v = fmaf(-sc.slope2, d[k], v);
-                }
-              }
-            }
+            transform32<AXES, CAP>(s + c * 32, pos, c * 32, own, sc);
             if (c * 32 + 32 > nc) {
 #pragma unroll
               for (int i = 0; i < 32; ++i)
                 if (c * 32 + i >= nc) s[c * 32 + i] = -INFINITY;
             }
-            float t0 = s[c * 32], t1 = s[c * 32 + 1];
+            float t0 = top, t1 = s[c * 32];
 #pragma unroll
-            for (int i = 2; i < 32; i += 2) {
-              t0 = fmaxf(t0, s[c * 32 + i]);
-              t1 = fmaxf(t1, s[c * 32 + i + 1]);
+            for (int i = 1; i < 31; i += 3) {                 // three-way maxima, two chains
+              t0 = fmaxf(fmaxf(t0, s[c * 32 + i]), s[c * 32 + i + 1]);
+              t1 = fmaxf(t1, s[c * 32 + i + 2]);
             }
-            top = fmaxf(top, fmaxf(t0, t1));
+            top = fmaxf(fmaxf(t0, t1), s[c * 32 + 31]);
           }
-          if (!(CAP || AXES)) top *= sc.scale2;               // scale > 0
+          top *= sc.scale2;                                   // scale > 0
         }
         // P's columns, and O, are free once the previous product is done
-        if (c0 > lo) {
-          ok = wwait(o_full, (step - 1) & 1, limit, abort_flag, lane, err, site(K_ATTN_FWD, 0, 2), step);
+        if (j > 0) {
+          ok = wwait_all(o_full, (step - 1) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 2), step);
           if (!ok) break;
           tc_fence_after();
           const bool grow = top > m + kLag;
@@ -277,29 +300,38 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
           m = top;
         }
         if (any) {
-          const float k2 = (CAP || AXES) ? 1.f : sc.scale2;
-          float l0 = 0.f, l1 = 0.f;
+          const uint64_t k2 = pk2(sc.scale2, sc.scale2), off = pk2(-m, -m);
+          uint64_t l0 = 0, l1 = 0;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             if (c * 32 >= nc) continue;
             uint32_t pk[16];
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float a = ex2(fmaf(s[c * 32 + i], k2, -m)), b = ex2(fmaf(s[c * 32 + i + 1], k2, -m));
-              l0 += a;
-              l1 += b;
+            for (int i = 0; i < 32; i += 4) {
+              float a, b, d, e;
+              unpk2(fma2(pk2(s[c * 32 + i], s[c * 32 + i + 1]), k2, off), a, b);
+              unpk2(fma2(pk2(s[c * 32 + i + 2], s[c * 32 + i + 3]), k2, off), d, e);
+              a = ex2(a);
+              b = ex2(b);
+              d = ex2(d);
+              e = ex2(e);
+              l0 = add2(l0, pk2(a, b));
+              l1 = add2(l1, pk2(d, e));
               pk[i / 2] = Pair<E>::pack(a, b);
+              pk[i / 2 + 1] = Pair<E>::pack(d, e);
             }
             tmem_st_32x32b_x16(my + C::P_COL + c * 16, pk);
           }
-          l += l0 + l1;
+          float a, b;
+          unpk2(add2(l0, l1), a, b);
+          l += a + b;
           tmem_wait_st();
         }
         tc_fence_before();
         mbar_arrive(p_full);
       }
       if (!ok) break;
-      ok = wwait(o_full, (step - 1) & 1, limit, abort_flag, lane, err, site(K_ATTN_FWD, 0, 3), step);
+      ok = wwait_all(o_full, (step - 1) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 3), step);
       if (!ok) break;
       tc_fence_after();
       if (any) {
@@ -316,12 +348,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
 #pragma unroll
           for (int i = 0; i < 16; i += 2)
             pk[i / 2] = Pair<E>::pack(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-          if (row < hi) {
+          if (live) {
             *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
             if (c * 16 + 8 < p.D) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
           }
         }
-        if (row < hi) p.lse[(int64_t)w.head * p.N + row] = (m + log2f(l)) * kLn2;
+        if (live) p.lse[(int64_t)w.head * p.N + row] = (m + log2f(l)) * kLn2;
       }
       tc_fence_before();
     }
@@ -334,18 +366,24 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
 }
 
 template <int DP, typename E, bool CAP>
-cudaError_t forward_axes(const Params& p, cudaStream_t st) {
+cudaError_t forward_axes(const Params& p, const Maps& maps, cudaStream_t st) {
   constexpr int smem = FwdCfg<DP>::SMEM;
   switch (p.axes) {
-    case 0: return launch_rows(attn_tc_fwd_kernel<DP, E, 0, CAP>, smem, p, p.H, st);
-    case 1: return launch_rows(attn_tc_fwd_kernel<DP, E, 1, CAP>, smem, p, p.H, st);
-    case 2: return launch_rows(attn_tc_fwd_kernel<DP, E, 2, CAP>, smem, p, p.H, st);
-    default: return launch_rows(attn_tc_fwd_kernel<DP, E, 3, CAP>, smem, p, p.H, st);
+    case 0: return launch_rows(attn_tc_fwd_kernel<DP, E, 0, CAP>, smem, p, maps, p.H, kThreads, st);
+    case 1: return launch_rows(attn_tc_fwd_kernel<DP, E, 1, CAP>, smem, p, maps, p.H, kThreads, st);
+    case 2: return launch_rows(attn_tc_fwd_kernel<DP, E, 2, CAP>, smem, p, maps, p.H, kThreads, st);
+    default: return launch_rows(attn_tc_fwd_kernel<DP, E, 3, CAP>, smem, p, maps, p.H, kThreads, st);
   }
 }
 template <int DP, typename E>
 cudaError_t forward_cap(const Params& p, cudaStream_t st) {
-  return p.cap > 0.f ? forward_axes<DP, E, true>(p, st) : forward_axes<DP, E, false>(p, st);
+  Maps maps;
+  cudaError_t e = make_map(&maps.m[0], p.q, Pair<E>::fmt, p, p.H, p.qs, ROWS);
+  if (e == cudaSuccess) e = make_map(&maps.m[1], p.k, Pair<E>::fmt, p, p.K, p.ks, ROWS);
+  if (e == cudaSuccess) e = make_map(&maps.m[2], p.v, Pair<E>::fmt, p, p.K, p.vs, ROWS);
+  if (e != cudaSuccess) return e;
+  maps.m[3] = maps.m[0];
+  return p.cap > 0.f ? forward_axes<DP, E, true>(p, maps, st) : forward_axes<DP, E, false>(p, maps, st);
 }
 template <typename E>
 cudaError_t forward_dim(const Params& p, cudaStream_t st) {

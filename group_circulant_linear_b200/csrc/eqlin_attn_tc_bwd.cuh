@@ -50,14 +50,78 @@ template <int DP, bool KEYS> struct BwdCfg {
   static_assert(BLOCKS * SMEM <= 227 * 1024, "shared memory");
 };
 
+// One 32-column chunk of a row: raw scores rs and dP rd in, packed P and du out.
+//   KEYS: lse and delta belong to the columns (ls, dl in shared memory, already
+//   in base 2 and scaled), else to the row.
+template <int AXES, bool CAP, bool KEYS, bool SMALL, typename E>
+__device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, const float* side, int c0, const float* own,
+                                       float lse2, float delta, const Score& sc, int left, uint32_t* pp, uint32_t* pd) {
+  constexpr bool F16 = Pair<E>::fmt == 0;
+  constexpr float kDown = F16 ? 1.f / 256.f : 1.f;
+  const uint64_t k2 = pk2(sc.scale2, sc.scale2), in = pk2(sc.in, sc.in), slope = pk2(-sc.slope, -sc.slope);
+  const uint64_t one = pk2(1.f, 1.f), neg = pk2(-1.f, -1.f), down = pk2(kDown, kDown);
+  const uint64_t row_off = pk2(-lse2, -lse2), row_delta = pk2(-delta, -delta);
+#pragma unroll
+  for (int j = 0; j < 32; j += 4) {
+    float d[4];
+    if (AXES) distances<AXES>(side, c0 + j, own, d);
+    ulonglong2 ls, dl;
+    if (KEYS) {
+      ls = *reinterpret_cast<const ulonglong2*>(side + kMaxAxes * ROWS + c0 + j);
+      dl = *reinterpret_cast<const ulonglong2*>(side + kMaxAxes * ROWS + ROWS + c0 + j);
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int i = j + 2 * h;
+      uint64_t x = pk2(__uint_as_float(rs[i]), __uint_as_float(rs[i + 1]));
+      const uint64_t dp = pk2(__uint_as_float(rd[i]), __uint_as_float(rd[i + 1]));
+      uint64_t gain = one;                           // 1 - tanh^2
+      if (CAP) {
+        if (SMALL) {
+          const uint64_t u = mul2(x, in), q = q_small2(u), t = mul2(u, q);
+          x = mul2(x, q);
+          gain = fma2(mul2(t, neg), t, one);
+        } else {
+          float a, b;
+          unpk2(x, a, b);
+          a = tanh_any(a, sc);
+          b = tanh_any(b, sc);
+          const uint64_t t = pk2(a, b);
+          x = pk2(sc.out * a, sc.out * b);
+          gain = fma2(mul2(t, neg), t, one);
+        }
+      }
+      if (AXES) x = fma2(slope, pk2(d[2 * h], d[2 * h + 1]), x);
+      const uint64_t lse_h = KEYS ? mul2(h ? ls.y : ls.x, neg) : row_off;
+      float a, b;
+      unpk2(fma2(x, k2, lse_h), a, b);
+      a = ex2(a);
+      b = ex2(b);
+      uint64_t diff;
+      if (KEYS) diff = fma2(h ? dl.y : dl.x, neg, F16 ? mul2(dp, down) : dp);
+      else diff = add2(dp, row_delta);
+      uint64_t du = mul2(pk2(a, b), diff);
+      if (CAP) du = mul2(du, gain);
+      float e, f;
+      unpk2(du, e, f);
+      if (left < 32) {                               // the document ends inside the chunk
+        if (i >= left) a = e = 0.f;
+        if (i + 1 >= left) b = f = 0.f;
+      }
+      if (KEYS) pp[i / 2] = Pair<E>::pack(a, b);
+      pd[i / 2] = Pair<E>::pack(e, f);
+    }
+  }
+}
+
 template <int DP, typename E, int AXES, bool CAP, bool KEYS>
 __global__ void __launch_bounds__(BwdCfg<DP, KEYS>::THREADS, BwdCfg<DP, KEYS>::BLOCKS)
-attn_tc_bwd_kernel(const __grid_constant__ Params p) {
+attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
   using C = BwdCfg<DP, KEYS>;
   constexpr int CW = C::CW, NWG = C::NWG;
   constexpr uint32_t KID = KEYS ? K_ATTN_DKV : K_ATTN_DQ;
   constexpr bool F16 = Pair<E>::fmt == 0;
-  constexpr float kUp = F16 ? 8.f : 0.f;             // P's factor, as an exponent
+  constexpr float kUp = F16 ? 8.f : 0.f;             // P's factor, as an exponent (KEYS)
   constexpr float kDown = F16 ? 1.f / 256.f : 1.f;
   constexpr int MMA = NWG * 4, LOAD = NWG * 4 + 1;
   extern __shared__ uint8_t smem_raw[];
@@ -83,8 +147,8 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p) {
   grid_dep_wait();
   const int rep = p.H / p.K;
   const Work w = work_of(p, KEYS ? p.K : p.H);
-  const int64_t kh = (int64_t)(KEYS ? w.head : w.head / rep) * p.D;
-  const int64_t qh0 = (int64_t)(KEYS ? w.head * rep : w.head) * p.D;
+  const int kv_head = KEYS ? w.head : w.head / rep, q_head = KEYS ? w.head * rep : w.head;
+  const int64_t kh = (int64_t)kv_head * p.D, qh0 = (int64_t)q_head * p.D;
   if (w.doc == p.docs) {
     outside_rows(p, w.tile, [&](int64_t r) {
       for (int d = threadIdx.x; d < p.D; d += C::THREADS) {
@@ -98,9 +162,14 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p) {
     });
     return;
   }
-  int64_t lo, hi;
-  doc_range(p, w.doc, lo, hi);
-  if (lo + (int64_t)w.tile * ROWS >= hi) return;
+  int64_t lo64, hi64;
+  doc_range(p, w.doc, lo64, hi64);
+  if (lo64 + (int64_t)w.tile * ROWS >= hi64) return;
+  const int lo = (int)uniform((uint32_t)lo64), hi = (int)uniform((uint32_t)hi64);
+  const int first = lo + w.tile * ROWS;
+  const int own_tiles = (int)(((int64_t)(hi - first) + (int64_t)p.hint * ROWS - 1) / ((int64_t)p.hint * ROWS));
+  const int tiles = (hi - lo - 1) / CW + 1;          // moving tiles of one head
+  const int passes = KEYS ? rep : 1;                 // query heads that pass by
 
   if (threadIdx.x == 0) {
     mbar_init(own_full, 32);
@@ -125,127 +194,152 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p) {
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = *tmem_slot;
+  const uint32_t tmem = uniform(*tmem_slot);
   grid_dep_launch();                                 // after the allocation, as in the forward
   volatile int* abort_flag = abort_word;
   int* err = p.err ? p.err : local_err;
   const uint32_t limit = p.wait_limit;
   const int d16 = (p.D + 15) / 16;
-  const int64_t first = lo + (int64_t)w.tile * ROWS, stride = (int64_t)p.hint * ROWS;
-  const int passes = KEYS ? rep : 1;                 // query heads that pass by
-  auto width = [&](int64_t c0) { return (int)(hi - c0 < CW ? hi - c0 : CW); };
 
   if (warp == LOAD) {
     Pending pend;
-    uint32_t item = 0, tile_no = 0;
+    Side<AXES, KEYS, CW> sides;
+    uint32_t item = 0;
     bool ok = true;
-    for (int64_t r0 = first; ok && r0 < hi; r0 += stride, ++tile_no) {
-      ok = claim(pend, own_empty, (tile_no & 1) ^ 1, limit, abort_flag, lane, err, site(KID, 2, 0), tile_no);
+    sides.fetch(p, q_head, lo, hi, lane);
+    for (int t = 0; ok && t < own_tiles; ++t) {
+      const int r0 = first + t * p.hint * ROWS;
+      ok = claim(pend, own_empty, (t & 1) ^ 1, limit, abort_flag, err, site(KID, 2, 0), t);
       if (!ok) break;
-      load_rows<DP, E>(smem_u32(smem), KEYS ? p.k : p.q, KEYS ? p.ks : p.qs, KEYS ? kh : qh0, r0, hi, ROWS, p.D, 2 * d16,
-                       lane);
-      load_rows<DP, E>(smem_u32(smem + C::OWN), KEYS ? p.v : p.go, KEYS ? p.vs : p.gos, KEYS ? kh : qh0, r0, hi, ROWS,
-                       p.D, 2 * d16, lane);
-      cp_async_commit();
-      announce_later(pend, own_full);
+      if (hi - r0 >= ROWS) {
+        if (lane == 0) {
+          expect_bytes(own_full, 2 * C::OWN);
+          tma_rows<DP, ROWS>(smem, &maps.m[0], KEYS ? kv_head : q_head, r0, own_full);
+          tma_rows<DP, ROWS>(smem + C::OWN, &maps.m[1], KEYS ? kv_head : q_head, r0, own_full);
+        }
+        mbar_arrive(own_full);
+      } else {
+        load_rows<DP, E>(smem_u32(smem), KEYS ? p.k : p.q, KEYS ? p.ks : p.qs, KEYS ? kh : qh0, r0, hi, ROWS, p.D,
+                         2 * d16, lane);
+        load_rows<DP, E>(smem_u32(smem + C::OWN), KEYS ? p.v : p.go, KEYS ? p.vs : p.gos, KEYS ? kh : qh0, r0, hi, ROWS,
+                         p.D, 2 * d16, lane);
+        cp_async_commit();
+        announce_later(pend, own_full);
+      }
       for (int g = 0; ok && g < passes; ++g) {
         const int64_t qh = qh0 + (int64_t)g * p.D;
-        for (int64_t c0 = lo; c0 < hi; c0 += CW, ++item) {
-          const int nc = width(c0), rows = (nc + 15) & ~15, slot = item % C::SLOTS;
-          ok = claim(pend, empty + slot, ((item / C::SLOTS) & 1) ^ 1, limit, abort_flag, lane, err, site(KID, 2, 1), item);
+        for (int j = 0; j < tiles; ++j, ++item) {
+          const int c0 = lo + j * CW, nc = min(hi - c0, CW), slot = item % C::SLOTS;
+          ok = claim(pend, empty + slot, ((item / C::SLOTS) & 1) ^ 1, limit, abort_flag, err, site(KID, 2, 1), item);
           if (!ok) break;
-          const uint32_t to = smem_u32(ring + slot * 2 * C::MOV);
-          load_rows<DP, E, CW>(to, KEYS ? p.q : p.k, KEYS ? p.qs : p.ks, KEYS ? qh : kh, c0, hi, rows, p.D, 2 * d16, lane);
-          load_rows<DP, E, CW>(to + C::MOV, KEYS ? p.go : p.v, KEYS ? p.gos : p.vs, KEYS ? qh : kh, c0, hi, rows, p.D,
-                               2 * d16, lane);
-          float* sd = side + slot * SIDE_F;
-          const int rows32 = (nc + 31) & ~31;
-          if (AXES) load_positions(sd, p, c0, hi, rows32, lane);
-          if (KEYS) {
-            const int64_t at = (int64_t)(w.head * rep + g) * p.N + c0;
-            for (int r = lane; r < rows32; r += 32) {
-              sd[kMaxAxes * ROWS + r] = r < nc ? fmaf(p.lse[at + r], kLog2e, -kUp) : 0.f;
-              sd[kMaxAxes * ROWS + ROWS + r] = r < nc ? p.delta[at + r] * kDown : 0.f;
-            }
+          uint8_t* to = ring + slot * 2 * C::MOV;
+          if (nc == CW && lane == 0) {
+            const int head = KEYS ? q_head + g : kv_head;
+            expect_bytes(full + slot, 2 * C::MOV);
+            tma_rows<DP, CW>(to, &maps.m[2], head, c0, full + slot);
+            tma_rows<DP, CW>(to + C::MOV, &maps.m[3], head, c0, full + slot);
           }
-          cp_async_commit();
-          announce_later(pend, full + slot);
+          if (AXES || KEYS) {
+            sides.store(side + slot * SIDE_F, kUp, kDown, lane);
+            const bool last = j + 1 == tiles;
+            sides.fetch(p, q_head + (last ? (g + 1 < passes ? g + 1 : 0) : g), last ? lo : c0 + CW, hi, lane);
+          }
+          if (nc == CW) {
+            mbar_arrive(full + slot);
+          } else {
+            const int rows = (nc + 15) & ~15;
+            load_rows<DP, E, CW>(smem_u32(to), KEYS ? p.q : p.k, KEYS ? p.qs : p.ks, KEYS ? qh : kh, c0, hi, rows, p.D,
+                                 2 * d16, lane);
+            load_rows<DP, E, CW>(smem_u32(to + C::MOV), KEYS ? p.go : p.v, KEYS ? p.gos : p.vs, KEYS ? qh : kh, c0, hi,
+                                 rows, p.D, 2 * d16, lane);
+            cp_async_commit();
+            announce_later(pend, full + slot);
+          }
         }
       }
     }
     announce_all(pend);
     if (!ok && lane == 0) raise_abort(abort_flag, err);
   } else if (warp == MMA) {
-    if (lane == 0) {
-      uint32_t item = 0, tile_no = 0;
-      bool ok = true;
-      const uint32_t a0 = smem_u32(smem), a1 = smem_u32(smem + C::OWN);
-      const uint32_t id_acc = idesc_f16(Pair<E>::fmt, (uint32_t)(16 * d16)) | kBTransposed;
-      auto p_col = [](uint32_t base, int s) { return base + 32 * (s >> 1) + 8 * (s & 1); };   // over the scores' chunks
-      auto scores = [&](uint32_t it, int64_t c0) -> bool {
-        const int slot = it % C::SLOTS;
-        if (!bwait(full + slot, (it / C::SLOTS) & 1, limit, abort_flag, err, site(KID, 1, 1), it)) return false;
-        if (C::SEP && !bwait(s_free, (it & 1) ^ 1, limit, abort_flag, err, site(KID, 1, 2), it)) return false;
+    const uint32_t leader = lane == 0;
+    uint32_t item = 0;
+    bool ok = true;
+    const uint32_t a0 = smem_u32(smem), a1 = smem_u32(smem + C::OWN);
+    const uint32_t id_acc = idesc_f16(Pair<E>::fmt, (uint32_t)(16 * d16)) | kBTransposed;
+    auto scores = [&](uint32_t it, int j) -> bool {
+      const int slot = it % C::SLOTS;
+      if (!wwait_all(full + slot, (it / C::SLOTS) & 1, limit, abort_flag, err, site(KID, 1, 1), it)) return false;
+      if (C::SEP && !wwait_all(s_free, (it & 1) ^ 1, limit, abort_flag, err, site(KID, 1, 2), it)) return false;
+      tc_fence_after();
+      const uint32_t id = idesc_f16(Pair<E>::fmt, (uint32_t)((min(hi - lo - j * CW, CW) + 15) & ~15));
+      const uint32_t x = smem_u32(ring + slot * 2 * C::MOV);
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d)
+        if (d < d16) {
+          const uint32_t oa = (d >> 2) * PANEL + (d & 3) * 32, ob = (d >> 2) * C::MOV_PANEL + (d & 3) * 32;
+          mma_ss(leader, tmem + C::S_COL, smem_desc(a0 + oa, 128), smem_desc(x + ob, 128), id, d > 0);
+        }
+#pragma unroll
+      for (int d = 0; d < DP / 16; ++d)
+        if (d < d16) {
+          const uint32_t oa = (d >> 2) * PANEL + (d & 3) * 32, ob = (d >> 2) * C::MOV_PANEL + (d & 3) * 32;
+          mma_ss(leader, tmem + C::DP_COL, smem_desc(a1 + oa, 128), smem_desc(x + C::MOV + ob, 128), id, d > 0);
+        }
+      commit(leader, s_full);
+      return true;
+    };
+    for (int t = 0; ok && t < own_tiles; ++t) {
+      ok = wwait_all(own_full, t & 1, limit, abort_flag, err, site(KID, 1, 0), t) && scores(item, 0);
+      const int all = passes * tiles;
+      int j = 0;                                     // moving tile of the present pass
+      for (int i = 0; ok && i < all; ++i, ++item) {
+        const bool more = i + 1 < all;
+        const int next = j + 1 < tiles ? j + 1 : 0;
+        if (C::SEP && more) ok = scores(item + 1, next);
+        ok = ok && wwait_all(p_full, item & 1, limit, abort_flag, err, site(KID, 1, 3), item);
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t id = idesc_f16(Pair<E>::fmt, (uint32_t)((width(c0) + 15) & ~15));
-        const uint32_t x = smem_u32(ring + slot * 2 * C::MOV);
-        for (int d = 0; d < d16; ++d) {
-          const uint32_t oa = (d >> 2) * PANEL + (d & 3) * 32, ob = (d >> 2) * C::MOV_PANEL + (d & 3) * 32;
-          mma_f16_ss(tmem + C::S_COL, smem_desc(a0 + oa, 128), smem_desc(x + ob, 128), id, d > 0);
+        const int steps = (min(hi - lo - j * CW, CW) + 15) / 16, slot = item % C::SLOTS;
+        const uint32_t x = smem_u32(ring + slot * 2 * C::MOV), y = x + C::MOV;
+        // P and du: over the scores' chunks (KEYS), or du in its own columns
+        if (KEYS) {
+#pragma unroll
+          for (int s = 0; s < CW / 16; ++s)
+            if (s < steps)
+              mma_ts(leader, tmem + C::ACC0, tmem + C::S_COL + 32 * (s >> 1) + 8 * (s & 1),
+                     smem_desc_mn(y + s * 2048, C::MOV_PANEL, 1024), id_acc, i > 0 || s > 0);
+#pragma unroll
+          for (int s = 0; s < CW / 16; ++s)
+            if (s < steps)
+              mma_ts(leader, tmem + C::ACC1, tmem + C::DP_COL + 32 * (s >> 1) + 8 * (s & 1),
+                     smem_desc_mn(x + s * 2048, C::MOV_PANEL, 1024), id_acc, i > 0 || s > 0);
+        } else {
+#pragma unroll
+          for (int s = 0; s < CW / 16; ++s)
+            if (s < steps)
+              mma_ts(leader, tmem + C::ACC0, tmem + C::ACC1 + s * 8, smem_desc_mn(x + s * 2048, C::MOV_PANEL, 1024),
+                     id_acc, i > 0 || s > 0);
         }
-        for (int d = 0; d < d16; ++d) {
-          const uint32_t oa = (d >> 2) * PANEL + (d & 3) * 32, ob = (d >> 2) * C::MOV_PANEL + (d & 3) * 32;
-          mma_f16_ss(tmem + C::DP_COL, smem_desc(a1 + oa, 128), smem_desc(x + C::MOV + ob, 128), id, d > 0);
-        }
-        mma_commit(s_full);
-        return true;
-      };
-      for (int64_t r0 = first; ok && r0 < hi; r0 += stride, ++tile_no) {
-        ok = bwait(own_full, tile_no & 1, limit, abort_flag, err, site(KID, 1, 0), tile_no) && scores(item, lo);
-        bool fresh = true;                           // accumulators start from zero
-        for (int g = 0; ok && g < passes; ++g) {
-          for (int64_t c0 = lo; ok && c0 < hi; c0 += CW, ++item) {
-            const bool more = c0 + CW < hi || g + 1 < passes;
-            const int64_t next = c0 + CW < hi ? c0 + CW : lo;
-            if (C::SEP && more) ok = scores(item + 1, next);
-            ok = ok && bwait(p_full, item & 1, limit, abort_flag, err, site(KID, 1, 3), item);
-            if (!ok) break;
-            tc_fence_after();
-            const int steps = (width(c0) + 15) / 16, slot = item % C::SLOTS;
-            const uint32_t x = smem_u32(ring + slot * 2 * C::MOV), y = x + C::MOV;
-            if (KEYS) {
-              for (int s = 0; s < steps; ++s)
-                mma_f16_ts(tmem + C::ACC0, p_col(tmem + C::S_COL, s), smem_desc_mn(y + s * 2048, C::MOV_PANEL, 1024),
-                           id_acc, !fresh || s > 0);
-              for (int s = 0; s < steps; ++s)
-                mma_f16_ts(tmem + C::ACC1, p_col(tmem + C::DP_COL, s), smem_desc_mn(x + s * 2048, C::MOV_PANEL, 1024),
-                           id_acc, !fresh || s > 0);
-            } else {
-              for (int s = 0; s < steps; ++s)
-                mma_f16_ts(tmem + C::ACC0, tmem + C::ACC1 + s * 8, smem_desc_mn(x + s * 2048, C::MOV_PANEL, 1024), id_acc,
-                           !fresh || s > 0);
-            }
-            fresh = false;
-            mma_commit(acc_full);
-            mma_commit(empty + slot);
-            if (!more) mma_commit(own_empty);
-            if (!C::SEP && more) ok = scores(item + 1, next);
-          }
-        }
+        commit(leader, acc_full);
+        commit(leader, empty + slot);
+        if (!more) commit(leader, own_empty);
+        if (!C::SEP && more) ok = scores(item + 1, next);
+        j = next;
       }
-      if (!ok) raise_abort(abort_flag, err);
-      mma_commit(drain);
-      mbar_wait(drain, 0, kDefaultWaitLimit);
     }
+    if (!ok && lane == 0) raise_abort(abort_flag, err);
+    commit(leader, drain);
+    mbar_wait(drain, 0, kDefaultWaitLimit);
     __syncwarp();
   } else {
     const int wg = warp >> 2, quarter = warp & 3;
     const uint32_t my = tmem + ((uint32_t)(quarter * 32) << 16);
     uint32_t item = 0;
     bool ok = true;
-    for (int64_t r0 = first; ok && r0 < hi; r0 += stride) {
-      const int64_t row = r0 + quarter * 32 + lane;
-      const bool any = r0 + quarter * 32 < hi, live = row < hi;
+    for (int t = 0; ok && t < own_tiles; ++t) {
+      const int r0 = first + t * p.hint * ROWS + quarter * 32;
+      const bool any = r0 < hi, live = lane < hi - r0;
+      const int64_t row = (int64_t)r0 + lane;
       float own[AXES ? AXES : 1];
 #pragma unroll
       for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
@@ -264,10 +358,10 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p) {
         if (wg == 0) p.delta[(int64_t)w.head * p.N + row] = delta;
       }
       for (int g = 0; ok && g < passes; ++g) {
-        const Score sc = score_of(p, KEYS ? w.head * rep + g : w.head);
-        for (int64_t c0 = lo; c0 < hi; c0 += CW, ++item) {
-          const int nc = width(c0), slot = item % C::SLOTS;
-          ok = wwait(s_full, item & 1, limit, abort_flag, lane, err, site(KID, 0, 0), item);
+        const Score sc = score_of(p, q_head + g);
+        for (int j = 0; j < tiles; ++j, ++item) {
+          const int nc = min(hi - lo - j * CW, CW), slot = item % C::SLOTS;
+          ok = wwait_all(s_full, item & 1, limit, abort_flag, err, site(KID, 0, 0), item);
           if ((AXES || KEYS) && ok)
             ok = wwait_all(full + slot, (item / C::SLOTS) & 1, limit, abort_flag, err, site(KID, 0, 1), item);
           if (!ok) break;
@@ -294,7 +388,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p) {
             tc_fence_before();
             mbar_arrive(s_free);
             if (item > 0) {                          // du's columns are free once the last product is done
-              ok = wwait(acc_full, (item - 1) & 1, limit, abort_flag, lane, err, site(KID, 0, 2), item);
+              ok = wwait_all(acc_full, (item - 1) & 1, limit, abort_flag, err, site(KID, 0, 2), item);
               if (!ok) break;
               tc_fence_after();
             }
@@ -305,43 +399,11 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p) {
             for (int i = 0; i < 2; ++i) {
               const int c = wg + i * NWG;
               if (c * 32 >= nc) continue;
-              const bool edge = c * 32 + 32 > nc;
               uint32_t pp[16], pd[16];
-#pragma unroll
-              for (int j = 0; j < 32; j += 4) {
-                float dist[4] = {0.f, 0.f, 0.f, 0.f}, ls[4], dl[4], pr[4], du[4];
-                if (AXES) distances<AXES>(sd, c * 32 + j, own, dist);
-                if (KEYS) {
-                  *reinterpret_cast<float4*>(ls) = *reinterpret_cast<const float4*>(sd + kMaxAxes * ROWS + c * 32 + j);
-                  *reinterpret_cast<float4*>(dl) =
-                      *reinterpret_cast<const float4*>(sd + kMaxAxes * ROWS + ROWS + c * 32 + j);
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                  const float raw = __uint_as_float(rs[i][j + k]), dp = __uint_as_float(rd[i][j + k]);
-                  const float off = KEYS ? ls[k] : lse2;
-                  float t = 0.f, x;
-                  if (CAP) {
-                    t = tanh_raw(raw, sc);
-                    x = fmaf(sc.cap2, t, -off);
-                  } else {
-                    x = fmaf(raw, sc.scale2, -off);
-                  }
-                  if (AXES) x = fmaf(-sc.slope2, dist[k], x);
-                  pr[k] = ex2(x);
-                  // KEYS: pr carries 2^kUp, delta and dP its inverse
-                  const float diff = KEYS ? (F16 ? fmaf(dp, kDown, -dl[k]) : dp - dl[k]) : dp - delta;
-                  du[k] = pr[k] * diff;
-                  if (CAP) du[k] *= fmaf(-t, t, 1.f);
-                  if (edge && c * 32 + j + k >= nc) pr[k] = du[k] = 0.f;
-                }
-                if (KEYS) {
-                  pp[j / 2] = Pair<E>::pack(pr[0], pr[1]);
-                  pp[j / 2 + 1] = Pair<E>::pack(pr[2], pr[3]);
-                }
-                pd[j / 2] = Pair<E>::pack(du[0], du[1]);
-                pd[j / 2 + 1] = Pair<E>::pack(du[2], du[3]);
-              }
+              if (CAP && all_small(reinterpret_cast<const float*>(rs[i]), sc))
+                grad32<AXES, CAP, KEYS, true, E>(rs[i], rd[i], sd, c * 32, own, lse2, delta, sc, nc - c * 32, pp, pd);
+              else
+                grad32<AXES, CAP, KEYS, false, E>(rs[i], rd[i], sd, c * 32, own, lse2, delta, sc, nc - c * 32, pp, pd);
               if (KEYS) {
                 tmem_st_32x32b_x16(my + C::S_COL + c * 32, pp);
                 tmem_st_32x32b_x16(my + C::DP_COL + c * 32, pd);
@@ -356,7 +418,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p) {
         }
       }
       if (!ok) break;
-      ok = wwait(acc_full, (item - 1) & 1, limit, abort_flag, lane, err, site(KID, 0, 3), item);
+      ok = wwait_all(acc_full, (item - 1) & 1, limit, abort_flag, err, site(KID, 0, 3), item);
       if (!ok) break;
       tc_fence_after();
       if (any) {
@@ -393,19 +455,27 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p) {
 }
 
 template <int DP, typename E, bool CAP, bool KEYS>
-cudaError_t backward_axes(const Params& p, cudaStream_t st) {
+cudaError_t backward_axes(const Params& p, const Maps& maps, cudaStream_t st) {
   using C = BwdCfg<DP, KEYS>;
   const int heads = KEYS ? p.K : p.H;
   switch (p.axes) {
-    case 0: return launch_rows(attn_tc_bwd_kernel<DP, E, 0, CAP, KEYS>, C::SMEM, p, heads, st, C::THREADS);
-    case 1: return launch_rows(attn_tc_bwd_kernel<DP, E, 1, CAP, KEYS>, C::SMEM, p, heads, st, C::THREADS);
-    case 2: return launch_rows(attn_tc_bwd_kernel<DP, E, 2, CAP, KEYS>, C::SMEM, p, heads, st, C::THREADS);
-    default: return launch_rows(attn_tc_bwd_kernel<DP, E, 3, CAP, KEYS>, C::SMEM, p, heads, st, C::THREADS);
+    case 0: return launch_rows(attn_tc_bwd_kernel<DP, E, 0, CAP, KEYS>, C::SMEM, p, maps, heads, C::THREADS, st);
+    case 1: return launch_rows(attn_tc_bwd_kernel<DP, E, 1, CAP, KEYS>, C::SMEM, p, maps, heads, C::THREADS, st);
+    case 2: return launch_rows(attn_tc_bwd_kernel<DP, E, 2, CAP, KEYS>, C::SMEM, p, maps, heads, C::THREADS, st);
+    default: return launch_rows(attn_tc_bwd_kernel<DP, E, 3, CAP, KEYS>, C::SMEM, p, maps, heads, C::THREADS, st);
   }
 }
 template <int DP, typename E, bool KEYS>
 cudaError_t backward_cap(const Params& p, cudaStream_t st) {
-  return p.cap > 0.f ? backward_axes<DP, E, true, KEYS>(p, st) : backward_axes<DP, E, false, KEYS>(p, st);
+  constexpr uint32_t fmt = Pair<E>::fmt;
+  constexpr int CW = BwdCfg<DP, KEYS>::CW;
+  Maps maps;                                         // own tiles A0, A1, moving tiles X, Y
+  cudaError_t e = make_map(&maps.m[KEYS ? 2 : 0], p.q, fmt, p, p.H, p.qs, KEYS ? CW : ROWS);
+  if (e == cudaSuccess) e = make_map(&maps.m[KEYS ? 3 : 1], p.go, fmt, p, p.H, p.gos, KEYS ? CW : ROWS);
+  if (e == cudaSuccess) e = make_map(&maps.m[KEYS ? 0 : 2], p.k, fmt, p, p.K, p.ks, KEYS ? ROWS : CW);
+  if (e == cudaSuccess) e = make_map(&maps.m[KEYS ? 1 : 3], p.v, fmt, p, p.K, p.vs, KEYS ? ROWS : CW);
+  if (e != cudaSuccess) return e;
+  return p.cap > 0.f ? backward_axes<DP, E, true, KEYS>(p, maps, st) : backward_axes<DP, E, false, KEYS>(p, maps, st);
 }
 template <bool KEYS>
 cudaError_t backward_pick(const Params& p, eqlin_dtype_t dt, cudaStream_t st) {

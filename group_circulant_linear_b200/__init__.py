@@ -6,7 +6,8 @@ half spectrum and an inverse DFT, all inside hand-written CUDA kernels behind
 the C ABI declared in ``include/eqlin.h``.
 
 ``group_circulant_linear_b200.eqlin`` is the thin Python binding (argument
-marshalling only).  Importing this package does not load the CUDA library;
+marshalling only), ``ops`` the block's norm, rotary positions and attention as
+differentiable functions, ``block`` the layers.  Importing this package does not load the CUDA library;
 the binding loads it on first use and raises if it is missing.
 """
 from . import inputs, workloads  # noqa: F401  (no CUDA needed)

@@ -21,13 +21,17 @@ blocks ("Flash EQ-Linear", technical summary, sections "Implementacao" and
   shared along the group axis, attention heads split C', and GELU is
   pointwise, so the block commutes with a cyclic shift of the group axis.
   Weights are synthetic (random).
+  With ``native=True`` the norms and the attention run the library's kernels
+  too (``ops.py``), and the block takes rotary positions, capped scores, a
+  distance bias, shared key heads and packed images of different sizes.
 * ``expand_dense`` and ``DenseEQViTBlock`` -- the naive layer the pages
   compare against: the block-circulant dense matrix W_dense[d*T+s, c*T+t] =
   W[d, c, (s-t) mod T] applied with an ordinary (cuBLAS) linear.  It is
   timed beside the Flash block for context only.
 
 ``python -m group_circulant_linear_b200.block`` times one block, forward and
-forward + backward, both ways, and prints one JSON line.
+forward + backward, both ways, and prints one JSON line; ``--native`` adds the
+block with the library's norms and attention.
 """
 from __future__ import annotations
 
@@ -39,7 +43,7 @@ import torch
 import torch.nn as nn
 import torch.nn.functional as F
 
-from . import eqlin
+from . import eqlin, ops
 
 
 class EQLinearFunction(torch.autograd.Function):
@@ -145,15 +149,23 @@ class EQLinear(nn.Module):
 
 class GroupLayerNorm(nn.Module):
     """LayerNorm over all C'*T features, with one scale and shift per channel
-    c shared by its T group positions (so it commutes with a cyclic shift)."""
+    c shared by its T group positions (so it commutes with a cyclic shift).
 
-    def __init__(self, Cp: int, T: int, eps: float = 1e-6, dtype=torch.bfloat16, device="cuda"):
+    ``native`` runs the library's kernel, which also takes a residual: then
+    ``norm(x, res)`` is the pair of the normalised sum and the sum itself."""
+
+    def __init__(self, Cp: int, T: int, eps: float = 1e-6, dtype=torch.bfloat16, device="cuda", native: bool = False):
         super().__init__()
-        self.Cp, self.T, self.eps = Cp, T, eps
+        self.Cp, self.T, self.eps, self.native = Cp, T, eps, bool(native)
         self.weight = nn.Parameter(torch.ones(Cp, dtype=dtype, device=device))
         self.bias = nn.Parameter(torch.zeros(Cp, dtype=dtype, device=device))
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
+    def forward(self, x: torch.Tensor, res: torch.Tensor | None = None):
+        if self.native:
+            return ops.group_layer_norm(x, self.weight, self.bias, self.T, self.eps, res)
+        if res is not None:
+            x = x + res
+            return self.forward(x), x
         y = F.layer_norm(x, (self.Cp * self.T,), None, None, self.eps)
         y = y.view(*x.shape[:-1], self.Cp, self.T) * self.weight[:, None] + self.bias[:, None]
         return y.view(x.shape)
@@ -168,25 +180,76 @@ def _attention(h: torch.Tensor, heads: int, Cp: int, T: int) -> torch.Tensor:
 
 
 class EQViTBlock(nn.Module):
-    """Pre-norm ViT block on features [B, L, C'*T] with EQ-Linear layers."""
+    """Pre-norm ViT block on features [B, L, C'*T] with EQ-Linear layers.
+
+    The options from ``kv_heads`` on need ``native=True``:
+
+    * ``kv_heads``: key and value heads (a divisor of ``heads``), each shared
+      by heads / kv_heads query heads;
+    * ``rope_sections``: channel pairs of a head that turn with each axis of
+      the positions (``rope_base`` sets their frequencies, ``eqlin.Rope``);
+    * ``cap``: scores are capped to +-cap by a tanh (0: not);
+    * ``distance``: a bias of -slope * city-block distance between positions,
+      head h's slope being 2^(-8 (h+1) / heads).
+
+    All of them keep the block's commutation with a shift of the group axis.
+    ``forward(x, pos)`` takes positions [L, axes] (the same grid for every
+    image), [B, L, axes] or [N, axes]; ``forward(x [N, C'*T], pos, offsets,
+    max_len)`` takes packed images of different sizes (``offsets`` int32
+    [images + 1])."""
 
     def __init__(self, Cp: int, heads: int, T: int = 4, mlp_ratio: int = 4, dtype=torch.bfloat16,
-                 device="cuda", seed: int = 0):
+                 device="cuda", seed: int = 0, native: bool = False, kv_heads: int | None = None, rope_sections=None,
+                 rope_base: float = 100.0, cap: float = 0.0, distance: bool = False):
         super().__init__()
         if Cp % heads:
             raise ValueError("heads must divide C'")
+        self.kv_heads = heads if kv_heads is None else int(kv_heads)
+        if self.kv_heads < 1 or heads % self.kv_heads:
+            raise ValueError("kv_heads must divide heads")
+        if not native and (self.kv_heads != heads or rope_sections is not None or cap or distance):
+            raise ValueError("kv_heads, rope_sections, cap and distance need native=True")
         g = torch.Generator().manual_seed(seed)
-        self.Cp, self.T, self.heads = Cp, T, heads
-        self.norm1 = GroupLayerNorm(Cp, T, dtype=dtype, device=device)
-        self.qkv = EQLinear(Cp, 3 * Cp, T, dtype=dtype, device=device, generator=g)
+        self.Cp, self.T, self.heads, self.native, self.cap = Cp, T, heads, bool(native), float(cap)
+        self.rope = None if rope_sections is None else eqlin.Rope(T, Cp // heads, rope_sections, rope_base)
+        self.register_buffer("slopes", torch.tensor([2.0 ** (-8.0 * (h + 1) / heads) for h in range(heads)],
+                                                    dtype=torch.float32, device=device) if distance else None,
+                             persistent=False)
+        self.norm1 = GroupLayerNorm(Cp, T, dtype=dtype, device=device, native=native)
+        self.qkv = EQLinear(Cp, (heads + 2 * self.kv_heads) * (Cp // heads), T, dtype=dtype, device=device, generator=g)
         self.proj = EQLinear(Cp, Cp, T, dtype=dtype, device=device, generator=g)
-        self.norm2 = GroupLayerNorm(Cp, T, dtype=dtype, device=device)
+        self.norm2 = GroupLayerNorm(Cp, T, dtype=dtype, device=device, native=native)
         self.fc1 = EQLinear(Cp, mlp_ratio * Cp, T, dtype=dtype, device=device, generator=g)
         self.fc2 = EQLinear(mlp_ratio * Cp, Cp, T, dtype=dtype, device=device, generator=g)
 
-    def forward(self, x: torch.Tensor) -> torch.Tensor:
-        x = x + self.proj(_attention(self.qkv(self.norm1(x)), self.heads, self.Cp, self.T))
-        return x + self.fc2(F.gelu(self.fc1(self.norm2(x))))
+    def forward(self, x: torch.Tensor, pos: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
+                max_len: int | None = None) -> torch.Tensor:
+        if not self.native:
+            if pos is not None or offsets is not None:
+                raise ValueError("positions and packed images need native=True")
+            x = x + self.proj(_attention(self.qkv(self.norm1(x)), self.heads, self.Cp, self.T))
+            return x + self.fc2(F.gelu(self.fc1(self.norm2(x))))
+        if offsets is None and x.dim() != 3:
+            raise ValueError("x must be [B, L, C'*T], or [N, C'*T] with offsets")
+        if pos is None and (self.rope is not None or self.slopes is not None):
+            raise ValueError("rotary positions and the distance bias need pos")
+        h = self.qkv(self.norm1(x))
+        o = ops.qkv_attention(h.reshape(-1, self.heads + 2 * self.kv_heads, (self.Cp // self.heads) * self.T), self.heads,
+                              self.kv_heads, plan=self.rope, pos=pos,
+                              slopes=None if self.slopes is None else self.slopes.float(),
+                              docs=x.shape[0] if offsets is None else 1, offsets=offsets, max_len=max_len, cap=self.cap)
+        y, x = self.norm2(x, self.proj(o.reshape(x.shape)))
+        return x + self.fc2(F.gelu(self.fc1(y)))
+
+
+def grid_positions(height: int, width: int, frames: int | None = None, lead: int = 0, device="cuda") -> torch.Tensor:
+    """Positions [lead + patches, axes] of an image's patches in reading order
+    (axes: height, width) or of a clip's (frame, height, width), after ``lead``
+    tokens (class tokens, say) at the origin."""
+    dims = (height, width) if frames is None else (frames, height, width)
+    grid = torch.stack(torch.meshgrid(*(torch.arange(n, device=device) for n in dims), indexing="ij"), -1)
+    grid = grid.reshape(-1, len(dims)).float()
+    return torch.cat([torch.zeros((lead, len(dims)), device=device), grid])
 
 
 def expand_dense(W: torch.Tensor) -> torch.Tensor:
@@ -253,6 +316,7 @@ def main(argv=None):
     ap.add_argument("--dtype", default="bf16", choices=("bf16", "f16"))
     ap.add_argument("--iters", type=int, default=50)
     ap.add_argument("--warmup", type=int, default=5)
+    ap.add_argument("--native", action="store_true", help="also time the block with the library's norms and attention")
     args = ap.parse_args(argv)
     dt = {"bf16": torch.bfloat16, "f16": torch.float16}[args.dtype]
     Cp, heads = MODELS[args.model]
@@ -272,12 +336,17 @@ def main(argv=None):
 
     out = {"model": args.model, "batch": args.batch, "tokens": args.tokens, "dtype": args.dtype, "T": T,
            "C_prime": Cp, "heads": heads, "unit": "ms", "weights": "synthetic (random)"}
-    for name, m in (("flash", blk), ("dense_matrix", dense)):
+    timed = [("flash", blk), ("dense_matrix", dense)]
+    if args.native:
+        timed.append(("native", EQViTBlock(Cp, heads, T, dtype=dt, native=True)))
+    for name, m in timed:
         out[f"{name}_fwd_ms"] = _time(lambda: fwd(m), args.iters, args.warmup)
         out[f"{name}_fwd_bwd_ms"] = _time(lambda: fwd_bwd(m), args.iters, args.warmup)
     out["speedup_fwd"] = out["dense_matrix_fwd_ms"] / out["flash_fwd_ms"]
     out["speedup_fwd_bwd"] = out["dense_matrix_fwd_bwd_ms"] / out["flash_fwd_bwd_ms"]
-    for layer in (blk.qkv, blk.proj, blk.fc1, blk.fc2):
+    if args.native:
+        out["native_speedup_fwd_bwd"] = out["flash_fwd_bwd_ms"] / out["native_fwd_bwd_ms"]
+    for layer in [getattr(m, n) for _, m in timed if isinstance(m, EQViTBlock) for n in ("qkv", "proj", "fc1", "fc2")]:
         if eqlin.get_error(layer.h) != 0:
             raise RuntimeError("device-side timeout in an EQ-Linear kernel")
     print(json.dumps(out), flush=True)

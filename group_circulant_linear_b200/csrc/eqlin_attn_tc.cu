@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
   if (warp == LOAD_WARP) {
     Pending pend;
     Side<AXES, false, ROWS> sidev;
-    uint32_t item = 0;
+    uint32_t item = 0, owns = 0;
     bool ok = true;
     if (AXES) sidev.fetch(p, w.head, lo, hi, lane);
     for (int t = 0; ok && t < own_tiles; ++t) {
@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
         cp_async_commit();
         announce_later(pend, q_full);
       }
+      ++owns;
       for (int j = 0; ok && j < key_tiles; ++j) {
         const int c0 = lo + j * ROWS, nc = min(hi - c0, ROWS);
 #pragma unroll 1
@@ -159,6 +160,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
       }
     }
     announce_all(pend);
+    drain_loads(q_full, owns, kv_full, item, C::SLOTS);
     if (!ok && lane == 0) raise_abort(abort_flag, err);
   } else if (warp == MMA_WARP) {
     const uint32_t leader = lane == 0;

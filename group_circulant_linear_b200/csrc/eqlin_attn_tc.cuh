@@ -261,6 +261,16 @@ __device__ __forceinline__ bool claim(Pending& q, uint64_t* empty, uint32_t pari
   return wwait_all(empty, parity, limit, abort_flag, err, where, iter);
 }
 
+// No copy of this block may be in flight when it exits: wait for the last
+// `slots` tiles of the ring and the last own tile (long done unless a wait ran
+// out somewhere).
+__device__ __forceinline__ void drain_loads(uint64_t* own_full, uint32_t own_count, uint64_t* full, uint32_t items,
+                                            uint32_t slots) {
+  for (uint32_t k = items > slots ? items - slots : 0; k < items; ++k)
+    mbar_wait(full + k % slots, (k / slots) & 1, kDefaultWaitLimit);
+  if (own_count) mbar_wait(own_full, (own_count - 1) & 1, kDefaultWaitLimit);
+}
+
 // Scores in units of the raw product q.k (the softmax multiplies by scale2 =
 // scale log2 e): x = cap/scale tanh(raw scale/cap) - slope/scale distance.
 struct Score {

@@ -204,7 +204,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
   if (warp == LOAD) {
     Pending pend;
     Side<AXES, KEYS, CW> sides;
-    uint32_t item = 0;
+    uint32_t item = 0, owns = 0;
     bool ok = true;
     sides.fetch(p, q_head, lo, hi, lane);
     for (int t = 0; ok && t < own_tiles; ++t) {
@@ -226,6 +226,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
         cp_async_commit();
         announce_later(pend, own_full);
       }
+      ++owns;
       for (int g = 0; ok && g < passes; ++g) {
         const int64_t qh = qh0 + (int64_t)g * p.D;
         for (int j = 0; j < tiles; ++j, ++item) {
@@ -259,6 +260,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
       }
     }
     announce_all(pend);
+    drain_loads(own_full, owns, full, item, C::SLOTS);
     if (!ok && lane == 0) raise_abort(abort_flag, err);
   } else if (warp == MMA) {
     const uint32_t leader = lane == 0;

@@ -1,26 +1,34 @@
 // eqlin_attn_tc_bwd.cuh -- document attention, backward, on the tensor cores.
 //
 // Two kernels of one template.  KEYS = false owns 128 query rows and passes
-// over the keys: dq, and delta = do.o on the way.  KEYS = true owns 128 key
-// rows and passes over the queries of every head that shares them: dk, dv.
-// Both form the scores again; in exchange no sum crosses blocks, so there are
-// no atomics and results are the same in every run.  With own tiles (A0, A1) =
-// (Q, dO) or (K, V) and moving tiles (X, Y) = (K, V) or (Q, dO):
+// over the keys: dq, and delta on the way.  KEYS = true owns 128 key rows and
+// passes over the queries of every head that shares them: dk, dv.  Both form
+// the scores again; in exchange no sum crosses blocks, so there are no atomics
+// and results are the same in every run.  With own tiles (A0, A1) = (Q, dO) or
+// (K, V) and moving tiles (X, Y) = (K, V) or (Q, dO):
 //
 //   S = A0 X^T,  dP = A1 Y^T          TMEM accumulators
-//   P = 2^(s - lse),  du = P (dP - delta) (1 - tanh^2)   FP32 registers
-//   dq += du X        or       dv += P Y,  dk += du X     A from TMEM, 16 bits
+//   P = 2^(s - lse),  du = P (dP - delta) g,  g = 1 - tanh^2    FP32 registers
+//   KEYS:  dv += P Y,  dk += du X     A from TMEM, 16 bits
+//   else:  e += (P g) X,  dq += du X
 //
 // P and du are rounded to the inputs' type as operands of those products, half
 // a step each; sums are FP32 in TMEM.  In f16 P carries a factor 2^8 on its
 // way to dv, so that probabilities of long documents (1e-5 and less) stay out
 // of the subnormals.
 //
+// delta = do.o from the stored o would carry o's rounding (its own and that of
+// P in the forward) into every du; for short documents that is more than all
+// other roundings together.  It only serves as a first guess d0 here: the
+// dq kernel sums eps = sum_j P (dP - d0), so delta = d0 + eps exactly in FP32,
+// which is what the dk, dv kernel reads, and corrects its own result by
+// dq = sum du0 k - eps sum P g k.  That second product costs a quarter of the
+// kernel's MMAs; another pass for delta would cost twice that.
+//
 // A thread owns one row and 64 columns of a tile (NWG warpgroups of rows, the
-// 32-column chunks dealt out in turn).  Where TMEM allows, P and du have
-// columns of their own (SEP) and the next tile's scores are issued as soon as
-// the present ones are in registers; else they lie over the scores they came
-// from, chunk by chunk, and the SM's other block fills the gap.
+// 32-column chunks dealt out in turn).  P and du lie over the scores they came
+// from, chunk by chunk: the accumulators take the rest of the columns, and the
+// SM's other block fills the gap until the next scores.
 #pragma once
 
 #include "eqlin_attn_tc.cuh"
@@ -36,17 +44,17 @@ template <int DP, bool KEYS> struct BwdCfg {
   static constexpr int BLOCKS = DP > 64 ? 1 : 2;
   static constexpr int THREADS = NWG * 128 + 64;
   static constexpr int TMEM = DP > 64 ? 512 : 256;
-  static constexpr bool SEP = !KEYS;
-  static constexpr int S_COL = 0, DP_COL = CW, ACC0 = 2 * CW;   // dq, or dv
-  static constexpr int ACC1 = ACC0 + DP;                        // KEYS: dk;  else: du's columns
+  static constexpr int S_COL = 0, DP_COL = CW, ACC0 = 2 * CW;   // ACC0: dv, or e
+  static constexpr int ACC1 = ACC0 + DP;                        // dk, or dq
   static constexpr int OWN = DP / 64 * PANEL;                   // bytes of one own tile
   static constexpr int MOV_PANEL = CW * 128;
   static constexpr int MOV = DP / 64 * MOV_PANEL;               // bytes of one moving tile
   static constexpr int SLOTS = DP > 64 ? 2 : 4;
   static constexpr int SIDE = (kMaxAxes * ROWS + (KEYS ? 2 * ROWS : 0)) * 4;   // positions, lse, delta of a slot
-  static constexpr int NBAR = 2 + 2 * SLOTS + 5;
-  static constexpr int SMEM = 2 * OWN + SLOTS * (2 * MOV + SIDE) + NBAR * 8 + 64 + 1024;
-  static_assert(ACC1 + (KEYS ? DP : CW / 2) <= TMEM, "TMEM columns");
+  static constexpr int NBAR = 2 + 2 * SLOTS + 4;
+  static constexpr int EPS = NWG == 2 ? 2 * ROWS * 4 : 0;       // eps of the two warpgroups
+  static constexpr int SMEM = 2 * OWN + SLOTS * (2 * MOV + SIDE) + EPS + NBAR * 8 + 64 + 1024;
+  static_assert(ACC1 + DP <= TMEM, "TMEM columns");
   static_assert(BLOCKS * SMEM <= 227 * 1024, "shared memory");
 };
 
@@ -55,7 +63,8 @@ template <int DP, bool KEYS> struct BwdCfg {
 //   in base 2 and scaled), else to the row.
 template <int AXES, bool CAP, bool KEYS, bool SMALL, typename E>
 __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, const float* side, int c0, const float* own,
-                                       float lse2, float delta, const Score& sc, int left, uint32_t* pp, uint32_t* pd) {
+                                       float lse2, float delta, const Score& sc, int left, uint64_t& eps, uint32_t* pp,
+                                       uint32_t* pd) {
   constexpr bool F16 = Pair<E>::fmt == 0;
   constexpr float kDown = F16 ? 1.f / 256.f : 1.f;
   const uint64_t k2 = pk2(sc.scale2, sc.scale2), in = pk2(sc.in, sc.in), slope = pk2(-sc.slope, -sc.slope);
@@ -100,15 +109,23 @@ __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, c
       uint64_t diff;
       if (KEYS) diff = fma2(h ? dl.y : dl.x, neg, F16 ? mul2(dp, down) : dp);
       else diff = add2(dp, row_delta);
-      uint64_t du = mul2(pk2(a, b), diff);
-      if (CAP) du = mul2(du, gain);
-      float e, f;
-      unpk2(du, e, f);
       if (left < 32) {                               // the document ends inside the chunk
-        if (i >= left) a = e = 0.f;
-        if (i + 1 >= left) b = f = 0.f;
+        if (i >= left) a = 0.f;
+        if (i + 1 >= left) b = 0.f;
+        // dP is then a product with zero rows, but delta may be anything
+        float e, f;
+        unpk2(diff, e, f);
+        diff = pk2(i < left ? e : 0.f, i + 1 < left ? f : 0.f);
       }
-      if (KEYS) pp[i / 2] = Pair<E>::pack(a, b);
+      uint64_t prob = pk2(a, b);
+      if (!KEYS) eps = fma2(prob, diff, eps);
+      if (!KEYS && CAP) prob = mul2(prob, gain);     // KEYS: dv takes P itself
+      uint64_t du = mul2(prob, diff);
+      if (KEYS && CAP) du = mul2(du, gain);
+      float e, f;
+      unpk2(prob, a, b);
+      unpk2(du, e, f);
+      pp[i / 2] = Pair<E>::pack(a, b);
       pd[i / 2] = Pair<E>::pack(e, f);
     }
   }
@@ -129,14 +146,14 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
   uint8_t* ring = smem + 2 * C::OWN;
   float* side = reinterpret_cast<float*>(ring + C::SLOTS * 2 * C::MOV);
   constexpr int SIDE_F = C::SIDE / 4;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(side + C::SLOTS * SIDE_F);
+  float* eps_sum = side + C::SLOTS * SIDE_F;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(eps_sum + C::EPS / 4);
   uint64_t* own_full = bars;
   uint64_t* own_empty = bars + 1;
   uint64_t* full = bars + 2;
   uint64_t* empty = full + C::SLOTS;
   uint64_t* s_full = empty + C::SLOTS;
-  uint64_t* s_free = s_full + 1;
-  uint64_t* p_full = s_free + 1;
+  uint64_t* p_full = s_full + 1;
   uint64_t* acc_full = p_full + 1;
   uint64_t* drain = acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
@@ -179,7 +196,6 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
       mbar_init(empty + i, 1);
     }
     mbar_init(s_full, 1);
-    mbar_init(s_free, NWG * 128);
     mbar_init(p_full, NWG * 128);
     mbar_init(acc_full, 1);
     mbar_init(drain, 1);
@@ -271,7 +287,6 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
     auto scores = [&](uint32_t it, int j) -> bool {
       const int slot = it % C::SLOTS;
       if (!wwait_all(full + slot, (it / C::SLOTS) & 1, limit, abort_flag, err, site(KID, 1, 1), it)) return false;
-      if (C::SEP && !wwait_all(s_free, (it & 1) ^ 1, limit, abort_flag, err, site(KID, 1, 2), it)) return false;
       tc_fence_after();
       const uint32_t id = idesc_f16(Pair<E>::fmt, (uint32_t)((min(hi - lo - j * CW, CW) + 15) & ~15));
       const uint32_t x = smem_u32(ring + slot * 2 * C::MOV);
@@ -297,35 +312,27 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
       for (int i = 0; ok && i < all; ++i, ++item) {
         const bool more = i + 1 < all;
         const int next = j + 1 < tiles ? j + 1 : 0;
-        if (C::SEP && more) ok = scores(item + 1, next);
-        ok = ok && wwait_all(p_full, item & 1, limit, abort_flag, err, site(KID, 1, 3), item);
+        ok = wwait_all(p_full, item & 1, limit, abort_flag, err, site(KID, 1, 3), item);
         if (!ok) break;
         tc_fence_after();
         const int steps = (min(hi - lo - j * CW, CW) + 15) / 16, slot = item % C::SLOTS;
         const uint32_t x = smem_u32(ring + slot * 2 * C::MOV), y = x + C::MOV;
-        // P and du: over the scores' chunks (KEYS), or du in its own columns
-        if (KEYS) {
+        // P and du lie over the scores' chunks
+        const uint32_t b0 = KEYS ? y : x;
 #pragma unroll
-          for (int s = 0; s < CW / 16; ++s)
-            if (s < steps)
-              mma_ts(leader, tmem + C::ACC0, tmem + C::S_COL + 32 * (s >> 1) + 8 * (s & 1),
-                     smem_desc_mn(y + s * 2048, C::MOV_PANEL, 1024), id_acc, i > 0 || s > 0);
+        for (int s = 0; s < CW / 16; ++s)
+          if (s < steps)
+            mma_ts(leader, tmem + C::ACC0, tmem + C::S_COL + 32 * (s >> 1) + 8 * (s & 1),
+                   smem_desc_mn(b0 + s * 2048, C::MOV_PANEL, 1024), id_acc, i > 0 || s > 0);
 #pragma unroll
-          for (int s = 0; s < CW / 16; ++s)
-            if (s < steps)
-              mma_ts(leader, tmem + C::ACC1, tmem + C::DP_COL + 32 * (s >> 1) + 8 * (s & 1),
-                     smem_desc_mn(x + s * 2048, C::MOV_PANEL, 1024), id_acc, i > 0 || s > 0);
-        } else {
-#pragma unroll
-          for (int s = 0; s < CW / 16; ++s)
-            if (s < steps)
-              mma_ts(leader, tmem + C::ACC0, tmem + C::ACC1 + s * 8, smem_desc_mn(x + s * 2048, C::MOV_PANEL, 1024),
-                     id_acc, i > 0 || s > 0);
-        }
+        for (int s = 0; s < CW / 16; ++s)
+          if (s < steps)
+            mma_ts(leader, tmem + C::ACC1, tmem + C::DP_COL + 32 * (s >> 1) + 8 * (s & 1),
+                   smem_desc_mn(x + s * 2048, C::MOV_PANEL, 1024), id_acc, i > 0 || s > 0);
         commit(leader, acc_full);
         commit(leader, empty + slot);
         if (!more) commit(leader, own_empty);
-        if (!C::SEP && more) ok = scores(item + 1, next);
+        if (more) ok = scores(item + 1, next);   // in order behind the products that read P and du
         j = next;
       }
     }
@@ -357,8 +364,8 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
           for (int k = 0; k < 8; ++k) delta = fmaf(Elem<E>::to_f(x[k]), Elem<E>::to_f(y[k]), delta);
         }
         lse2 = p.lse[(int64_t)w.head * p.N + row] * kLog2e;
-        if (wg == 0) p.delta[(int64_t)w.head * p.N + row] = delta;
       }
+      uint64_t eps2 = 0;
       for (int g = 0; ok && g < passes; ++g) {
         const Score sc = score_of(p, q_head + g);
         for (int j = 0; j < tiles; ++j, ++item) {
@@ -386,15 +393,6 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
               tie32(rd[i]);
             }
           }
-          if (C::SEP) {
-            tc_fence_before();
-            mbar_arrive(s_free);
-            if (item > 0) {                          // du's columns are free once the last product is done
-              ok = wwait_all(acc_full, (item - 1) & 1, limit, abort_flag, err, site(KID, 0, 2), item);
-              if (!ok) break;
-              tc_fence_after();
-            }
-          }
           if (any) {
             const float* sd = side + slot * SIDE_F;
 #pragma unroll
@@ -403,15 +401,11 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
               if (c * 32 >= nc) continue;
               uint32_t pp[16], pd[16];
               if (CAP && all_small(reinterpret_cast<const float*>(rs[i]), sc))
-                grad32<AXES, CAP, KEYS, true, E>(rs[i], rd[i], sd, c * 32, own, lse2, delta, sc, nc - c * 32, pp, pd);
+                grad32<AXES, CAP, KEYS, true, E>(rs[i], rd[i], sd, c * 32, own, lse2, delta, sc, nc - c * 32, eps2, pp, pd);
               else
-                grad32<AXES, CAP, KEYS, false, E>(rs[i], rd[i], sd, c * 32, own, lse2, delta, sc, nc - c * 32, pp, pd);
-              if (KEYS) {
-                tmem_st_32x32b_x16(my + C::S_COL + c * 32, pp);
-                tmem_st_32x32b_x16(my + C::DP_COL + c * 32, pd);
-              } else {
-                tmem_st_32x32b_x16(my + C::ACC1 + c * 16, pd);
-              }
+                grad32<AXES, CAP, KEYS, false, E>(rs[i], rd[i], sd, c * 32, own, lse2, delta, sc, nc - c * 32, eps2, pp, pd);
+              tmem_st_32x32b_x16(my + C::S_COL + c * 32, pp);
+              tmem_st_32x32b_x16(my + C::DP_COL + c * 32, pd);
             }
             tmem_wait_st();
           }
@@ -423,25 +417,51 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
       ok = wwait_all(acc_full, (item - 1) & 1, limit, abort_flag, err, site(KID, 0, 3), item);
       if (!ok) break;
       tc_fence_after();
+      float eps = 0.f;
+      if (!KEYS) {
+        float a, b;
+        unpk2(eps2, a, b);
+        eps = a + b;
+        if (NWG == 2) {                              // the two halves of the row's columns
+          eps_sum[wg * ROWS + quarter * 32 + lane] = eps;
+          named_bar_sync(1, NWG * 128);
+          eps = eps_sum[quarter * 32 + lane] + eps_sum[ROWS + quarter * 32 + lane];
+          named_bar_sync(1, NWG * 128);
+        }
+        if (live && wg == 0) p.delta[(int64_t)w.head * p.N + row] = delta + eps;
+      }
       if (any) {
 #pragma unroll
-        for (int which = 0; which < (KEYS ? 2 : 1); ++which) {
-          const float mul = KEYS && which == 0 ? kDown : p.scale;
-          E* out = KEYS ? (which == 0 ? static_cast<E*>(p.dv) + row * p.dvs + kh : static_cast<E*>(p.dk) + row * p.dks + kh)
-                        : static_cast<E*>(p.dq) + row * p.dqs + qh0;
+        for (int c = 0; c < DP / 16; ++c) {
+          if (c >= d16 || c % NWG != wg) continue;
+          uint32_t x[16], y[16];
+          tmem_ld_32x32b_x16(my + C::ACC0 + c * 16, x);
+          tmem_ld_32x32b_x16(my + C::ACC1 + c * 16, y);
+          tmem_wait_ld();
+          tie16(x);
+          tie16(y);
+          uint32_t px[8], py[8];
 #pragma unroll
-          for (int c = 0; c < DP / 16; ++c) {
-            if (c >= d16 || c % NWG != wg) continue;
-            uint32_t o[16], pk[8];
-            tmem_ld_32x32b_x16(my + (which ? C::ACC1 : C::ACC0) + c * 16, o);
-            tmem_wait_ld();
-            tie16(o);
-#pragma unroll
-            for (int i = 0; i < 16; i += 2)
-              pk[i / 2] = Pair<E>::pack(__uint_as_float(o[i]) * mul, __uint_as_float(o[i + 1]) * mul);
-            if (live) {
-              *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-              if (c * 16 + 8 < p.D) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
+          for (int i = 0; i < 16; i += 2) {
+            const float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
+            float y0 = __uint_as_float(y[i]), y1 = __uint_as_float(y[i + 1]);
+            if (KEYS) {
+              px[i / 2] = Pair<E>::pack(x0 * kDown, x1 * kDown);
+            } else {
+              y0 = fmaf(-eps, x0, y0);
+              y1 = fmaf(-eps, x1, y1);
+            }
+            py[i / 2] = Pair<E>::pack(y0 * p.scale, y1 * p.scale);
+          }
+          if (live) {
+            E* out = KEYS ? static_cast<E*>(p.dk) + row * p.dks + kh : static_cast<E*>(p.dq) + row * p.dqs + qh0;
+            const bool second = c * 16 + 8 < p.D;
+            *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(py[0], py[1], py[2], py[3]);
+            if (second) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(py[4], py[5], py[6], py[7]);
+            if (KEYS) {
+              out = static_cast<E*>(p.dv) + row * p.dvs + kh;
+              *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(px[0], px[1], px[2], px[3]);
+              if (second) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(px[4], px[5], px[6], px[7]);
             }
           }
         }

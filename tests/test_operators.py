@@ -282,8 +282,14 @@ def attention_bounds(q, k, v, go, lens, lead, cap, pos, slopes, scale, dt, p16):
             dP = G @ V.T
             delta = (G * o).sum(1, keepdim=True)
             du = P * (dP - delta) * slope
-            edelta = (G.abs() * tol["o"][r, h]).sum(1, keepdim=True) + D * W * (G * o).abs().sum(1, keepdim=True)
             edp = D * W * G.abs() @ V.abs().T
+            # delta: the FP32 sum of P dP; and in dq the correction by eps = delta - do.o as stored, whose
+            # product passes through 16 bits
+            eps = (G.abs() * tol["o"][r, h]).sum(1, keepdim=True) + D * W * (G * o).abs().sum(1, keepdim=True)
+            edelta = (eta * P * dP.abs() + P * edp + (n + 8) * W * P * (dP.abs() + delta.abs())).sum(1, keepdim=True) \
+                + (up + eta + n * W) * eps
+            if not p16:
+                edelta = edelta + eps                              # the CUDA-core kernel takes do.o itself
             # 1 - tanh^2 to a few 2^-24 absolute, and its argument's error
             eslope = (8 * W + 2 * (D + 4) * W * mag / cap) if cap else torch.zeros_like(uu)
             edu = P * slope * (eta * (dP - delta).abs() + edelta + edp + 4 * W * (dP.abs() + delta.abs())) \

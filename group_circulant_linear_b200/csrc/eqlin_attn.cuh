@@ -45,23 +45,23 @@ struct Params {
   const float* slopes;    // [H]
   int axes;               // 0: no bias
   int H, K, D;
-  int hint;               // blocks per (document, head); each walks the tiles hint apart
+  int hint;               // work items per (document, head); each walks the tiles hint apart
+  uint32_t items;         // work items in all
   float scale, cap;
   int* err;               // error record (eqlin_wait.cuh), or null
   uint32_t wait_limit;
 };
 
-// The block's document, head and first tile: tiles vary fastest, so that
+// A work item's document, head and first tile: tiles vary fastest, so that
 // blocks which share keys run together.
 struct Work {
   int64_t doc;
   int head, tile;
 };
-__device__ __forceinline__ Work work_of(const Params& p, int heads) {
-  const uint32_t b = blockIdx.x;
-  const uint32_t rest = b / (uint32_t)p.hint;
+__device__ __forceinline__ Work work_of(const Params& p, uint32_t item, int heads) {
+  const uint32_t rest = item / (uint32_t)p.hint;
   Work w;
-  w.tile = (int)(b - rest * (uint32_t)p.hint);
+  w.tile = (int)(item - rest * (uint32_t)p.hint);
   const uint32_t d = rest / (uint32_t)heads;
   w.head = (int)(rest - d * (uint32_t)heads);
   w.doc = d;
@@ -80,7 +80,7 @@ __device__ __forceinline__ void doc_range(const Params& p, int64_t doc, int64_t&
   hi = min(max((int64_t)p.offsets[doc + 1], lo), p.N);
 }
 
-// Blocks whose document index is `docs` (packed calls only) clear the rows
+// Items whose document index is `docs` (packed calls only) clear the rows
 // outside all documents: [0, first offset) and [last offset, N).
 template <typename F>
 __device__ __forceinline__ void outside_rows(const Params& p, int tile, F&& clear) {

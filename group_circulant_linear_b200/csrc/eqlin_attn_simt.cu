@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_co
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   grid_dep_launch();
   grid_dep_wait();
-  const Work w = work_of(p, p.H);
+  const Work w = work_of(p, blockIdx.x, p.H);
   const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)(w.head / (p.H / p.K)) * p.D;
   if (w.doc == p.docs) {
     outside_rows(p, w.tile, [&](int64_t r) {
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const __grid_con
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   grid_dep_launch();
   grid_dep_wait();
-  const Work w = work_of(p, p.H);
+  const Work w = work_of(p, blockIdx.x, p.H);
   const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)(w.head / (p.H / p.K)) * p.D;
   if (w.doc == p.docs) {
     outside_rows(p, w.tile, [&](int64_t r) { clear_row<E>(p.dq, p.dqs, qh, r, p.D); });
@@ -357,7 +357,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const __grid_co
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   grid_dep_launch();
   grid_dep_wait();
-  const Work w = work_of(p, p.K);
+  const Work w = work_of(p, blockIdx.x, p.K);
   const int rep = p.H / p.K;
   const int64_t kh = (int64_t)w.head * p.D;
   if (w.doc == p.docs) {
@@ -442,8 +442,9 @@ cudaError_t run(void (*k)(Params), int smem, Params p, int heads, cudaStream_t s
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
   const int64_t room = 0x7fffffff / items;
   p.hint = (int)(tiles < room ? tiles : room);
+  p.items = (uint32_t)(items * p.hint);
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(k), smem);
-  if (e == cudaSuccess) e = launch_pdl(k, dim3((unsigned)(items * p.hint)), dim3(kThreads), (size_t)smem, st, p);
+  if (e == cudaSuccess) e = launch_pdl(k, dim3(p.items), dim3(kThreads), (size_t)smem, st, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

@@ -57,24 +57,19 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
-  const Work w = work_of(p, p.H);
-  const int kv_head = w.head / (p.H / p.K);
-  const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)kv_head * p.D;
-  if (w.doc == p.docs) {
-    outside_rows(p, w.tile, [&](int64_t r) {
-      for (int d = threadIdx.x; d < p.D; d += kThreads) static_cast<E*>(p.o)[r * p.os + qh + d] = Elem<E>::from_f(0.f);
-      if (threadIdx.x == 0) p.lse[(int64_t)w.head * p.N + r] = 0.f;
-    });
-    return;
+  if (p.offsets) {                                            // one item per block: it may have nothing to do
+    const Work w = work_of(p, blockIdx.x, p.H);
+    if (w.doc == p.docs) {
+      const int64_t qh = (int64_t)w.head * p.D;
+      outside_rows(p, w.tile, [&](int64_t r) {
+        for (int d = threadIdx.x; d < p.D; d += kThreads) static_cast<E*>(p.o)[r * p.os + qh + d] = Elem<E>::from_f(0.f);
+        if (threadIdx.x == 0) p.lse[(int64_t)w.head * p.N + r] = 0.f;
+      });
+      return;
+    }
+    if (item_of<false>(p, blockIdx.x, p.H).tiles == 0) return;
   }
-  int64_t lo64, hi64;
-  doc_range(p, w.doc, lo64, hi64);
-  if (lo64 + (int64_t)w.tile * ROWS >= hi64) return;
-  const int lo = (int)uniform((uint32_t)lo64), hi = (int)uniform((uint32_t)hi64);
-  const int first = lo + w.tile * ROWS;
-  // tokens are below 2^31, a tile's end may not be: loops count tiles
-  const int own_tiles = (int)(((int64_t)(hi - first) + (int64_t)p.hint * ROWS - 1) / ((int64_t)p.hint * ROWS));
-  const int key_tiles = (hi - lo - 1) / ROWS + 1;
+  const int rep = p.H / p.K;
 
   if (threadIdx.x == 0) {
     mbar_init(q_full, 32);
@@ -113,48 +108,53 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
     Side<AXES, false, ROWS> sidev;
     uint32_t item = 0, owns = 0;
     bool ok = true;
-    if (AXES) sidev.fetch(p, w.head, lo, hi, lane);
-    for (int t = 0; ok && t < own_tiles; ++t) {
-      const int r0 = first + t * p.hint * ROWS;
-      ok = claim(pend, q_empty, (t & 1) ^ 1, limit, abort_flag, err, site(K_ATTN_FWD, 2, 0), t);
-      if (!ok) break;
-      if (hi - r0 >= ROWS) {
-        if (lane == 0) {
-          expect_bytes(q_full, C::TILE);
-          tma_rows<DP, ROWS>(smem, &maps.m[0], w.head, r0, q_full);
+    for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
+      const Item w = item_of<false>(p, work, p.H);
+      const int lo = w.lo, hi = w.hi, kv_head = w.head / rep, key_tiles = (hi - lo - 1) / ROWS + 1;
+      const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)kv_head * p.D;
+      if (AXES) sidev.fetch(p, w.head, lo, hi, lane);
+      for (int t = 0; ok && t < w.tiles; ++t) {
+        const int r0 = w.first + t * p.hint * ROWS;
+        ok = claim(pend, q_empty, (owns & 1) ^ 1, limit, abort_flag, err, site(K_ATTN_FWD, 2, 0), owns);
+        if (!ok) break;
+        if (hi - r0 >= ROWS) {
+          if (lane == 0) {
+            expect_bytes(q_full, C::TILE);
+            tma_rows<DP, ROWS>(smem, &maps.m[0], w.head, r0, q_full);
+          }
+          mbar_arrive(q_full);
+        } else {
+          load_rows<DP, E>(smem_u32(smem), p.q, p.qs, qh, r0, hi, ROWS, p.D, 2 * d16, lane);
+          cp_async_commit();
+          announce_later(pend, q_full);
         }
-        mbar_arrive(q_full);
-      } else {
-        load_rows<DP, E>(smem_u32(smem), p.q, p.qs, qh, r0, hi, ROWS, p.D, 2 * d16, lane);
-        cp_async_commit();
-        announce_later(pend, q_full);
-      }
-      ++owns;
-      for (int j = 0; ok && j < key_tiles; ++j) {
-        const int c0 = lo + j * ROWS, nc = min(hi - c0, ROWS);
+        ++owns;
+        for (int j = 0; ok && j < key_tiles; ++j) {
+          const int c0 = lo + j * ROWS, nc = min(hi - c0, ROWS);
 #pragma unroll 1
-        for (int kv = 0; kv < 2; ++kv, ++item) {
-          const int slot = item % C::SLOTS;
-          ok = claim(pend, kv_empty + slot, ((item / C::SLOTS) & 1) ^ 1, limit, abort_flag, err, site(K_ATTN_FWD, 2, 1),
-                     item);
-          if (!ok) break;
-          uint8_t* to = ring + slot * C::TILE;
-          if (nc == ROWS && lane == 0) {
-            expect_bytes(kv_full + slot, C::TILE);
-            tma_rows<DP, ROWS>(to, &maps.m[1 + kv], kv_head, c0, kv_full + slot);
-          }
-          // positions go with V: its slot is free once the softmax has used them
-          if (AXES && kv) {
-            sidev.store(spos + (slot >> 1) * kMaxAxes * ROWS, 0.f, 0.f, lane);
-            sidev.fetch(p, w.head, j + 1 < key_tiles ? c0 + ROWS : lo, hi, lane);
-          }
-          if (nc == ROWS) {
-            mbar_arrive(kv_full + slot);
-          } else {
-            load_rows<DP, E>(smem_u32(to), kv ? p.v : p.k, kv ? p.vs : p.ks, kh, c0, hi, (nc + 15) & ~15, p.D, 2 * d16,
-                             lane);
-            cp_async_commit();
-            announce_later(pend, kv_full + slot);
+          for (int kv = 0; kv < 2; ++kv, ++item) {
+            const int slot = item % C::SLOTS;
+            ok = claim(pend, kv_empty + slot, ((item / C::SLOTS) & 1) ^ 1, limit, abort_flag, err, site(K_ATTN_FWD, 2, 1),
+                       item);
+            if (!ok) break;
+            uint8_t* to = ring + slot * C::TILE;
+            if (nc == ROWS && lane == 0) {
+              expect_bytes(kv_full + slot, C::TILE);
+              tma_rows<DP, ROWS>(to, &maps.m[1 + kv], kv_head, c0, kv_full + slot);
+            }
+            // positions go with V: its slot is free once the softmax has used them
+            if (AXES && kv) {
+              sidev.store(spos + (slot >> 1) * kMaxAxes * ROWS, 0.f, 0.f, lane);
+              if (j + 1 < key_tiles || t + 1 < w.tiles) sidev.fetch(p, w.head, j + 1 < key_tiles ? c0 + ROWS : lo, hi, lane);
+            }
+            if (nc == ROWS) {
+              mbar_arrive(kv_full + slot);
+            } else {
+              load_rows<DP, E>(smem_u32(to), kv ? p.v : p.k, kv ? p.vs : p.ks, kh, c0, hi, (nc + 15) & ~15, p.D, 2 * d16,
+                               lane);
+              cp_async_commit();
+              announce_later(pend, kv_full + slot);
+            }
           }
         }
       }
@@ -164,8 +164,9 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
     if (!ok && lane == 0) raise_abort(abort_flag, err);
   } else if (warp == MMA_WARP) {
     const uint32_t leader = lane == 0;
-    uint32_t item = 0, step = 0;                              // step: key tiles since the start
+    uint32_t item = 0, step = 0, owns = 0;                    // step: key tiles since the start
     bool ok = true;
+    int lo = 0, hi = 0;
     const uint32_t q_addr = smem_u32(smem);
     const uint32_t id_o = idesc_f16(Pair<E>::fmt, (uint32_t)(16 * d16)) | kBTransposed;
     // scores of key tile j, step n, whose K is item `it`
@@ -188,29 +189,35 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
       commit(leader, kv_empty + slot);
       return true;
     };
-    for (int t = 0; ok && t < own_tiles; ++t) {
-      ok = wwait_all(q_full, t & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 0), t) && qk(0, item, step);
-      for (int j = 0; ok && j < key_tiles; ++j, item += 2, ++step) {
-        const bool more = j + 1 < key_tiles;
-        if (!C::OVER && more) ok = qk(j + 1, item + 2, step + 1);
-        if (!C::OVER && !more) commit(leader, q_empty);
-        const uint32_t vi = item + 1;
-        const int slot = vi % C::SLOTS;
-        ok = ok && wwait_all(kv_full + slot, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 1), vi) &&
-             wwait_all(p_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 3), step);
-        if (!ok) break;
-        tc_fence_after();
-        const int steps = (min(hi - lo - j * ROWS, ROWS) + 15) / 16;
-        const uint32_t v_addr = smem_u32(ring + slot * C::TILE);
+    for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
+      const Item w = item_of<true>(p, work, p.H);
+      lo = w.lo;
+      hi = w.hi;
+      const int key_tiles = (hi - lo - 1) / ROWS + 1;
+      for (int t = 0; ok && t < w.tiles; ++t, ++owns) {
+        ok = wwait_all(q_full, owns & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 0), owns) && qk(0, item, step);
+        for (int j = 0; ok && j < key_tiles; ++j, item += 2, ++step) {
+          const bool more = j + 1 < key_tiles;
+          if (!C::OVER && more) ok = qk(j + 1, item + 2, step + 1);
+          if (!C::OVER && !more) commit(leader, q_empty);
+          const uint32_t vi = item + 1;
+          const int slot = vi % C::SLOTS;
+          ok = ok && wwait_all(kv_full + slot, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 1), vi) &&
+               wwait_all(p_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 3), step);
+          if (!ok) break;
+          tc_fence_after();
+          const int steps = (min(hi - lo - j * ROWS, ROWS) + 15) / 16;
+          const uint32_t v_addr = smem_u32(ring + slot * C::TILE);
 #pragma unroll
-        for (int s = 0; s < ROWS / 16; ++s)
-          if (s < steps)
-            mma_ts(leader, tmem + C::O_COL, tmem + C::P_COL + s * 8, smem_desc_mn(v_addr + s * 2048, PANEL, 1024), id_o,
-                   j > 0 || s > 0);
-        commit(leader, o_full);
-        commit(leader, kv_empty + slot);
-        if (C::OVER && more) ok = qk(j + 1, item + 2, step + 1);
-        if (C::OVER && !more) commit(leader, q_empty);
+          for (int s = 0; s < ROWS / 16; ++s)
+            if (s < steps)
+              mma_ts(leader, tmem + C::O_COL, tmem + C::P_COL + s * 8, smem_desc_mn(v_addr + s * 2048, PANEL, 1024), id_o,
+                     j > 0 || s > 0);
+          commit(leader, o_full);
+          commit(leader, kv_empty + slot);
+          if (C::OVER && more) ok = qk(j + 1, item + 2, step + 1);
+          if (C::OVER && !more) commit(leader, q_empty);
+        }
       }
     }
     if (!ok && lane == 0) raise_abort(abort_flag, err);
@@ -219,145 +226,150 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
     __syncwarp();
   } else {
     const uint32_t my = tmem + ((uint32_t)(warp * 32) << 16);
-    const Score sc = score_of(p, w.head);
     uint32_t step = 0;
     bool ok = true;
-    for (int t = 0; ok && t < own_tiles; ++t) {
-      const int r0 = first + t * p.hint * ROWS + warp * 32;   // the warp's first row
-      const bool any = r0 < hi, live = lane < hi - r0;
-      const int64_t row = (int64_t)r0 + lane;
-      float own[AXES ? AXES : 1];
+    for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
+      const Item w = item_of<false>(p, work, p.H);
+      const int lo = w.lo, hi = w.hi, key_tiles = (hi - lo - 1) / ROWS + 1;
+      const int64_t qh = (int64_t)w.head * p.D;
+      const Score sc = score_of(p, w.head);
+      for (int t = 0; ok && t < w.tiles; ++t) {
+        const int r0 = w.first + t * p.hint * ROWS + warp * 32;   // the warp's first row
+        const bool any = r0 < hi, live = lane < hi - r0;
+        const int64_t row = (int64_t)r0 + lane;
+        float own[AXES ? AXES : 1];
 #pragma unroll
-      for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
-      float m = -INFINITY, l = 0.f;                           // m in base-2 units
-      for (int j = 0; j < key_tiles; ++j, ++step) {
-        const int nc = min(hi - lo - j * ROWS, ROWS);
-        ok = wwait_all(s_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 0), step);
-        if (AXES && ok) {
-          const uint32_t vi = 2 * step + 1;
-          ok = wwait_all(kv_full + vi % C::SLOTS, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 1), step);
-        }
-        if (!ok) break;
-        tc_fence_after();
-        uint32_t raw[ROWS];
-        float* s = reinterpret_cast<float*>(raw);
-        if (any) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (c * 32 < nc) tmem_ld32(my + c * 32, raw + c * 32);
-          tmem_wait_ld();
-#pragma unroll
-          for (int c = 0; c < 4; ++c) tie32(raw + c * 32);
-        }
-        if (!C::OVER) {
-          tc_fence_before();
-          mbar_arrive(s_free);
-        }
-        float top = -INFINITY;
-        if (any) {
-          const float* pos = spos + (((2 * step + 1) % C::SLOTS) >> 1) * kMaxAxes * ROWS;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c * 32 >= nc) continue;
-            transform32<AXES, CAP>(s + c * 32, pos, c * 32, own, sc);
-            if (c * 32 + 32 > nc) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (c * 32 + i >= nc) s[c * 32 + i] = -INFINITY;
-            }
-            float t0 = top, t1 = s[c * 32];
-#pragma unroll
-            for (int i = 1; i < 31; i += 3) {                 // three-way maxima, two chains
-              t0 = fmaxf(fmaxf(t0, s[c * 32 + i]), s[c * 32 + i + 1]);
-              t1 = fmaxf(t1, s[c * 32 + i + 2]);
-            }
-            top = fmaxf(fmaxf(t0, t1), s[c * 32 + 31]);
+        for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
+        float m = -INFINITY, l = 0.f;                           // m in base-2 units
+        for (int j = 0; j < key_tiles; ++j, ++step) {
+          const int nc = min(hi - lo - j * ROWS, ROWS);
+          ok = wwait_all(s_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 0), step);
+          if (AXES && ok) {
+            const uint32_t vi = 2 * step + 1;
+            ok = wwait_all(kv_full + vi % C::SLOTS, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 1), step);
           }
-          top *= sc.scale2;                                   // scale > 0
-        }
-        // P's columns, and O, are free once the previous product is done
-        if (j > 0) {
-          ok = wwait_all(o_full, (step - 1) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 2), step);
           if (!ok) break;
           tc_fence_after();
-          const bool grow = top > m + kLag;
-          if (__any_sync(0xffffffffu, grow)) {
-            const float fix = grow ? ex2(m - top) : 1.f;
-            l *= fix;
-            if (grow) m = top;
+          uint32_t raw[ROWS];
+          float* s = reinterpret_cast<float*>(raw);
+          if (any) {
 #pragma unroll
-            for (int c = 0; c < DP / 16; ++c) {
-              if (c >= d16) continue;
-              uint32_t o[16];
-              tmem_ld_32x32b_x16(my + C::O_COL + c * 16, o);
-              tmem_wait_ld();
-              tie16(o);
+            for (int c = 0; c < 4; ++c)
+              if (c * 32 < nc) tmem_ld32(my + c * 32, raw + c * 32);
+            tmem_wait_ld();
 #pragma unroll
-              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
-              tmem_st_32x32b_x16(my + C::O_COL + c * 16, o);
+            for (int c = 0; c < 4; ++c) tie32(raw + c * 32);
+          }
+          if (!C::OVER) {
+            tc_fence_before();
+            mbar_arrive(s_free);
+          }
+          float top = -INFINITY;
+          if (any) {
+            const float* pos = spos + (((2 * step + 1) % C::SLOTS) >> 1) * kMaxAxes * ROWS;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (c * 32 >= nc) continue;
+              transform32<AXES, CAP>(s + c * 32, pos, c * 32, own, sc);
+              if (c * 32 + 32 > nc) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (c * 32 + i >= nc) s[c * 32 + i] = -INFINITY;
+              }
+              float t0 = top, t1 = s[c * 32];
+#pragma unroll
+              for (int i = 1; i < 31; i += 3) {                 // three-way maxima, two chains
+                t0 = fmaxf(fmaxf(t0, s[c * 32 + i]), s[c * 32 + i + 1]);
+                t1 = fmaxf(t1, s[c * 32 + i + 2]);
+              }
+              top = fmaxf(fmaxf(t0, t1), s[c * 32 + 31]);
             }
+            top *= sc.scale2;                                   // scale > 0
+          }
+          // P's columns, and O, are free once the previous product is done
+          if (j > 0) {
+            ok = wwait_all(o_full, (step - 1) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 2), step);
+            if (!ok) break;
+            tc_fence_after();
+            const bool grow = top > m + kLag;
+            if (__any_sync(0xffffffffu, grow)) {
+              const float fix = grow ? ex2(m - top) : 1.f;
+              l *= fix;
+              if (grow) m = top;
+#pragma unroll
+              for (int c = 0; c < DP / 16; ++c) {
+                if (c >= d16) continue;
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(my + C::O_COL + c * 16, o);
+                tmem_wait_ld();
+                tie16(o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+                tmem_st_32x32b_x16(my + C::O_COL + c * 16, o);
+              }
+              tmem_wait_st();
+            }
+          } else {
+            m = top;
+          }
+          if (any) {
+            const uint64_t k2 = pk2(sc.scale2, sc.scale2), off = pk2(-m, -m);
+            uint64_t l0 = 0, l1 = 0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              if (c * 32 >= nc) continue;
+              uint32_t pk[16];
+#pragma unroll
+              for (int i = 0; i < 32; i += 4) {
+                float a, b, d, e;
+                unpk2(fma2(pk2(s[c * 32 + i], s[c * 32 + i + 1]), k2, off), a, b);
+                unpk2(fma2(pk2(s[c * 32 + i + 2], s[c * 32 + i + 3]), k2, off), d, e);
+                a = ex2(a);
+                b = ex2(b);
+                d = ex2(d);
+                e = ex2(e);
+                l0 = add2(l0, pk2(a, b));
+                l1 = add2(l1, pk2(d, e));
+                pk[i / 2] = Pair<E>::pack(a, b);
+                pk[i / 2 + 1] = Pair<E>::pack(d, e);
+              }
+              tmem_st_32x32b_x16(my + C::P_COL + c * 16, pk);
+            }
+            float a, b;
+            unpk2(add2(l0, l1), a, b);
+            l += a + b;
             tmem_wait_st();
           }
-        } else {
-          m = top;
+          tc_fence_before();
+          mbar_arrive(p_full);
         }
+        if (!ok) break;
+        ok = wwait_all(o_full, (step - 1) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 3), step);
+        if (!ok) break;
+        tc_fence_after();
         if (any) {
-          const uint64_t k2 = pk2(sc.scale2, sc.scale2), off = pk2(-m, -m);
-          uint64_t l0 = 0, l1 = 0;
+          const float inv = 1.f / l;
+          E* out = static_cast<E*>(p.o) + row * p.os + qh;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c * 32 >= nc) continue;
-            uint32_t pk[16];
+          for (int c = 0; c < DP / 16; ++c) {
+            if (c >= d16) continue;
+            uint32_t o[16];
+            tmem_ld_32x32b_x16(my + C::O_COL + c * 16, o);
+            tmem_wait_ld();
+            tie16(o);
+            uint32_t pk[8];
 #pragma unroll
-            for (int i = 0; i < 32; i += 4) {
-              float a, b, d, e;
-              unpk2(fma2(pk2(s[c * 32 + i], s[c * 32 + i + 1]), k2, off), a, b);
-              unpk2(fma2(pk2(s[c * 32 + i + 2], s[c * 32 + i + 3]), k2, off), d, e);
-              a = ex2(a);
-              b = ex2(b);
-              d = ex2(d);
-              e = ex2(e);
-              l0 = add2(l0, pk2(a, b));
-              l1 = add2(l1, pk2(d, e));
-              pk[i / 2] = Pair<E>::pack(a, b);
-              pk[i / 2 + 1] = Pair<E>::pack(d, e);
+            for (int i = 0; i < 16; i += 2)
+              pk[i / 2] = Pair<E>::pack(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+            if (live) {
+              *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+              if (c * 16 + 8 < p.D) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
             }
-            tmem_st_32x32b_x16(my + C::P_COL + c * 16, pk);
           }
-          float a, b;
-          unpk2(add2(l0, l1), a, b);
-          l += a + b;
-          tmem_wait_st();
+          if (live) p.lse[(int64_t)w.head * p.N + row] = (m + log2f(l)) * kLn2;
         }
         tc_fence_before();
-        mbar_arrive(p_full);
       }
-      if (!ok) break;
-      ok = wwait_all(o_full, (step - 1) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 3), step);
-      if (!ok) break;
-      tc_fence_after();
-      if (any) {
-        const float inv = 1.f / l;
-        E* out = static_cast<E*>(p.o) + row * p.os + qh;
-#pragma unroll
-        for (int c = 0; c < DP / 16; ++c) {
-          if (c >= d16) continue;
-          uint32_t o[16];
-          tmem_ld_32x32b_x16(my + C::O_COL + c * 16, o);
-          tmem_wait_ld();
-          tie16(o);
-          uint32_t pk[8];
-#pragma unroll
-          for (int i = 0; i < 16; i += 2)
-            pk[i / 2] = Pair<E>::pack(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-          if (live) {
-            *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-            if (c * 16 + 8 < p.D) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-          }
-        }
-        if (live) p.lse[(int64_t)w.head * p.N + row] = (m + log2f(l)) * kLn2;
-      }
-      tc_fence_before();
     }
     if (!ok && lane == 0) raise_abort(abort_flag, err);
   }
@@ -371,10 +383,10 @@ template <int DP, typename E, bool CAP>
 cudaError_t forward_axes(const Params& p, const Maps& maps, cudaStream_t st) {
   constexpr int smem = FwdCfg<DP>::SMEM;
   switch (p.axes) {
-    case 0: return launch_rows(attn_tc_fwd_kernel<DP, E, 0, CAP>, smem, p, maps, p.H, kThreads, st);
-    case 1: return launch_rows(attn_tc_fwd_kernel<DP, E, 1, CAP>, smem, p, maps, p.H, kThreads, st);
-    case 2: return launch_rows(attn_tc_fwd_kernel<DP, E, 2, CAP>, smem, p, maps, p.H, kThreads, st);
-    default: return launch_rows(attn_tc_fwd_kernel<DP, E, 3, CAP>, smem, p, maps, p.H, kThreads, st);
+    case 0: return launch_rows(attn_tc_fwd_kernel<DP, E, 0, CAP>, smem, p, maps, p.H, kThreads, 2, st);
+    case 1: return launch_rows(attn_tc_fwd_kernel<DP, E, 1, CAP>, smem, p, maps, p.H, kThreads, 2, st);
+    case 2: return launch_rows(attn_tc_fwd_kernel<DP, E, 2, CAP>, smem, p, maps, p.H, kThreads, 2, st);
+    default: return launch_rows(attn_tc_fwd_kernel<DP, E, 3, CAP>, smem, p, maps, p.H, kThreads, 2, st);
   }
 }
 template <int DP, typename E>

@@ -204,7 +204,7 @@ template <int AXES, bool STAT, int TILE_ROWS> struct Side {
 #pragma unroll
       for (int a = 0; a < AXES; ++a) pos[a * R + i] = on ? p.pos[(int64_t)r * AXES + a] : 0.f;
       if (STAT) {
-        lse[i] = on ? p.lse[(int64_t)head * p.N + r] : 0.f;
+        lse[i] = on ? p.lse[(int64_t)head * p.N + r] : INFINITY;
         delta[i] = on ? p.delta[(int64_t)head * p.N + r] : 0.f;
       }
     }
@@ -215,6 +215,7 @@ template <int AXES, bool STAT, int TILE_ROWS> struct Side {
 #pragma unroll
       for (int a = 0; a < AXES; ++a) dst[a * ROWS + lane + 32 * i] = -pos[a * R + i];
       if (STAT) {
+        // past the document's end +inf: P = 0 there
         dst[kMaxAxes * ROWS + lane + 32 * i] = fmaf(lse[i], kLog2e, -up);
         dst[kMaxAxes * ROWS + ROWS + lane + 32 * i] = delta[i] * down;
       }
@@ -387,8 +388,35 @@ inline cudaError_t make_map(CUtensorMap* map, const void* base, uint32_t fmt, co
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// A work item in the kernels' 32-bit coordinates: own rows first, first + step,
+// ... below hi (`tiles` of them) of the document [lo, hi).
+struct Item {
+  int head, lo, hi, first, tiles;
+};
+template <bool UNIFORM>
+__device__ __forceinline__ Item item_of(const Params& p, uint32_t item, int heads) {
+  const Work w = work_of(p, item, heads);
+  int64_t lo, hi;
+  doc_range(p, w.doc, lo, hi);
+  Item i;
+  i.head = w.head;
+  i.lo = UNIFORM ? (int)uniform((uint32_t)lo) : (int)lo;
+  i.hi = UNIFORM ? (int)uniform((uint32_t)hi) : (int)hi;
+  const int64_t first = lo + (int64_t)w.tile * ROWS, step = (int64_t)p.hint * ROWS;
+  i.first = first < hi ? (int)first : (int)hi;
+  i.tiles = (int)((hi - i.first + step - 1) / step);
+  if (UNIFORM) {
+    i.first = (int)uniform((uint32_t)i.first);
+    i.tiles = (int)uniform((uint32_t)i.tiles);
+  }
+  return i;
+}
+
+// Documents of one length: as many blocks as fit the SMs walk all items, so
+// that one item's loads run under the previous one's products and its stores.
+// Packed documents: a block per item, many of which may be empty.
 inline cudaError_t launch_rows(void (*k)(Params, Maps), int smem, Params p, const Maps& maps, int heads, int threads,
-                               cudaStream_t st) {
+                               int blocks_per_sm, cudaStream_t st) {
   int64_t tiles = (p.len + ROWS - 1) / ROWS;
   if (tiles < 1) tiles = 1;
   const int64_t items = (p.docs + (p.offsets ? 1 : 0)) * heads;
@@ -396,8 +424,18 @@ inline cudaError_t launch_rows(void (*k)(Params, Maps), int smem, Params p, cons
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
   const int64_t room = 0x7fffffff / items;
   p.hint = (int)(tiles < room ? tiles : room);
+  p.items = (uint32_t)(items * p.hint);
+  uint32_t grid = p.items;
+  if (!p.offsets) {
+    int dev = 0, sms = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+    if (e != cudaSuccess) return e;
+    const uint32_t most = (uint32_t)(sms * blocks_per_sm);
+    if (grid > most) grid = most;
+  }
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(k), smem);
-  if (e == cudaSuccess) e = launch_pdl(k, dim3((unsigned)(items * p.hint)), dim3(threads), (size_t)smem, st, p, maps);
+  if (e == cudaSuccess) e = launch_pdl(k, dim3(grid), dim3(threads), (size_t)smem, st, p, maps);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }

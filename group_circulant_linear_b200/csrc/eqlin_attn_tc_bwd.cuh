@@ -63,7 +63,7 @@ template <int DP, bool KEYS> struct BwdCfg {
 //   in base 2 and scaled), else to the row.
 template <int AXES, bool CAP, bool KEYS, bool SMALL, typename E>
 __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, const float* side, int c0, const float* own,
-                                       float lse2, float delta, const Score& sc, int left, uint64_t& eps, uint32_t* pp,
+                                       float lse2, float delta, const Score& sc, uint64_t& eps, uint32_t* pp,
                                        uint32_t* pd) {
   constexpr bool F16 = Pair<E>::fmt == 0;
   constexpr float kDown = F16 ? 1.f / 256.f : 1.f;
@@ -109,14 +109,6 @@ __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, c
       uint64_t diff;
       if (KEYS) diff = fma2(h ? dl.y : dl.x, neg, F16 ? mul2(dp, down) : dp);
       else diff = add2(dp, row_delta);
-      if (left < 32) {                               // the document ends inside the chunk
-        if (i >= left) a = 0.f;
-        if (i + 1 >= left) b = 0.f;
-        // dP is then a product with zero rows, but delta may be anything
-        float e, f;
-        unpk2(diff, e, f);
-        diff = pk2(i < left ? e : 0.f, i + 1 < left ? f : 0.f);
-      }
       uint64_t prob = pk2(a, b);
       if (!KEYS) eps = fma2(prob, diff, eps);
       if (!KEYS && CAP) prob = mul2(prob, gain);     // KEYS: dv takes P itself
@@ -162,31 +154,26 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
-  const int rep = p.H / p.K;
-  const Work w = work_of(p, KEYS ? p.K : p.H);
-  const int kv_head = KEYS ? w.head : w.head / rep, q_head = KEYS ? w.head * rep : w.head;
-  const int64_t kh = (int64_t)kv_head * p.D, qh0 = (int64_t)q_head * p.D;
-  if (w.doc == p.docs) {
-    outside_rows(p, w.tile, [&](int64_t r) {
-      for (int d = threadIdx.x; d < p.D; d += C::THREADS) {
-        if (KEYS) {
-          static_cast<E*>(p.dk)[r * p.dks + kh + d] = Elem<E>::from_f(0.f);
-          static_cast<E*>(p.dv)[r * p.dvs + kh + d] = Elem<E>::from_f(0.f);
-        } else {
-          static_cast<E*>(p.dq)[r * p.dqs + qh0 + d] = Elem<E>::from_f(0.f);
-        }
-      }
-    });
-    return;
-  }
-  int64_t lo64, hi64;
-  doc_range(p, w.doc, lo64, hi64);
-  if (lo64 + (int64_t)w.tile * ROWS >= hi64) return;
-  const int lo = (int)uniform((uint32_t)lo64), hi = (int)uniform((uint32_t)hi64);
-  const int first = lo + w.tile * ROWS;
-  const int own_tiles = (int)(((int64_t)(hi - first) + (int64_t)p.hint * ROWS - 1) / ((int64_t)p.hint * ROWS));
-  const int tiles = (hi - lo - 1) / CW + 1;          // moving tiles of one head
+  const int rep = p.H / p.K, heads = KEYS ? p.K : p.H;
   const int passes = KEYS ? rep : 1;                 // query heads that pass by
+  if (p.offsets) {                                   // one item per block: it may have nothing to do
+    const Work w = work_of(p, blockIdx.x, heads);
+    if (w.doc == p.docs) {
+      const int64_t at = (int64_t)w.head * p.D;
+      outside_rows(p, w.tile, [&](int64_t r) {
+        for (int d = threadIdx.x; d < p.D; d += C::THREADS) {
+          if (KEYS) {
+            static_cast<E*>(p.dk)[r * p.dks + at + d] = Elem<E>::from_f(0.f);
+            static_cast<E*>(p.dv)[r * p.dvs + at + d] = Elem<E>::from_f(0.f);
+          } else {
+            static_cast<E*>(p.dq)[r * p.dqs + at + d] = Elem<E>::from_f(0.f);
+          }
+        }
+      });
+      return;
+    }
+    if (item_of<false>(p, blockIdx.x, heads).tiles == 0) return;
+  }
 
   if (threadIdx.x == 0) {
     mbar_init(own_full, 32);
@@ -222,55 +209,62 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
     Side<AXES, KEYS, CW> sides;
     uint32_t item = 0, owns = 0;
     bool ok = true;
-    sides.fetch(p, q_head, lo, hi, lane);
-    for (int t = 0; ok && t < own_tiles; ++t) {
-      const int r0 = first + t * p.hint * ROWS;
-      ok = claim(pend, own_empty, (t & 1) ^ 1, limit, abort_flag, err, site(KID, 2, 0), t);
-      if (!ok) break;
-      if (hi - r0 >= ROWS) {
-        if (lane == 0) {
-          expect_bytes(own_full, 2 * C::OWN);
-          tma_rows<DP, ROWS>(smem, &maps.m[0], KEYS ? kv_head : q_head, r0, own_full);
-          tma_rows<DP, ROWS>(smem + C::OWN, &maps.m[1], KEYS ? kv_head : q_head, r0, own_full);
+    for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
+      const Item w = item_of<false>(p, work, heads);
+      const int kv_head = KEYS ? w.head : w.head / rep, q_head = KEYS ? w.head * rep : w.head;
+      const int64_t kh = (int64_t)kv_head * p.D, qh0 = (int64_t)q_head * p.D;
+      const int lo = w.lo, hi = w.hi, tiles = (hi - lo - 1) / CW + 1;   // moving tiles of one head
+      sides.fetch(p, q_head, lo, hi, lane);
+      for (int t = 0; ok && t < w.tiles; ++t) {
+        const int r0 = w.first + t * p.hint * ROWS;
+        ok = claim(pend, own_empty, (owns & 1) ^ 1, limit, abort_flag, err, site(KID, 2, 0), owns);
+        if (!ok) break;
+        if (hi - r0 >= ROWS) {
+          if (lane == 0) {
+            expect_bytes(own_full, 2 * C::OWN);
+            tma_rows<DP, ROWS>(smem, &maps.m[0], KEYS ? kv_head : q_head, r0, own_full);
+            tma_rows<DP, ROWS>(smem + C::OWN, &maps.m[1], KEYS ? kv_head : q_head, r0, own_full);
+          }
+          mbar_arrive(own_full);
+        } else {
+          load_rows<DP, E>(smem_u32(smem), KEYS ? p.k : p.q, KEYS ? p.ks : p.qs, KEYS ? kh : qh0, r0, hi, ROWS, p.D,
+                           2 * d16, lane);
+          load_rows<DP, E>(smem_u32(smem + C::OWN), KEYS ? p.v : p.go, KEYS ? p.vs : p.gos, KEYS ? kh : qh0, r0, hi, ROWS,
+                           p.D, 2 * d16, lane);
+          cp_async_commit();
+          announce_later(pend, own_full);
         }
-        mbar_arrive(own_full);
-      } else {
-        load_rows<DP, E>(smem_u32(smem), KEYS ? p.k : p.q, KEYS ? p.ks : p.qs, KEYS ? kh : qh0, r0, hi, ROWS, p.D,
-                         2 * d16, lane);
-        load_rows<DP, E>(smem_u32(smem + C::OWN), KEYS ? p.v : p.go, KEYS ? p.vs : p.gos, KEYS ? kh : qh0, r0, hi, ROWS,
-                         p.D, 2 * d16, lane);
-        cp_async_commit();
-        announce_later(pend, own_full);
-      }
-      ++owns;
-      for (int g = 0; ok && g < passes; ++g) {
-        const int64_t qh = qh0 + (int64_t)g * p.D;
-        for (int j = 0; j < tiles; ++j, ++item) {
-          const int c0 = lo + j * CW, nc = min(hi - c0, CW), slot = item % C::SLOTS;
-          ok = claim(pend, empty + slot, ((item / C::SLOTS) & 1) ^ 1, limit, abort_flag, err, site(KID, 2, 1), item);
-          if (!ok) break;
-          uint8_t* to = ring + slot * 2 * C::MOV;
-          if (nc == CW && lane == 0) {
-            const int head = KEYS ? q_head + g : kv_head;
-            expect_bytes(full + slot, 2 * C::MOV);
-            tma_rows<DP, CW>(to, &maps.m[2], head, c0, full + slot);
-            tma_rows<DP, CW>(to + C::MOV, &maps.m[3], head, c0, full + slot);
-          }
-          if (AXES || KEYS) {
-            sides.store(side + slot * SIDE_F, kUp, kDown, lane);
-            const bool last = j + 1 == tiles;
-            sides.fetch(p, q_head + (last ? (g + 1 < passes ? g + 1 : 0) : g), last ? lo : c0 + CW, hi, lane);
-          }
-          if (nc == CW) {
-            mbar_arrive(full + slot);
-          } else {
-            const int rows = (nc + 15) & ~15;
-            load_rows<DP, E, CW>(smem_u32(to), KEYS ? p.q : p.k, KEYS ? p.qs : p.ks, KEYS ? qh : kh, c0, hi, rows, p.D,
-                                 2 * d16, lane);
-            load_rows<DP, E, CW>(smem_u32(to + C::MOV), KEYS ? p.go : p.v, KEYS ? p.gos : p.vs, KEYS ? qh : kh, c0, hi,
-                                 rows, p.D, 2 * d16, lane);
-            cp_async_commit();
-            announce_later(pend, full + slot);
+        ++owns;
+        for (int g = 0; ok && g < passes; ++g) {
+          const int64_t qh = qh0 + (int64_t)g * p.D;
+          for (int j = 0; j < tiles; ++j, ++item) {
+            const int c0 = lo + j * CW, nc = min(hi - c0, CW), slot = item % C::SLOTS;
+            ok = claim(pend, empty + slot, ((item / C::SLOTS) & 1) ^ 1, limit, abort_flag, err, site(KID, 2, 1), item);
+            if (!ok) break;
+            uint8_t* to = ring + slot * 2 * C::MOV;
+            if (nc == CW && lane == 0) {
+              const int head = KEYS ? q_head + g : kv_head;
+              expect_bytes(full + slot, 2 * C::MOV);
+              tma_rows<DP, CW>(to, &maps.m[2], head, c0, full + slot);
+              tma_rows<DP, CW>(to + C::MOV, &maps.m[3], head, c0, full + slot);
+            }
+            if (AXES || KEYS) {
+              sides.store(side + slot * SIDE_F, kUp, kDown, lane);
+              const bool last = j + 1 == tiles;
+              if (!last || g + 1 < passes || t + 1 < w.tiles)
+                sides.fetch(p, q_head + (last ? (g + 1 < passes ? g + 1 : 0) : g), last ? lo : c0 + CW, hi, lane);
+            }
+            if (nc == CW) {
+              mbar_arrive(full + slot);
+            } else {
+              const int rows = (nc + 15) & ~15;
+              load_rows<DP, E, CW>(smem_u32(to), KEYS ? p.q : p.k, KEYS ? p.qs : p.ks, KEYS ? qh : kh, c0, hi, rows, p.D,
+                                   2 * d16, lane);
+              load_rows<DP, E, CW>(smem_u32(to + C::MOV), KEYS ? p.go : p.v, KEYS ? p.gos : p.vs, KEYS ? qh : kh, c0, hi,
+                                   rows, p.D, 2 * d16, lane);
+              cp_async_commit();
+              announce_later(pend, full + slot);
+            }
           }
         }
       }
@@ -280,8 +274,9 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
     if (!ok && lane == 0) raise_abort(abort_flag, err);
   } else if (warp == MMA) {
     const uint32_t leader = lane == 0;
-    uint32_t item = 0;
+    uint32_t item = 0, owns = 0;
     bool ok = true;
+    int lo = 0, hi = 0;
     const uint32_t a0 = smem_u32(smem), a1 = smem_u32(smem + C::OWN);
     const uint32_t id_acc = idesc_f16(Pair<E>::fmt, (uint32_t)(16 * d16)) | kBTransposed;
     auto scores = [&](uint32_t it, int j) -> bool {
@@ -305,35 +300,41 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
       commit(leader, s_full);
       return true;
     };
-    for (int t = 0; ok && t < own_tiles; ++t) {
-      ok = wwait_all(own_full, t & 1, limit, abort_flag, err, site(KID, 1, 0), t) && scores(item, 0);
-      const int all = passes * tiles;
-      int j = 0;                                     // moving tile of the present pass
-      for (int i = 0; ok && i < all; ++i, ++item) {
-        const bool more = i + 1 < all;
-        const int next = j + 1 < tiles ? j + 1 : 0;
-        ok = wwait_all(p_full, item & 1, limit, abort_flag, err, site(KID, 1, 3), item);
-        if (!ok) break;
-        tc_fence_after();
-        const int steps = (min(hi - lo - j * CW, CW) + 15) / 16, slot = item % C::SLOTS;
-        const uint32_t x = smem_u32(ring + slot * 2 * C::MOV), y = x + C::MOV;
-        // P and du lie over the scores' chunks
-        const uint32_t b0 = KEYS ? y : x;
+    for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
+      const Item w = item_of<true>(p, work, heads);
+      lo = w.lo;
+      hi = w.hi;
+      const int tiles = (hi - lo - 1) / CW + 1;      // moving tiles of one head
+      for (int t = 0; ok && t < w.tiles; ++t, ++owns) {
+        ok = wwait_all(own_full, owns & 1, limit, abort_flag, err, site(KID, 1, 0), owns) && scores(item, 0);
+        const int all = passes * tiles;
+        int j = 0;                                     // moving tile of the present pass
+        for (int i = 0; ok && i < all; ++i, ++item) {
+          const bool more = i + 1 < all;
+          const int next = j + 1 < tiles ? j + 1 : 0;
+          ok = wwait_all(p_full, item & 1, limit, abort_flag, err, site(KID, 1, 3), item);
+          if (!ok) break;
+          tc_fence_after();
+          const int steps = (min(hi - lo - j * CW, CW) + 15) / 16, slot = item % C::SLOTS;
+          const uint32_t x = smem_u32(ring + slot * 2 * C::MOV), y = x + C::MOV;
+          // P and du lie over the scores' chunks
+          const uint32_t b0 = KEYS ? y : x;
 #pragma unroll
-        for (int s = 0; s < CW / 16; ++s)
-          if (s < steps)
-            mma_ts(leader, tmem + C::ACC0, tmem + C::S_COL + 32 * (s >> 1) + 8 * (s & 1),
-                   smem_desc_mn(b0 + s * 2048, C::MOV_PANEL, 1024), id_acc, i > 0 || s > 0);
+          for (int s = 0; s < CW / 16; ++s)
+            if (s < steps)
+              mma_ts(leader, tmem + C::ACC0, tmem + C::S_COL + 32 * (s >> 1) + 8 * (s & 1),
+                     smem_desc_mn(b0 + s * 2048, C::MOV_PANEL, 1024), id_acc, i > 0 || s > 0);
 #pragma unroll
-        for (int s = 0; s < CW / 16; ++s)
-          if (s < steps)
-            mma_ts(leader, tmem + C::ACC1, tmem + C::DP_COL + 32 * (s >> 1) + 8 * (s & 1),
-                   smem_desc_mn(x + s * 2048, C::MOV_PANEL, 1024), id_acc, i > 0 || s > 0);
-        commit(leader, acc_full);
-        commit(leader, empty + slot);
-        if (!more) commit(leader, own_empty);
-        if (more) ok = scores(item + 1, next);   // in order behind the products that read P and du
-        j = next;
+          for (int s = 0; s < CW / 16; ++s)
+            if (s < steps)
+              mma_ts(leader, tmem + C::ACC1, tmem + C::DP_COL + 32 * (s >> 1) + 8 * (s & 1),
+                     smem_desc_mn(x + s * 2048, C::MOV_PANEL, 1024), id_acc, i > 0 || s > 0);
+          commit(leader, acc_full);
+          commit(leader, empty + slot);
+          if (!more) commit(leader, own_empty);
+          if (more) ok = scores(item + 1, next);   // in order behind the products that read P and du
+          j = next;
+        }
       }
     }
     if (!ok && lane == 0) raise_abort(abort_flag, err);
@@ -345,128 +346,130 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
     const uint32_t my = tmem + ((uint32_t)(quarter * 32) << 16);
     uint32_t item = 0;
     bool ok = true;
-    for (int t = 0; ok && t < own_tiles; ++t) {
-      const int r0 = first + t * p.hint * ROWS + quarter * 32;
-      const bool any = r0 < hi, live = lane < hi - r0;
-      const int64_t row = (int64_t)r0 + lane;
-      float own[AXES ? AXES : 1];
+    for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
+      const Item w = item_of<false>(p, work, heads);
+      const int kv_head = KEYS ? w.head : w.head / rep, q_head = KEYS ? w.head * rep : w.head;
+      const int64_t kh = (int64_t)kv_head * p.D, qh0 = (int64_t)q_head * p.D;
+      const int lo = w.lo, hi = w.hi, tiles = (hi - lo - 1) / CW + 1;   // moving tiles of one head
+      for (int t = 0; ok && t < w.tiles; ++t) {
+        const int r0 = w.first + t * p.hint * ROWS + quarter * 32;
+        const bool any = r0 < hi, live = lane < hi - r0;
+        const int64_t row = (int64_t)r0 + lane;
+        float own[AXES ? AXES : 1];
 #pragma unroll
-      for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
-      float lse2 = 0.f, delta = 0.f;                 // of the own row (queries own)
-      if (!KEYS && live) {
-        const uint4* a = reinterpret_cast<const uint4*>(static_cast<const E*>(p.go) + row * p.gos + qh0);
-        const uint4* b = reinterpret_cast<const uint4*>(static_cast<const E*>(p.o) + row * p.os + qh0);
-        for (int c = 0; c < p.D / 8; ++c) {
-          const uint4 u = a[c], v = b[c];
-          const E* x = reinterpret_cast<const E*>(&u);
-          const E* y = reinterpret_cast<const E*>(&v);
+        for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
+        float lse2 = 0.f, delta = 0.f;                 // of the own row (queries own)
+        if (!KEYS && live) {
+          const uint4* a = reinterpret_cast<const uint4*>(static_cast<const E*>(p.go) + row * p.gos + qh0);
+          const uint4* b = reinterpret_cast<const uint4*>(static_cast<const E*>(p.o) + row * p.os + qh0);
+          for (int c = 0; c < p.D / 8; ++c) {
+            const uint4 u = a[c], v = b[c];
+            const E* x = reinterpret_cast<const E*>(&u);
+            const E* y = reinterpret_cast<const E*>(&v);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) delta = fmaf(Elem<E>::to_f(x[k]), Elem<E>::to_f(y[k]), delta);
+            for (int k = 0; k < 8; ++k) delta = fmaf(Elem<E>::to_f(x[k]), Elem<E>::to_f(y[k]), delta);
+          }
+          lse2 = p.lse[(int64_t)w.head * p.N + row] * kLog2e;
         }
-        lse2 = p.lse[(int64_t)w.head * p.N + row] * kLog2e;
-      }
-      uint64_t eps2 = 0;
-      for (int g = 0; ok && g < passes; ++g) {
-        const Score sc = score_of(p, q_head + g);
-        for (int j = 0; j < tiles; ++j, ++item) {
-          const int nc = min(hi - lo - j * CW, CW), slot = item % C::SLOTS;
-          ok = wwait_all(s_full, item & 1, limit, abort_flag, err, site(KID, 0, 0), item);
-          if ((AXES || KEYS) && ok)
-            ok = wwait_all(full + slot, (item / C::SLOTS) & 1, limit, abort_flag, err, site(KID, 0, 1), item);
-          if (!ok) break;
-          tc_fence_after();
-          // this warpgroup's chunks: wg, wg + NWG
-          uint32_t rs[2][32], rd[2][32];
-          if (any) {
+        uint64_t eps2 = 0;
+        for (int g = 0; ok && g < passes; ++g) {
+          const Score sc = score_of(p, q_head + g);
+          for (int j = 0; j < tiles; ++j, ++item) {
+            const int nc = min(hi - lo - j * CW, CW), slot = item % C::SLOTS;
+            ok = wwait_all(s_full, item & 1, limit, abort_flag, err, site(KID, 0, 0), item);
+            if ((AXES || KEYS) && ok)
+              ok = wwait_all(full + slot, (item / C::SLOTS) & 1, limit, abort_flag, err, site(KID, 0, 1), item);
+            if (!ok) break;
+            tc_fence_after();
+            if (any) {
+              const float* sd = side + slot * SIDE_F;
+              // this warpgroup's chunks: wg, wg + NWG
+#pragma unroll 1
+              for (int c = wg; c * 32 < nc; c += NWG) {
+                uint32_t rs[32], rd[32], pp[16], pd[16];
+                tmem_ld32(my + C::S_COL + c * 32, rs);
+                tmem_ld32(my + C::DP_COL + c * 32, rd);
+                tmem_wait_ld();
+                tie32(rs);
+                tie32(rd);
+                // Past the document's end: P = 0 and dP = delta, so that nothing adds to eps or du.  Under a cap
+                // P is what -cap gives, at most 1, and its product with g is 0.  (KEYS: lse is +inf there.)
+                if (!KEYS && c * 32 + 32 > nc) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int c = wg + i * NWG;
-              if (c * 32 < nc) {
-                tmem_ld32(my + C::S_COL + c * 32, rs[i]);
-                tmem_ld32(my + C::DP_COL + c * 32, rd[i]);
+                  for (int k = 0; k < 32; ++k)
+                    if (c * 32 + k >= nc) {
+                      rs[k] = __float_as_uint(-INFINITY);
+                      rd[k] = __float_as_uint(delta);
+                    }
+                }
+                if (CAP && all_small(reinterpret_cast<const float*>(rs), sc))
+                  grad32<AXES, CAP, KEYS, true, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);
+                else
+                  grad32<AXES, CAP, KEYS, false, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);
+                tmem_st_32x32b_x16(my + C::S_COL + c * 32, pp);
+                tmem_st_32x32b_x16(my + C::DP_COL + c * 32, pd);
+              }
+              tmem_wait_st();
+            }
+            tc_fence_before();
+            mbar_arrive(p_full);
+          }
+        }
+        if (!ok) break;
+        ok = wwait_all(acc_full, (item - 1) & 1, limit, abort_flag, err, site(KID, 0, 3), item);
+        if (!ok) break;
+        tc_fence_after();
+        float eps = 0.f;
+        if (!KEYS) {
+          float a, b;
+          unpk2(eps2, a, b);
+          eps = a + b;
+          if (NWG == 2) {                              // the two halves of the row's columns
+            eps_sum[wg * ROWS + quarter * 32 + lane] = eps;
+            named_bar_sync(1, NWG * 128);
+            eps = eps_sum[quarter * 32 + lane] + eps_sum[ROWS + quarter * 32 + lane];
+            named_bar_sync(1, NWG * 128);
+          }
+          if (live && wg == 0) p.delta[(int64_t)w.head * p.N + row] = delta + eps;
+        }
+        if (any) {
+#pragma unroll
+          for (int c = 0; c < DP / 16; ++c) {
+            if (c >= d16 || c % NWG != wg) continue;
+            uint32_t x[16], y[16];
+            tmem_ld_32x32b_x16(my + C::ACC0 + c * 16, x);
+            tmem_ld_32x32b_x16(my + C::ACC1 + c * 16, y);
+            tmem_wait_ld();
+            tie16(x);
+            tie16(y);
+            uint32_t px[8], py[8];
+#pragma unroll
+            for (int i = 0; i < 16; i += 2) {
+              const float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
+              float y0 = __uint_as_float(y[i]), y1 = __uint_as_float(y[i + 1]);
+              if (KEYS) {
+                px[i / 2] = Pair<E>::pack(x0 * kDown, x1 * kDown);
+              } else {
+                y0 = fmaf(-eps, x0, y0);
+                y1 = fmaf(-eps, x1, y1);
+              }
+              py[i / 2] = Pair<E>::pack(y0 * p.scale, y1 * p.scale);
+            }
+            if (live) {
+              E* out = KEYS ? static_cast<E*>(p.dk) + row * p.dks + kh : static_cast<E*>(p.dq) + row * p.dqs + qh0;
+              const bool second = c * 16 + 8 < p.D;
+              *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(py[0], py[1], py[2], py[3]);
+              if (second) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(py[4], py[5], py[6], py[7]);
+              if (KEYS) {
+                out = static_cast<E*>(p.dv) + row * p.dvs + kh;
+                *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(px[0], px[1], px[2], px[3]);
+                if (second) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(px[4], px[5], px[6], px[7]);
               }
             }
-            tmem_wait_ld();
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              tie32(rs[i]);
-              tie32(rd[i]);
-            }
-          }
-          if (any) {
-            const float* sd = side + slot * SIDE_F;
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-              const int c = wg + i * NWG;
-              if (c * 32 >= nc) continue;
-              uint32_t pp[16], pd[16];
-              if (CAP && all_small(reinterpret_cast<const float*>(rs[i]), sc))
-                grad32<AXES, CAP, KEYS, true, E>(rs[i], rd[i], sd, c * 32, own, lse2, delta, sc, nc - c * 32, eps2, pp, pd);
-              else
-                grad32<AXES, CAP, KEYS, false, E>(rs[i], rd[i], sd, c * 32, own, lse2, delta, sc, nc - c * 32, eps2, pp, pd);
-              tmem_st_32x32b_x16(my + C::S_COL + c * 32, pp);
-              tmem_st_32x32b_x16(my + C::DP_COL + c * 32, pd);
-            }
-            tmem_wait_st();
-          }
-          tc_fence_before();
-          mbar_arrive(p_full);
-        }
-      }
-      if (!ok) break;
-      ok = wwait_all(acc_full, (item - 1) & 1, limit, abort_flag, err, site(KID, 0, 3), item);
-      if (!ok) break;
-      tc_fence_after();
-      float eps = 0.f;
-      if (!KEYS) {
-        float a, b;
-        unpk2(eps2, a, b);
-        eps = a + b;
-        if (NWG == 2) {                              // the two halves of the row's columns
-          eps_sum[wg * ROWS + quarter * 32 + lane] = eps;
-          named_bar_sync(1, NWG * 128);
-          eps = eps_sum[quarter * 32 + lane] + eps_sum[ROWS + quarter * 32 + lane];
-          named_bar_sync(1, NWG * 128);
-        }
-        if (live && wg == 0) p.delta[(int64_t)w.head * p.N + row] = delta + eps;
-      }
-      if (any) {
-#pragma unroll
-        for (int c = 0; c < DP / 16; ++c) {
-          if (c >= d16 || c % NWG != wg) continue;
-          uint32_t x[16], y[16];
-          tmem_ld_32x32b_x16(my + C::ACC0 + c * 16, x);
-          tmem_ld_32x32b_x16(my + C::ACC1 + c * 16, y);
-          tmem_wait_ld();
-          tie16(x);
-          tie16(y);
-          uint32_t px[8], py[8];
-#pragma unroll
-          for (int i = 0; i < 16; i += 2) {
-            const float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
-            float y0 = __uint_as_float(y[i]), y1 = __uint_as_float(y[i + 1]);
-            if (KEYS) {
-              px[i / 2] = Pair<E>::pack(x0 * kDown, x1 * kDown);
-            } else {
-              y0 = fmaf(-eps, x0, y0);
-              y1 = fmaf(-eps, x1, y1);
-            }
-            py[i / 2] = Pair<E>::pack(y0 * p.scale, y1 * p.scale);
-          }
-          if (live) {
-            E* out = KEYS ? static_cast<E*>(p.dk) + row * p.dks + kh : static_cast<E*>(p.dq) + row * p.dqs + qh0;
-            const bool second = c * 16 + 8 < p.D;
-            *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(py[0], py[1], py[2], py[3]);
-            if (second) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(py[4], py[5], py[6], py[7]);
-            if (KEYS) {
-              out = static_cast<E*>(p.dv) + row * p.dvs + kh;
-              *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(px[0], px[1], px[2], px[3]);
-              if (second) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(px[4], px[5], px[6], px[7]);
-            }
           }
         }
+        tc_fence_before();
       }
-      tc_fence_before();
     }
     if (!ok && lane == 0) raise_abort(abort_flag, err);
   }
@@ -481,10 +484,10 @@ cudaError_t backward_axes(const Params& p, const Maps& maps, cudaStream_t st) {
   using C = BwdCfg<DP, KEYS>;
   const int heads = KEYS ? p.K : p.H;
   switch (p.axes) {
-    case 0: return launch_rows(attn_tc_bwd_kernel<DP, E, 0, CAP, KEYS>, C::SMEM, p, maps, heads, C::THREADS, st);
-    case 1: return launch_rows(attn_tc_bwd_kernel<DP, E, 1, CAP, KEYS>, C::SMEM, p, maps, heads, C::THREADS, st);
-    case 2: return launch_rows(attn_tc_bwd_kernel<DP, E, 2, CAP, KEYS>, C::SMEM, p, maps, heads, C::THREADS, st);
-    default: return launch_rows(attn_tc_bwd_kernel<DP, E, 3, CAP, KEYS>, C::SMEM, p, maps, heads, C::THREADS, st);
+    case 0: return launch_rows(attn_tc_bwd_kernel<DP, E, 0, CAP, KEYS>, C::SMEM, p, maps, heads, C::THREADS, C::BLOCKS, st);
+    case 1: return launch_rows(attn_tc_bwd_kernel<DP, E, 1, CAP, KEYS>, C::SMEM, p, maps, heads, C::THREADS, C::BLOCKS, st);
+    case 2: return launch_rows(attn_tc_bwd_kernel<DP, E, 2, CAP, KEYS>, C::SMEM, p, maps, heads, C::THREADS, C::BLOCKS, st);
+    default: return launch_rows(attn_tc_bwd_kernel<DP, E, 3, CAP, KEYS>, C::SMEM, p, maps, heads, C::THREADS, C::BLOCKS, st);
   }
 }
 template <int DP, typename E, bool KEYS>

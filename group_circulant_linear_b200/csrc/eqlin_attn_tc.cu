@@ -26,11 +26,12 @@ template <int DP> struct FwdCfg {
   static constexpr bool OVER = DP > 64;                       // P lies over S
   static constexpr int TILE = DP / 64 * PANEL;
   static constexpr int SLOTS = DP > 64 ? 2 : 4;               // K and V tiles in turn
-  static constexpr int NBAR = 2 + 2 * SLOTS + 5;
+  static constexpr int NBAR = 2 + 3 * SLOTS + 5;
   static constexpr int TMEM = 256;
   static constexpr int P_COL = OVER ? 0 : 128, O_COL = OVER ? 128 : 192;
   static constexpr int POS = (SLOTS / 2) * kMaxAxes * ROWS * 4;
-  static constexpr int SMEM = (1 + SLOTS) * TILE + POS + NBAR * 8 + 64 + 1024;
+  static constexpr int SMEM = (1 + SLOTS) * TILE + POS + 4 * STAGE + NBAR * 8 + 64 + 1024;
+  static_assert(2 * SMEM <= 227 * 1024, "two blocks per SM");
 };
 
 template <int DP, typename E, int AXES, bool CAP>
@@ -41,12 +42,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* ring = smem + C::TILE;
   float* spos = reinterpret_cast<float*>(ring + C::SLOTS * C::TILE);
-  uint64_t* bars = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(spos) + C::POS);
+  uint8_t* stage = reinterpret_cast<uint8_t*>(spos) + C::POS;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 4 * STAGE);
   uint64_t* q_full = bars;
   uint64_t* q_empty = bars + 1;
   uint64_t* kv_full = bars + 2;
   uint64_t* kv_empty = kv_full + C::SLOTS;
-  uint64_t* s_full = kv_empty + C::SLOTS;
+  uint64_t* land = kv_empty + C::SLOTS;
+  uint64_t* s_full = land + C::SLOTS;
   uint64_t* s_free = s_full + 1;
   uint64_t* p_full = s_free + 1;
   uint64_t* o_full = p_full + 1;
@@ -77,6 +80,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(kv_full + i, 32);
       mbar_init(kv_empty + i, 1);
+      mbar_init(land + i, 1);
     }
     mbar_init(s_full, 1);
     mbar_init(s_free, 128);
@@ -104,70 +108,56 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
   const int d16 = (p.D + 15) / 16;                            // 16-feature steps
 
   if (warp == LOAD_WARP) {
-    Pending pend;
+    const Waits wait{limit, abort_flag, err};
+    Tails tails;
     Side<AXES, false, ROWS> sidev;
     uint32_t item = 0, owns = 0;
     bool ok = true;
     for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
       const Item w = item_of<false>(p, work, p.H);
       const int lo = w.lo, hi = w.hi, kv_head = w.head / rep, key_tiles = (hi - lo - 1) / ROWS + 1;
-      const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)kv_head * p.D;
       if (AXES) sidev.fetch(p, w.head, lo, hi, lane);
       for (int t = 0; ok && t < w.tiles; ++t) {
-        const int r0 = w.first + t * p.hint * ROWS;
-        ok = claim(pend, q_empty, (owns & 1) ^ 1, limit, abort_flag, err, site(K_ATTN_FWD, 2, 0), owns);
+        ok = claim<DP, ROWS, 1>(tails, q_empty, (owns & 1) ^ 1, ring, land, kv_full, wait, site(K_ATTN_FWD, 2, 0), owns, lane);
         if (!ok) break;
-        if (hi - r0 >= ROWS) {
-          if (lane == 0) {
-            expect_bytes(q_full, C::TILE);
-            tma_rows<DP, ROWS>(smem, &maps.m[0], w.head, r0, q_full);
-          }
-          mbar_arrive(q_full);
-        } else {
-          load_rows<DP, E>(smem_u32(smem), p.q, p.qs, qh, r0, hi, ROWS, p.D, 2 * d16, lane);
-          cp_async_commit();
-          announce_later(pend, q_full);
+        if (lane == 0) {
+          expect_bytes(q_full, C::TILE);
+          tma_rows<DP, ROWS>(smem, &maps.m[0], w.head, w.first + t * p.hint * ROWS, q_full);
         }
+        mbar_arrive(q_full);
         ++owns;
         for (int j = 0; ok && j < key_tiles; ++j) {
           const int c0 = lo + j * ROWS, nc = min(hi - c0, ROWS);
 #pragma unroll 1
-          for (int kv = 0; kv < 2; ++kv, ++item) {
-            const int slot = item % C::SLOTS;
-            ok = claim(pend, kv_empty + slot, ((item / C::SLOTS) & 1) ^ 1, limit, abort_flag, err, site(K_ATTN_FWD, 2, 1),
-                       item);
+          for (int kv = 0; ok && kv < 2; ++kv) {
+            const uint32_t slot = item % C::SLOTS;
+            ok = claim<DP, ROWS, 1>(tails, kv_empty + slot, ((item / C::SLOTS) & 1) ^ 1, ring, land, kv_full, wait,
+                                    site(K_ATTN_FWD, 2, 1), item, lane);
             if (!ok) break;
-            uint8_t* to = ring + slot * C::TILE;
-            if (nc == ROWS && lane == 0) {
-              expect_bytes(kv_full + slot, C::TILE);
-              tma_rows<DP, ROWS>(to, &maps.m[1 + kv], kv_head, c0, kv_full + slot);
-            }
             // positions go with V: its slot is free once the softmax has used them
             if (AXES && kv) {
               sidev.store(spos + (slot >> 1) * kMaxAxes * ROWS, 0.f, 0.f, lane);
-              if (j + 1 < key_tiles || t + 1 < w.tiles) sidev.fetch(p, w.head, j + 1 < key_tiles ? c0 + ROWS : lo, hi, lane);
+              if (j + 1 < key_tiles || t + 1 < w.tiles)
+                sidev.fetch(p, w.head, j + 1 < key_tiles ? c0 + ROWS : lo, hi, lane);
             }
-            if (nc == ROWS) {
-              mbar_arrive(kv_full + slot);
-            } else {
-              load_rows<DP, E>(smem_u32(to), kv ? p.v : p.k, kv ? p.vs : p.ks, kh, c0, hi, (nc + 15) & ~15, p.D, 2 * d16,
-                               lane);
-              cp_async_commit();
-              announce_later(pend, kv_full + slot);
-            }
+            ok = bring<DP, ROWS, 1>(tails, slot, ring, land, kv_full, &maps.m[1 + kv], kv_head, c0, nc, wait,
+                                    site(K_ATTN_FWD, 2, 2), lane);
+            ++item;
           }
         }
       }
     }
-    announce_all(pend);
-    drain_loads(q_full, owns, kv_full, item, C::SLOTS);
+    if (ok) ok = settle<DP, ROWS, 1>(tails, tails.count, ring, land, kv_full, wait, site(K_ATTN_FWD, 2, 2), lane);
     if (!ok && lane == 0) raise_abort(abort_flag, err);
+    drain_loads(tails, land, q_full, owns, kv_full, item, C::SLOTS);
   } else if (warp == MMA_WARP) {
     const uint32_t leader = lane == 0;
     uint32_t item = 0, step = 0, owns = 0;                    // step: key tiles since the start
     bool ok = true;
     int lo = 0, hi = 0;
-    const uint32_t q_addr = smem_u32(smem);
+    const uint64_t q_desc = smem_desc(smem_u32(smem), 128);
+    const uint32_t q_lo = lo32(q_desc), k_hi = hi32(q_desc), v_hi = hi32(smem_desc_mn(0, PANEL, 1024));
+    const uint32_t ring_k = lo32(smem_desc(smem_u32(ring), 128)), ring_v = lo32(smem_desc_mn(smem_u32(ring), PANEL, 1024));
     const uint32_t id_o = idesc_f16(Pair<E>::fmt, (uint32_t)(16 * d16)) | kBTransposed;
     // scores of key tile j, step n, whose K is item `it`
     auto qk = [&](int j, uint32_t it, uint32_t n) -> bool {
@@ -178,12 +168,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
       tc_fence_after();
       const int nc = min(hi - lo - j * ROWS, ROWS);
       const uint32_t id = idesc_f16(Pair<E>::fmt, (uint32_t)((nc + 15) & ~15));
-      const uint32_t k_addr = smem_u32(ring + slot * C::TILE);
+      const uint32_t k_lo = ring_k + slot * (C::TILE >> 4);
 #pragma unroll
       for (int d = 0; d < DP / 16; ++d)
         if (d < d16) {
-          const uint32_t off = (d >> 2) * PANEL + (d & 3) * 32;
-          mma_ss(leader, tmem, smem_desc(q_addr + off, 128), smem_desc(k_addr + off, 128), id, d > 0);
+          const uint32_t off = ((d >> 2) * PANEL + (d & 3) * 32) >> 4;
+          mma_ss(leader, tmem, q_lo + off, k_lo + off, k_hi, id, d > 0);
         }
       commit(leader, s_full);
       commit(leader, kv_empty + slot);
@@ -199,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
         for (int j = 0; ok && j < key_tiles; ++j, item += 2, ++step) {
           const bool more = j + 1 < key_tiles;
           if (!C::OVER && more) ok = qk(j + 1, item + 2, step + 1);
-          if (!C::OVER && !more) commit(leader, q_empty);
+          if (!more) commit(leader, q_empty);                 // every product with this Q is issued
           const uint32_t vi = item + 1;
           const int slot = vi % C::SLOTS;
           ok = ok && wwait_all(kv_full + slot, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 1), vi) &&
@@ -207,16 +197,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
           if (!ok) break;
           tc_fence_after();
           const int steps = (min(hi - lo - j * ROWS, ROWS) + 15) / 16;
-          const uint32_t v_addr = smem_u32(ring + slot * C::TILE);
+          const uint32_t v_lo = ring_v + slot * (C::TILE >> 4);
 #pragma unroll
           for (int s = 0; s < ROWS / 16; ++s)
             if (s < steps)
-              mma_ts(leader, tmem + C::O_COL, tmem + C::P_COL + s * 8, smem_desc_mn(v_addr + s * 2048, PANEL, 1024), id_o,
+              mma_ts(leader, tmem + C::O_COL, tmem + C::P_COL + s * 8, v_lo + s * (2048 >> 4), v_hi, id_o,
                      j > 0 || s > 0);
           commit(leader, o_full);
           commit(leader, kv_empty + slot);
           if (C::OVER && more) ok = qk(j + 1, item + 2, step + 1);
-          if (C::OVER && !more) commit(leader, q_empty);
         }
       }
     }
@@ -270,8 +259,14 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
               if (c * 32 >= nc) continue;
-              transform32<AXES, CAP>(s + c * 32, pos, c * 32, own, sc);
-              if (c * 32 + 32 > nc) {
+              const bool edge = c * 32 + 32 > nc;             // the document ends in this chunk
+              if (CAP && edge) {                              // what lies past it must not choose the tanh
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (c * 32 + i >= nc) s[c * 32 + i] = 0.f;
+              }
+              transform32<AXES, CAP>(s + c * 32, pos, c * 32, own, sc, live);
+              if (edge) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                   if (c * 32 + i >= nc) s[c * 32 + i] = -INFINITY;
@@ -349,22 +344,18 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
         tc_fence_after();
         if (any) {
           const float inv = 1.f / l;
-          E* out = static_cast<E*>(p.o) + row * p.os + qh;
+          E* out = static_cast<E*>(p.o) + (int64_t)r0 * p.os + qh;
 #pragma unroll
-          for (int c = 0; c < DP / 16; ++c) {
-            if (c >= d16) continue;
-            uint32_t o[16];
-            tmem_ld_32x32b_x16(my + C::O_COL + c * 16, o);
+          for (int c = 0; c < DP / 32; ++c) {
+            if (c * 32 >= p.D) continue;
+            uint32_t o[32], pk[16];
+            tmem_ld32(my + C::O_COL + c * 32, o);
             tmem_wait_ld();
-            tie16(o);
-            uint32_t pk[8];
+            tie32(o);
 #pragma unroll
-            for (int i = 0; i < 16; i += 2)
+            for (int i = 0; i < 32; i += 2)
               pk[i / 2] = Pair<E>::pack(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-            if (live) {
-              *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
-              if (c * 16 + 8 < p.D) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(pk[4], pk[5], pk[6], pk[7]);
-            }
+            store32(stage + warp * STAGE, pk, out, p.os, hi - r0, c * 32, p.D, lane);
           }
           if (live) p.lse[(int64_t)w.head * p.N + row] = (m + log2f(l)) * kLn2;
         }

@@ -10,12 +10,13 @@
 //   warp 4      issues the MMAs: the whole warp runs the loops, so that
 //               descriptors stay in uniform registers, and one lane's predicate
 //               is set on the instruction itself; the warp allocates TMEM
-//   warp 5      brings tiles into shared memory: whole tiles with TMA (a 3D map
-//               over features, heads, tokens: features past D read as zero), the
-//               last, partial tile of a document with 16-byte asynchronous
-//               copies that write zeros past its end.  A neighbour's rows must
-//               not be in the tile at all: a product with P = 0 would spread
-//               their infinities and NaNs.
+//   warp 5      brings tiles into shared memory with TMA (a 3D map over
+//               features, heads, tokens: features past D read as zero) and
+//               clears the rows between a document's end and the next multiple
+//               of 16 in its last moving tile, which the products still read: a
+//               neighbour's rows must not be there, since a product with P = 0
+//               would spread their infinities and NaNs.  (Own rows past the end
+//               are whatever lies there: a row's results stay in that row.)
 //
 // Shared tiles are panels of 64 features: 128 rows of 128 bytes in the
 // 128-byte swizzle (16-byte chunk j of row r at chunk j ^ (r & 7)).  The same
@@ -62,27 +63,34 @@ template <> struct Pair<__nv_bfloat16> {
 
 // The MMAs below are issued by the lane whose `leader` is set; every lane of
 // the warp executes the statement, so operands stay warp-uniform.
+// Descriptors are passed as their low word (address and leading offset), which
+// advances by one 32-bit addition per step, and the constant high word.
 // D[tmem] (+)= A[tmem] * B[smem]: A holds 16-bit pairs, row = lane, two
 // consecutive k per column.
-__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
+__device__ __forceinline__ void mma_ts(uint32_t leader, uint32_t d, uint32_t a, uint32_t b_lo, uint32_t b_hi,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-      ::"r"(d), "r"(a), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %4, p;\n\t}"
+      ::"r"(d), "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
 }
-// D[tmem] (+)= A[smem] * B[smem]^T
-__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
-                                       uint32_t accumulate) {
+// D[tmem] (+)= A[smem] * B[smem]^T, both K-major (one high word)
+__device__ __forceinline__ void mma_ss(uint32_t leader, uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t hi,
+                                       uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-      ::"r"(d), "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
+      "mov.b64 da, {%1, %3};\n\t"
+      "mov.b64 db, {%2, %3};\n\t"
+      "setp.ne.b32 p, %5, 0;\n\t"
+      "setp.ne.b32 q, %6, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %4, p;\n\t}"
+      ::"r"(d), "r"(a_lo), "r"(b_lo), "r"(hi), "r"(idesc), "r"(accumulate), "r"(leader) : "memory");
 }
+__device__ __forceinline__ uint32_t lo32(uint64_t v) { return (uint32_t)v; }
+__device__ __forceinline__ uint32_t hi32(uint64_t v) { return (uint32_t)(v >> 32); }
 __device__ __forceinline__ void commit(uint32_t leader, uint64_t* bar) {
   asm volatile(
       "{\n\t.reg .pred q;\n\t"
@@ -145,41 +153,8 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   return v;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-// One warp copies `rows` rows (<= TILE_ROWS) from token r0 on of one head into the
-// panels at dst; rows at or past `hi`, and features at or past D, read as zero.
-// chunks: 16-byte chunks of a row that any product reads (ceil(D / 16) * 2).
-template <int DP, typename E, int TILE_ROWS = ROWS>
-__device__ __forceinline__ void load_rows(uint32_t dst, const void* src, int64_t stride, int64_t head_off, int r0,
-                                          int hi, int rows, int D, int chunks, int lane) {
-  const int sub = lane >> 3, ch0 = lane & 7;
-  const char* base = reinterpret_cast<const char*>(static_cast<const E*>(src) + head_off);
-  const int64_t step = stride * (int64_t)sizeof(E);
-  const int left = min(hi - r0, TILE_ROWS);
-#pragma unroll
-  for (int pn = 0; pn < DP / 64; ++pn) {
-    const int ch = pn * 8 + ch0;
-    if (ch >= chunks) continue;
-    const bool live_ch = ch * 8 < D;
-    const char* from = base + (int64_t)(r0 + sub) * step + ch * 16;
-    const uint32_t to = dst + pn * TILE_ROWS * 128;
-#pragma unroll 4
-    for (int r = sub; r < rows; r += 4, from += 4 * step) {
-      const bool on = live_ch && r < left;
-      cp_async16(to + r * 128 + ((ch0 ^ (r & 7)) << 4), on ? from : base, on ? 16u : 0u);
-    }
-  }
-}
-
-// Whole tiles: TILE_ROWS rows from token r0 on, all panels, announced on `bar`
-// by the copy's bytes (call from one lane, which arrives on `bar` afterwards).
+// TILE_ROWS rows from token r0 on, all panels, announced on `bar` by the copy's
+// bytes (call from one lane, which arrives on `bar` afterwards).
 template <int DP, int TILE_ROWS>
 __device__ __forceinline__ void tma_rows(void* dst, const CUtensorMap* map, int head, int r0, uint64_t* bar) {
 #pragma unroll
@@ -191,7 +166,7 @@ __device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
 }
 
 // What a tile needs beside its operands, one row per lane and round: negated
-// positions [axes][128] and, for moving queries, lse (base 2) and delta.  The
+// positions [axes][rows] and, for moving queries, lse (base 2) and delta.  The
 // loads are issued a tile ahead and stored when the slot is free.
 template <int AXES, bool STAT, int TILE_ROWS> struct Side {
   static constexpr int R = TILE_ROWS / 32;
@@ -213,63 +188,170 @@ template <int AXES, bool STAT, int TILE_ROWS> struct Side {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
-      for (int a = 0; a < AXES; ++a) dst[a * ROWS + lane + 32 * i] = -pos[a * R + i];
+      for (int a = 0; a < AXES; ++a) dst[a * TILE_ROWS + lane + 32 * i] = -pos[a * R + i];
       if (STAT) {
         // past the document's end +inf: P = 0 there
-        dst[kMaxAxes * ROWS + lane + 32 * i] = fmaf(lse[i], kLog2e, -up);
-        dst[kMaxAxes * ROWS + ROWS + lane + 32 * i] = delta[i] * down;
+        dst[kMaxAxes * TILE_ROWS + lane + 32 * i] = fmaf(lse[i], kLog2e, -up);
+        dst[(kMaxAxes + 1) * TILE_ROWS + lane + 32 * i] = delta[i] * down;
       }
     }
   }
 };
 
-// The loading warp's asynchronous copies that are not yet announced: a tile is
-// announced (32 arrivals) once its copies have landed and been made visible to
-// the tensor core, at the latest when the warp has nothing else to issue.
-struct Pending {
+// Moving tiles whose last rows are to be cleared once the copy has landed: the
+// loading warp settles them when it has nothing else to issue, at the latest
+// when three wait.  land[slot] counts the copy's bytes, full[slot] the warp's
+// 32 arrivals.
+struct Tails {
   int count = 0;
-  uint64_t* bar[3];
+  uint32_t phases = 0;    // of land, one bit per slot
+  uint32_t slot[3];
+  int from[3];            // first row to clear
 };
-__device__ __forceinline__ void announce_all(Pending& q) {
-  if (!q.count) return;
-  cp_async_wait<0>();
-  fence_proxy_async_smem();
-#pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (i < q.count) mbar_arrive(q.bar[i]);
-  q.count = 0;
-}
-// After an issue and its commit: at most two groups stay in flight unannounced.
-__device__ __forceinline__ void announce_later(Pending& q, uint64_t* bar) {
-#pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (i == q.count) q.bar[i] = bar;
-  if (++q.count == 3) {
-    cp_async_wait<2>();
-    fence_proxy_async_smem();
-    mbar_arrive(q.bar[0]);
-    q.bar[0] = q.bar[1];
-    q.bar[1] = q.bar[2];
-    q.count = 2;
+// What every wait of a role needs to know.
+struct Waits {
+  uint32_t limit;
+  volatile int* abort_flag;
+  int* err;
+  __device__ __forceinline__ bool on(uint64_t* bar, uint32_t parity, uint32_t where, uint32_t iter) const {
+    return wwait_all(bar, parity, limit, abort_flag, err, where, iter);
   }
+};
+// Settle the oldest `n` of the waiting tiles (NT tiles of TILE_ROWS rows per slot).
+template <int DP, int TILE_ROWS, int NT>
+__device__ __forceinline__ bool settle(Tails& q, int n, uint8_t* ring, uint64_t* land, uint64_t* full, const Waits& w,
+                                       uint32_t where, int lane) {
+  constexpr int TILE = DP / 64 * TILE_ROWS * 128;
+  for (; n > 0; --n) {
+    const uint32_t slot = q.slot[0];
+    const int from = q.from[0], rows = ((from + 15) & ~15) - from;
+    if (!w.on(land + slot, (q.phases >> slot) & 1, where, slot)) return false;
+    q.phases ^= 1u << slot;
+    uint8_t* base = ring + slot * NT * TILE + from * 128;
+#pragma unroll
+    for (int t = 0; t < NT * DP / 64; ++t)           // panels of the slot
+      for (int i = lane; i < rows * 8; i += 32)
+        *reinterpret_cast<uint4*>(base + t * TILE_ROWS * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    mbar_arrive(full + slot);
+    q.slot[0] = q.slot[1];
+    q.from[0] = q.from[1];
+    q.slot[1] = q.slot[2];
+    q.from[1] = q.from[2];
+    --q.count;
+  }
+  return true;
 }
-// Before writing into a slot: wait until it is free, announcing what is in
-// flight first if that takes time.  Uniform over the warp; false on abort.
-__device__ __forceinline__ bool claim(Pending& q, uint64_t* empty, uint32_t parity, uint32_t limit,
-                                      volatile int* abort_flag, int* err, uint32_t where, uint32_t iter) {
+// Start a moving tile's copies on slot `slot`, which is free; maps and heads of its NT
+// tiles, token c0, nc rows of the document.  What the lanes stored for the
+// tile before is announced with it.
+template <int DP, int TILE_ROWS, int NT>
+__device__ __forceinline__ bool bring(Tails& q, uint32_t slot, uint8_t* ring, uint64_t* land, uint64_t* full,
+                                      const CUtensorMap* map, int head, int c0, int nc, const Waits& w, uint32_t where,
+                                      int lane) {
+  constexpr int TILE = DP / 64 * TILE_ROWS * 128;
+  const bool whole = (nc & 15) == 0;
+  uint64_t* bar = whole ? full + slot : land + slot;
+  if (lane == 0) {
+    if (whole) expect_bytes(bar, NT * TILE);
+    else mbar_arrive_expect_tx(bar, NT * TILE);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) tma_rows<DP, TILE_ROWS>(ring + slot * NT * TILE + t * TILE, map + t, head, c0, bar);
+  }
+  if (whole) {
+    mbar_arrive(bar);
+    return true;
+  }
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    if (i == q.count) {
+      q.slot[i] = slot;
+      q.from[i] = nc;
+    }
+  return ++q.count < 3 || settle<DP, TILE_ROWS, NT>(q, 1, ring, land, full, w, where, lane);
+}
+// Before writing into a slot: wait until it is free, settling what waits first
+// if that takes time.  Uniform over the warp; false on abort.
+template <int DP, int TILE_ROWS, int NT>
+__device__ __forceinline__ bool claim(Tails& q, uint64_t* empty, uint32_t parity, uint8_t* ring, uint64_t* land,
+                                      uint64_t* full, const Waits& w, uint32_t where, uint32_t iter, int lane) {
   if (__all_sync(0xffffffffu, mbar_test_wait(empty, parity))) return true;
-  announce_all(q);
-  return wwait_all(empty, parity, limit, abort_flag, err, where, iter);
+  return settle<DP, TILE_ROWS, NT>(q, q.count, ring, land, full, w, where, lane) && w.on(empty, parity, where, iter);
 }
 
-// No copy of this block may be in flight when it exits: wait for the last
-// `slots` tiles of the ring and the last own tile (long done unless a wait ran
-// out somewhere).
-__device__ __forceinline__ void drain_loads(uint64_t* own_full, uint32_t own_count, uint64_t* full, uint32_t items,
-                                            uint32_t slots) {
+// No copy of this block may be in flight when it exits: wait for those of the
+// tiles not settled (after a wait ran out; nothing reads them any more), the
+// last `slots` tiles of the ring and the last own tile.
+__device__ __forceinline__ void drain_loads(Tails& q, uint64_t* land, uint64_t* own_full, uint32_t own_count,
+                                            uint64_t* full, uint32_t items, uint32_t slots) {
+  for (int i = 0; i < q.count; ++i) {
+    mbar_wait(land + q.slot[i], (q.phases >> q.slot[i]) & 1, kDefaultWaitLimit);
+    mbar_arrive(full + q.slot[i]);
+  }
   for (uint32_t k = items > slots ? items - slots : 0; k < items; ++k)
     mbar_wait(full + k % slots, (k / slots) & 1, kDefaultWaitLimit);
   if (own_count) mbar_wait(own_full, (own_count - 1) & 1, kDefaultWaitLimit);
+}
+
+// A warp's 32 rows x 32 features (16 packed words per lane, lane = row) into
+// global rows: through 2 KB of shared memory, so that four lanes write 64
+// consecutive bytes of a row.  Lanes writing 16 bytes of 32 rows each would
+// take the load/store unit a cycle per row and store.  Chunk j of row r lies
+// at chunk j ^ (r / 2 % 4) of its 64 bytes: no bank conflicts either way.
+constexpr int STAGE = 2048;
+template <typename E>
+__device__ __forceinline__ void store32(uint8_t* stage, const uint32_t* words, E* out, int64_t stride, int rows, int col,
+                                        int D, int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    *reinterpret_cast<uint4*>(stage + lane * 64 + ((j ^ ((lane >> 1) & 3)) << 4)) =
+        make_uint4(words[4 * j], words[4 * j + 1], words[4 * j + 2], words[4 * j + 3]);
+  __syncwarp();
+  const int j = lane & 3;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 2);
+    const uint4 v = *reinterpret_cast<const uint4*>(stage + r * 64 + ((j ^ ((r >> 1) & 3)) << 4));
+    if (r < rows && col + j * 8 < D) *reinterpret_cast<uint4*>(out + r * stride + col + j * 8) = v;
+  }
+  __syncwarp();
+}
+
+// Dot products of a warp's 32 rows of two tensors, one result per lane: eight
+// lanes read 128 consecutive bytes of a row.
+template <typename E>
+__device__ __forceinline__ float row_dots(const E* a, int64_t as, const E* b, int64_t bs, int rows, int D, int lane) {
+  float mine = 0.f, d[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) d[i] = 0.f;
+  for (int c = (lane & 7) * 8; c < ((D + 63) & ~63); c += 64) {
+    uint4 u[8], v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int r = 4 * i + (lane >> 3);
+      u[i] = v[i] = make_uint4(0, 0, 0, 0);
+      if (r < rows && c < D) {
+        u[i] = *reinterpret_cast<const uint4*>(a + r * as + c);
+        v[i] = *reinterpret_cast<const uint4*>(b + r * bs + c);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const E* x = reinterpret_cast<const E*>(&u[i]);
+      const E* y = reinterpret_cast<const E*>(&v[i]);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) d[i] = fmaf(Elem<E>::to_f(x[k]), Elem<E>::to_f(y[k]), d[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    d[i] += __shfl_xor_sync(0xffffffffu, d[i], 1);
+    d[i] += __shfl_xor_sync(0xffffffffu, d[i], 2);
+    d[i] += __shfl_xor_sync(0xffffffffu, d[i], 4);
+    const float x = __shfl_sync(0xffffffffu, d[i], (lane & 3) * 8);
+    if ((lane >> 2) == i) mine = x;
+  }
+  return mine;
 }
 
 // Scores in units of the raw product q.k (the softmax multiplies by scale2 =
@@ -311,24 +393,25 @@ __device__ __forceinline__ uint64_t q_small2(uint64_t x) {      // tanh(x) / x
 __device__ __forceinline__ float tanh_any(float raw, const Score& s) {
   return fmaf(-2.f, rcp(1.f + ex2(raw * s.twoin)), 1.f);
 }
-// Are all the warp's 32 x 32 raw scores small enough for the polynomial?
-__device__ __forceinline__ bool all_small(const float* raw, const Score& s) {
+// Are all the warp's 32 x 32 raw scores small enough for the polynomial?  Only
+// live rows count: results must not depend on what lies behind a document.
+__device__ __forceinline__ bool all_small(const float* raw, const Score& s, bool live) {
   float a = fabsf(raw[0]), b = fabsf(raw[1]);
 #pragma unroll
   for (int i = 2; i < 32; i += 2) {
     a = fmaxf(a, fabsf(raw[i]));
     b = fmaxf(b, fabsf(raw[i + 1]));
   }
-  return __all_sync(0xffffffffu, fmaxf(a, b) * s.in <= kSmall);   // a NaN is left out by fmaxf and survives either way
+  return __all_sync(0xffffffffu, !live || fmaxf(a, b) * s.in <= kSmall);   // a NaN survives either way
 }
 
 // City-block distances of four moving rows c0 .. c0+3 (their positions are
 // stored negated) from the own row.
-template <int AXES>
+template <int AXES, int TILE_ROWS>
 __device__ __forceinline__ void distances(const float* pos, int c0, const float* own, float (&d)[4]) {
 #pragma unroll
   for (int a = 0; a < AXES; ++a) {
-    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(pos + a * ROWS + c0);
+    const ulonglong2 v = *reinterpret_cast<const ulonglong2*>(pos + a * TILE_ROWS + c0);
     const uint64_t o = pk2(own[a], own[a]);
     float e[4];
     unpk2(add2(o, v.x), e[0], e[1]);
@@ -338,11 +421,12 @@ __device__ __forceinline__ void distances(const float* pos, int c0, const float*
   }
 }
 
-// Cap and bias of a row's 32 raw scores, in place; a and b pairs.
+// Cap and bias of a row's 32 raw scores, in place.
 template <int AXES, bool CAP>
-__device__ __forceinline__ void transform32(float* s, const float* pos, int c0, const float* own, const Score& sc) {
+__device__ __forceinline__ void transform32(float* s, const float* pos, int c0, const float* own, const Score& sc,
+                                            bool live) {
   if constexpr (CAP) {
-    if (all_small(s, sc)) {
+    if (all_small(s, sc, live)) {
       const uint64_t in = pk2(sc.in, sc.in);
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
@@ -359,7 +443,7 @@ __device__ __forceinline__ void transform32(float* s, const float* pos, int c0, 
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
       float d[4];
-      distances<AXES>(pos, c0 + i, own, d);
+      distances<AXES, ROWS>(pos, c0 + i, own, d);
       unpk2(fma2(slope, pk2(d[0], d[1]), pk2(s[i], s[i + 1])), s[i], s[i + 1]);
       unpk2(fma2(slope, pk2(d[2], d[3]), pk2(s[i + 2], s[i + 3])), s[i + 2], s[i + 3]);
     }
@@ -379,7 +463,7 @@ inline cudaError_t make_map(CUtensorMap* map, const void* base, uint32_t fmt, co
   if (!encode) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {(cuuint64_t)p.D, (cuuint64_t)heads, (cuuint64_t)p.N};
   const cuuint64_t strides[2] = {(cuuint64_t)p.D * 2, (cuuint64_t)stride * 2};
-  const cuuint32_t box[3] = {64, 1, (cuuint32_t)(rows < p.N ? rows : p.N)};   // a shorter sequence has no whole tile
+  const cuuint32_t box[3] = {64, 1, (cuuint32_t)rows};       // what lies outside the tensor reads as zero
   const cuuint32_t ones[3] = {1, 1, 1};
   const CUresult r =
       encode(map, fmt ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<void*>(base),

@@ -50,10 +50,10 @@ template <int DP, bool KEYS> struct BwdCfg {
   static constexpr int MOV_PANEL = CW * 128;
   static constexpr int MOV = DP / 64 * MOV_PANEL;               // bytes of one moving tile
   static constexpr int SLOTS = DP > 64 ? 2 : 4;
-  static constexpr int SIDE = (kMaxAxes * ROWS + (KEYS ? 2 * ROWS : 0)) * 4;   // positions, lse, delta of a slot
-  static constexpr int NBAR = 2 + 2 * SLOTS + 4;
+  static constexpr int SIDE = (kMaxAxes + (KEYS ? 2 : 0)) * CW * 4;            // positions, lse, delta of a slot
+  static constexpr int NBAR = 2 + 3 * SLOTS + 4;
   static constexpr int EPS = NWG == 2 ? 2 * ROWS * 4 : 0;       // eps of the two warpgroups
-  static constexpr int SMEM = 2 * OWN + SLOTS * (2 * MOV + SIDE) + EPS + NBAR * 8 + 64 + 1024;
+  static constexpr int SMEM = 2 * OWN + SLOTS * (2 * MOV + SIDE) + EPS + NWG * 4 * STAGE + NBAR * 8 + 64 + 1024;
   static_assert(ACC1 + DP <= TMEM, "TMEM columns");
   static_assert(BLOCKS * SMEM <= 227 * 1024, "shared memory");
 };
@@ -61,7 +61,7 @@ template <int DP, bool KEYS> struct BwdCfg {
 // One 32-column chunk of a row: raw scores rs and dP rd in, packed P and du out.
 //   KEYS: lse and delta belong to the columns (ls, dl in shared memory, already
 //   in base 2 and scaled), else to the row.
-template <int AXES, bool CAP, bool KEYS, bool SMALL, typename E>
+template <int AXES, bool CAP, bool KEYS, bool SMALL, int CW, typename E>
 __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, const float* side, int c0, const float* own,
                                        float lse2, float delta, const Score& sc, uint64_t& eps, uint32_t* pp,
                                        uint32_t* pd) {
@@ -73,11 +73,11 @@ __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, c
 #pragma unroll
   for (int j = 0; j < 32; j += 4) {
     float d[4];
-    if (AXES) distances<AXES>(side, c0 + j, own, d);
+    if (AXES) distances<AXES, CW>(side, c0 + j, own, d);
     ulonglong2 ls, dl;
     if (KEYS) {
-      ls = *reinterpret_cast<const ulonglong2*>(side + kMaxAxes * ROWS + c0 + j);
-      dl = *reinterpret_cast<const ulonglong2*>(side + kMaxAxes * ROWS + ROWS + c0 + j);
+      ls = *reinterpret_cast<const ulonglong2*>(side + kMaxAxes * CW + c0 + j);
+      dl = *reinterpret_cast<const ulonglong2*>(side + (kMaxAxes + 1) * CW + c0 + j);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -139,12 +139,14 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
   float* side = reinterpret_cast<float*>(ring + C::SLOTS * 2 * C::MOV);
   constexpr int SIDE_F = C::SIDE / 4;
   float* eps_sum = side + C::SLOTS * SIDE_F;
-  uint64_t* bars = reinterpret_cast<uint64_t*>(eps_sum + C::EPS / 4);
+  uint8_t* stage = reinterpret_cast<uint8_t*>(eps_sum + C::EPS / 4);
+  uint64_t* bars = reinterpret_cast<uint64_t*>(stage + NWG * 4 * STAGE);
   uint64_t* own_full = bars;
   uint64_t* own_empty = bars + 1;
   uint64_t* full = bars + 2;
   uint64_t* empty = full + C::SLOTS;
-  uint64_t* s_full = empty + C::SLOTS;
+  uint64_t* land = empty + C::SLOTS;
+  uint64_t* s_full = land + C::SLOTS;
   uint64_t* p_full = s_full + 1;
   uint64_t* acc_full = p_full + 1;
   uint64_t* drain = acc_full + 1;
@@ -181,6 +183,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
     for (int i = 0; i < C::SLOTS; ++i) {
       mbar_init(full + i, 32);
       mbar_init(empty + i, 1);
+      mbar_init(land + i, 1);
     }
     mbar_init(s_full, 1);
     mbar_init(p_full, NWG * 128);
@@ -205,97 +208,77 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
   const int d16 = (p.D + 15) / 16;
 
   if (warp == LOAD) {
-    Pending pend;
+    const Waits wait{limit, abort_flag, err};
+    Tails tails;
     Side<AXES, KEYS, CW> sides;
     uint32_t item = 0, owns = 0;
     bool ok = true;
     for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
       const Item w = item_of<false>(p, work, heads);
       const int kv_head = KEYS ? w.head : w.head / rep, q_head = KEYS ? w.head * rep : w.head;
-      const int64_t kh = (int64_t)kv_head * p.D, qh0 = (int64_t)q_head * p.D;
       const int lo = w.lo, hi = w.hi, tiles = (hi - lo - 1) / CW + 1;   // moving tiles of one head
       sides.fetch(p, q_head, lo, hi, lane);
       for (int t = 0; ok && t < w.tiles; ++t) {
-        const int r0 = w.first + t * p.hint * ROWS;
-        ok = claim(pend, own_empty, (owns & 1) ^ 1, limit, abort_flag, err, site(KID, 2, 0), owns);
+        ok = claim<DP, CW, 2>(tails, own_empty, (owns & 1) ^ 1, ring, land, full, wait, site(KID, 2, 0), owns, lane);
         if (!ok) break;
-        if (hi - r0 >= ROWS) {
-          if (lane == 0) {
-            expect_bytes(own_full, 2 * C::OWN);
-            tma_rows<DP, ROWS>(smem, &maps.m[0], KEYS ? kv_head : q_head, r0, own_full);
-            tma_rows<DP, ROWS>(smem + C::OWN, &maps.m[1], KEYS ? kv_head : q_head, r0, own_full);
-          }
-          mbar_arrive(own_full);
-        } else {
-          load_rows<DP, E>(smem_u32(smem), KEYS ? p.k : p.q, KEYS ? p.ks : p.qs, KEYS ? kh : qh0, r0, hi, ROWS, p.D,
-                           2 * d16, lane);
-          load_rows<DP, E>(smem_u32(smem + C::OWN), KEYS ? p.v : p.go, KEYS ? p.vs : p.gos, KEYS ? kh : qh0, r0, hi, ROWS,
-                           p.D, 2 * d16, lane);
-          cp_async_commit();
-          announce_later(pend, own_full);
+        if (lane == 0) {
+          const int r0 = w.first + t * p.hint * ROWS, head = KEYS ? kv_head : q_head;
+          expect_bytes(own_full, 2 * C::OWN);
+          tma_rows<DP, ROWS>(smem, &maps.m[0], head, r0, own_full);
+          tma_rows<DP, ROWS>(smem + C::OWN, &maps.m[1], head, r0, own_full);
         }
+        mbar_arrive(own_full);
         ++owns;
-        for (int g = 0; ok && g < passes; ++g) {
-          const int64_t qh = qh0 + (int64_t)g * p.D;
-          for (int j = 0; j < tiles; ++j, ++item) {
-            const int c0 = lo + j * CW, nc = min(hi - c0, CW), slot = item % C::SLOTS;
-            ok = claim(pend, empty + slot, ((item / C::SLOTS) & 1) ^ 1, limit, abort_flag, err, site(KID, 2, 1), item);
+        for (int g = 0; ok && g < passes; ++g)
+          for (int j = 0; ok && j < tiles; ++j) {
+            const int c0 = lo + j * CW, nc = min(hi - c0, CW);
+            const uint32_t slot = item % C::SLOTS;
+            ok = claim<DP, CW, 2>(tails, empty + slot, ((item / C::SLOTS) & 1) ^ 1, ring, land, full, wait,
+                                  site(KID, 2, 1), item, lane);
             if (!ok) break;
-            uint8_t* to = ring + slot * 2 * C::MOV;
-            if (nc == CW && lane == 0) {
-              const int head = KEYS ? q_head + g : kv_head;
-              expect_bytes(full + slot, 2 * C::MOV);
-              tma_rows<DP, CW>(to, &maps.m[2], head, c0, full + slot);
-              tma_rows<DP, CW>(to + C::MOV, &maps.m[3], head, c0, full + slot);
-            }
             if (AXES || KEYS) {
               sides.store(side + slot * SIDE_F, kUp, kDown, lane);
               const bool last = j + 1 == tiles;
               if (!last || g + 1 < passes || t + 1 < w.tiles)
                 sides.fetch(p, q_head + (last ? (g + 1 < passes ? g + 1 : 0) : g), last ? lo : c0 + CW, hi, lane);
             }
-            if (nc == CW) {
-              mbar_arrive(full + slot);
-            } else {
-              const int rows = (nc + 15) & ~15;
-              load_rows<DP, E, CW>(smem_u32(to), KEYS ? p.q : p.k, KEYS ? p.qs : p.ks, KEYS ? qh : kh, c0, hi, rows, p.D,
-                                   2 * d16, lane);
-              load_rows<DP, E, CW>(smem_u32(to + C::MOV), KEYS ? p.go : p.v, KEYS ? p.gos : p.vs, KEYS ? qh : kh, c0, hi,
-                                   rows, p.D, 2 * d16, lane);
-              cp_async_commit();
-              announce_later(pend, full + slot);
-            }
+            ok = bring<DP, CW, 2>(tails, slot, ring, land, full, &maps.m[2], KEYS ? q_head + g : kv_head, c0, nc, wait,
+                                  site(KID, 2, 2), lane);
+            ++item;
           }
-        }
       }
     }
-    announce_all(pend);
-    drain_loads(own_full, owns, full, item, C::SLOTS);
+    if (ok) ok = settle<DP, CW, 2>(tails, tails.count, ring, land, full, wait, site(KID, 2, 2), lane);
     if (!ok && lane == 0) raise_abort(abort_flag, err);
+    drain_loads(tails, land, own_full, owns, full, item, C::SLOTS);
   } else if (warp == MMA) {
     const uint32_t leader = lane == 0;
     uint32_t item = 0, owns = 0;
     bool ok = true;
     int lo = 0, hi = 0;
-    const uint32_t a0 = smem_u32(smem), a1 = smem_u32(smem + C::OWN);
+    const uint64_t own_desc = smem_desc(smem_u32(smem), 128);
+    const uint32_t a0 = lo32(own_desc), a1 = a0 + (C::OWN >> 4), k_hi = hi32(own_desc);
+    const uint32_t ring_k = lo32(smem_desc(smem_u32(ring), 128));
+    const uint64_t mn_desc = smem_desc_mn(smem_u32(ring), C::MOV_PANEL, 1024);
+    const uint32_t ring_mn = lo32(mn_desc), mn_hi = hi32(mn_desc);
     const uint32_t id_acc = idesc_f16(Pair<E>::fmt, (uint32_t)(16 * d16)) | kBTransposed;
     auto scores = [&](uint32_t it, int j) -> bool {
       const int slot = it % C::SLOTS;
       if (!wwait_all(full + slot, (it / C::SLOTS) & 1, limit, abort_flag, err, site(KID, 1, 1), it)) return false;
       tc_fence_after();
       const uint32_t id = idesc_f16(Pair<E>::fmt, (uint32_t)((min(hi - lo - j * CW, CW) + 15) & ~15));
-      const uint32_t x = smem_u32(ring + slot * 2 * C::MOV);
+      const uint32_t x = ring_k + slot * (2 * C::MOV >> 4);
 #pragma unroll
       for (int d = 0; d < DP / 16; ++d)
         if (d < d16) {
-          const uint32_t oa = (d >> 2) * PANEL + (d & 3) * 32, ob = (d >> 2) * C::MOV_PANEL + (d & 3) * 32;
-          mma_ss(leader, tmem + C::S_COL, smem_desc(a0 + oa, 128), smem_desc(x + ob, 128), id, d > 0);
+          const uint32_t oa = ((d >> 2) * PANEL + (d & 3) * 32) >> 4, ob = ((d >> 2) * C::MOV_PANEL + (d & 3) * 32) >> 4;
+          mma_ss(leader, tmem + C::S_COL, a0 + oa, x + ob, k_hi, id, d > 0);
         }
 #pragma unroll
       for (int d = 0; d < DP / 16; ++d)
         if (d < d16) {
-          const uint32_t oa = (d >> 2) * PANEL + (d & 3) * 32, ob = (d >> 2) * C::MOV_PANEL + (d & 3) * 32;
-          mma_ss(leader, tmem + C::DP_COL, smem_desc(a1 + oa, 128), smem_desc(x + C::MOV + ob, 128), id, d > 0);
+          const uint32_t oa = ((d >> 2) * PANEL + (d & 3) * 32) >> 4, ob = ((d >> 2) * C::MOV_PANEL + (d & 3) * 32) >> 4;
+          mma_ss(leader, tmem + C::DP_COL, a1 + oa, x + (C::MOV >> 4) + ob, k_hi, id, d > 0);
         }
       commit(leader, s_full);
       return true;
@@ -308,6 +291,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
       for (int t = 0; ok && t < w.tiles; ++t, ++owns) {
         ok = wwait_all(own_full, owns & 1, limit, abort_flag, err, site(KID, 1, 0), owns) && scores(item, 0);
         const int all = passes * tiles;
+        if (ok && all == 1) commit(leader, own_empty);
         int j = 0;                                     // moving tile of the present pass
         for (int i = 0; ok && i < all; ++i, ++item) {
           const bool more = i + 1 < all;
@@ -316,23 +300,23 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
           if (!ok) break;
           tc_fence_after();
           const int steps = (min(hi - lo - j * CW, CW) + 15) / 16, slot = item % C::SLOTS;
-          const uint32_t x = smem_u32(ring + slot * 2 * C::MOV), y = x + C::MOV;
+          const uint32_t x = ring_mn + slot * (2 * C::MOV >> 4), y = x + (C::MOV >> 4);
           // P and du lie over the scores' chunks
           const uint32_t b0 = KEYS ? y : x;
 #pragma unroll
           for (int s = 0; s < CW / 16; ++s)
             if (s < steps)
               mma_ts(leader, tmem + C::ACC0, tmem + C::S_COL + 32 * (s >> 1) + 8 * (s & 1),
-                     smem_desc_mn(b0 + s * 2048, C::MOV_PANEL, 1024), id_acc, i > 0 || s > 0);
+                     b0 + s * (2048 >> 4), mn_hi, id_acc, i > 0 || s > 0);
 #pragma unroll
           for (int s = 0; s < CW / 16; ++s)
             if (s < steps)
               mma_ts(leader, tmem + C::ACC1, tmem + C::DP_COL + 32 * (s >> 1) + 8 * (s & 1),
-                     smem_desc_mn(x + s * 2048, C::MOV_PANEL, 1024), id_acc, i > 0 || s > 0);
+                     x + s * (2048 >> 4), mn_hi, id_acc, i > 0 || s > 0);
           commit(leader, acc_full);
           commit(leader, empty + slot);
-          if (!more) commit(leader, own_empty);
           if (more) ok = scores(item + 1, next);   // in order behind the products that read P and du
+          if (i + 2 == all) commit(leader, own_empty);   // every product with the own tiles is issued
           j = next;
         }
       }
@@ -359,17 +343,10 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
 #pragma unroll
         for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
         float lse2 = 0.f, delta = 0.f;                 // of the own row (queries own)
-        if (!KEYS && live) {
-          const uint4* a = reinterpret_cast<const uint4*>(static_cast<const E*>(p.go) + row * p.gos + qh0);
-          const uint4* b = reinterpret_cast<const uint4*>(static_cast<const E*>(p.o) + row * p.os + qh0);
-          for (int c = 0; c < p.D / 8; ++c) {
-            const uint4 u = a[c], v = b[c];
-            const E* x = reinterpret_cast<const E*>(&u);
-            const E* y = reinterpret_cast<const E*>(&v);
-#pragma unroll
-            for (int k = 0; k < 8; ++k) delta = fmaf(Elem<E>::to_f(x[k]), Elem<E>::to_f(y[k]), delta);
-          }
-          lse2 = p.lse[(int64_t)w.head * p.N + row] * kLog2e;
+        if (!KEYS && any) {
+          delta = row_dots(static_cast<const E*>(p.go) + (int64_t)r0 * p.gos + qh0, p.gos,
+                           static_cast<const E*>(p.o) + (int64_t)r0 * p.os + qh0, p.os, hi - r0, p.D, lane);
+          if (live) lse2 = p.lse[(int64_t)w.head * p.N + row] * kLog2e;
         }
         uint64_t eps2 = 0;
         for (int g = 0; ok && g < passes; ++g) {
@@ -393,19 +370,20 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
                 tie32(rs);
                 tie32(rd);
                 // Past the document's end: P = 0 and dP = delta, so that nothing adds to eps or du.  Under a cap
-                // P is what -cap gives, at most 1, and its product with g is 0.  (KEYS: lse is +inf there.)
-                if (!KEYS && c * 32 + 32 > nc) {
+                // P is what -cap gives, at most 1, and its product with g is 0.  KEYS: lse is +inf there, so any
+                // finite score will do.
+                if ((!KEYS || CAP) && c * 32 + 32 > nc) {
 #pragma unroll
                   for (int k = 0; k < 32; ++k)
                     if (c * 32 + k >= nc) {
-                      rs[k] = __float_as_uint(-INFINITY);
-                      rd[k] = __float_as_uint(delta);
+                      rs[k] = KEYS ? 0u : __float_as_uint(-INFINITY);
+                      if (!KEYS) rd[k] = __float_as_uint(delta);
                     }
                 }
-                if (CAP && all_small(reinterpret_cast<const float*>(rs), sc))
-                  grad32<AXES, CAP, KEYS, true, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);
+                if (CAP && all_small(reinterpret_cast<const float*>(rs), sc, live))
+                  grad32<AXES, CAP, KEYS, true, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);
                 else
-                  grad32<AXES, CAP, KEYS, false, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);
+                  grad32<AXES, CAP, KEYS, false, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);
                 tmem_st_32x32b_x16(my + C::S_COL + c * 32, pp);
                 tmem_st_32x32b_x16(my + C::DP_COL + c * 32, pd);
               }
@@ -434,38 +412,32 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
         }
         if (any) {
 #pragma unroll
-          for (int c = 0; c < DP / 16; ++c) {
-            if (c >= d16 || c % NWG != wg) continue;
-            uint32_t x[16], y[16];
-            tmem_ld_32x32b_x16(my + C::ACC0 + c * 16, x);
-            tmem_ld_32x32b_x16(my + C::ACC1 + c * 16, y);
+          for (int c = 0; c < DP / 32; ++c) {
+            if (c * 32 >= p.D || c % NWG != wg) continue;
+            uint32_t x[32], y[32], pk[16];
+            tmem_ld32(my + C::ACC0 + c * 32, x);
+            tmem_ld32(my + C::ACC1 + c * 32, y);
             tmem_wait_ld();
-            tie16(x);
-            tie16(y);
-            uint32_t px[8], py[8];
+            tie32(x);
+            tie32(y);
+            uint8_t* st = stage + warp * STAGE;
+            if (KEYS) {
 #pragma unroll
-            for (int i = 0; i < 16; i += 2) {
-              const float x0 = __uint_as_float(x[i]), x1 = __uint_as_float(x[i + 1]);
-              float y0 = __uint_as_float(y[i]), y1 = __uint_as_float(y[i + 1]);
-              if (KEYS) {
-                px[i / 2] = Pair<E>::pack(x0 * kDown, x1 * kDown);
-              } else {
-                y0 = fmaf(-eps, x0, y0);
-                y1 = fmaf(-eps, x1, y1);
-              }
-              py[i / 2] = Pair<E>::pack(y0 * p.scale, y1 * p.scale);
+              for (int i = 0; i < 32; i += 2)
+                pk[i / 2] = Pair<E>::pack(__uint_as_float(x[i]) * kDown, __uint_as_float(x[i + 1]) * kDown);
+              store32(st, pk, static_cast<E*>(p.dv) + (int64_t)r0 * p.dvs + kh, p.dvs, hi - r0, c * 32, p.D, lane);
             }
-            if (live) {
-              E* out = KEYS ? static_cast<E*>(p.dk) + row * p.dks + kh : static_cast<E*>(p.dq) + row * p.dqs + qh0;
-              const bool second = c * 16 + 8 < p.D;
-              *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(py[0], py[1], py[2], py[3]);
-              if (second) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(py[4], py[5], py[6], py[7]);
-              if (KEYS) {
-                out = static_cast<E*>(p.dv) + row * p.dvs + kh;
-                *reinterpret_cast<uint4*>(out + c * 16) = make_uint4(px[0], px[1], px[2], px[3]);
-                if (second) *reinterpret_cast<uint4*>(out + c * 16 + 8) = make_uint4(px[4], px[5], px[6], px[7]);
+#pragma unroll
+            for (int i = 0; i < 32; i += 2) {
+              float a = __uint_as_float(y[i]), b = __uint_as_float(y[i + 1]);
+              if (!KEYS) {
+                a = fmaf(-eps, __uint_as_float(x[i]), a);
+                b = fmaf(-eps, __uint_as_float(x[i + 1]), b);
               }
+              pk[i / 2] = Pair<E>::pack(a * p.scale, b * p.scale);
             }
+            if (KEYS) store32(st, pk, static_cast<E*>(p.dk) + (int64_t)r0 * p.dks + kh, p.dks, hi - r0, c * 32, p.D, lane);
+            else store32(st, pk, static_cast<E*>(p.dq) + (int64_t)r0 * p.dqs + qh0, p.dqs, hi - r0, c * 32, p.D, lane);
           }
         }
         tc_fence_before();

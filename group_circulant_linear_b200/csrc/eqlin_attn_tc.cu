@@ -1,7 +1,7 @@
 // eqlin_attn_tc.cu -- document attention, forward, on the tensor cores.
 //
 // Per own tile of 128 queries, one pass over the document's keys in tiles of
-// up to 128 (trimmed to 16): S = Q K^T into TMEM, a thread per row reads its
+// up to CW (trimmed to 16): S = Q K^T into TMEM, a thread per row reads its
 // scores, keeps the running maximum m and sum l in FP32, and writes
 // P = 2^(s - m) back as 16-bit pairs, which the tensor core takes from TMEM
 // for O += P V.  P's rounding to 16 bits is the operand type's own (half a
@@ -11,10 +11,17 @@
 // (kLag): until then P is at most 256, far inside both types, and O and l
 // share the older m, so the quotient is the same.
 //
-// TMEM: 256 columns, so that two blocks share an SM and one's softmax runs
-// under the other's products: S [0, 128), then up to 64 features P [128, 192)
-// and O [192, 256) -- the next S is issued while P is still read -- and above
-// that P over S and O [128, 256).
+// Bound by the exponentials (128 x 128 of them take the four schedulers' MUFU
+// pipes 1024 cycles, the products 512) and by latency: TMEM and the registers
+// of a row per thread leave room for two blocks per SM.  Two forms:
+//   CW = 64    S, then P in its place, then the next S.
+//   CW = 128   P has columns of its own and the next S is issued while P is
+//              formed; half the hand-overs, but its 128 scores per thread only
+//              stay in registers for whole tiles away from the cap.
+// CW = 128 is taken for heads of up to 64 features (its columns need them) in
+// documents of 1024 tokens and more on average: 12544 tokens, 6 heads of 64
+// take 400 us against 534 (616 against 786 capped), 64 x 197 tokens, 12 heads
+// 103 us against 66, windows of 49 127 against 67.
 #include "eqlin_attn_tc.cuh"
 
 namespace eqlin {
@@ -22,26 +29,31 @@ namespace attn_tc {
 
 constexpr float kLag = 8.f;
 
-template <int DP> struct FwdCfg {
-  static constexpr bool OVER = DP > 64;                       // P lies over S
-  static constexpr int TILE = DP / 64 * PANEL;
-  static constexpr int SLOTS = DP > 64 ? 2 : 4;               // K and V tiles in turn
+template <int DP, int CW_> struct FwdCfg {
+  static constexpr int CW = CW_;                              // keys of a tile
+  static constexpr bool SEP = CW == 128;                      // P has its own columns
+  static constexpr int OWN = DP / 64 * PANEL;
+  static constexpr int MOV_PANEL = CW * 128;
+  static constexpr int MOV = DP / 64 * MOV_PANEL;
+  static constexpr int SLOTS = MOV > 8192 ? 4 : 6;            // K and V tiles in turn
   static constexpr int NBAR = 2 + 3 * SLOTS + 5;
-  static constexpr int TMEM = 256;
-  static constexpr int P_COL = OVER ? 0 : 128, O_COL = OVER ? 128 : 192;
-  static constexpr int POS = (SLOTS / 2) * kMaxAxes * ROWS * 4;
-  static constexpr int SMEM = (1 + SLOTS) * TILE + POS + 4 * STAGE + NBAR * 8 + 64 + 1024;
-  static_assert(2 * SMEM <= 227 * 1024, "two blocks per SM");
+  static constexpr int P_COL = SEP ? CW : 0, O_COL = SEP ? CW + CW / 2 : CW;
+  static constexpr int TMEM = O_COL + DP <= 128 ? 128 : 256;
+  static constexpr int POS = (SLOTS / 2) * kMaxAxes * CW * 4;
+  static constexpr int SMEM = OWN + SLOTS * MOV + POS + 4 * STAGE + NBAR * 8 + 64 + 1024;
+  static_assert(O_COL + DP <= TMEM, "TMEM columns");
+  static_assert(2 * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
+constexpr int kWideFrom = 1024;                               // average tokens of a document
 
-template <int DP, typename E, int AXES, bool CAP>
+template <int DP, int CW, typename E, int AXES, bool CAP>
 __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_constant__ Params p,
                                                                  const __grid_constant__ Maps maps) {
-  using C = FwdCfg<DP>;
+  using C = FwdCfg<DP, CW>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
-  uint8_t* ring = smem + C::TILE;
-  float* spos = reinterpret_cast<float*>(ring + C::SLOTS * C::TILE);
+  uint8_t* ring = smem + C::OWN;
+  float* spos = reinterpret_cast<float*>(ring + C::SLOTS * C::MOV);
   uint8_t* stage = reinterpret_cast<uint8_t*>(spos) + C::POS;
   uint64_t* bars = reinterpret_cast<uint64_t*>(stage + 4 * STAGE);
   uint64_t* q_full = bars;
@@ -110,44 +122,44 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
   if (warp == LOAD_WARP) {
     const Waits wait{limit, abort_flag, err};
     Tails tails;
-    Side<AXES, false, ROWS> sidev;
+    Side<AXES, false, CW> sidev;
     uint32_t item = 0, owns = 0;
     bool ok = true;
     for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
       const Item w = item_of<false>(p, work, p.H);
-      const int lo = w.lo, hi = w.hi, kv_head = w.head / rep, key_tiles = (hi - lo - 1) / ROWS + 1;
+      const int lo = w.lo, hi = w.hi, kv_head = w.head / rep, key_tiles = (hi - lo - 1) / CW + 1;
       if (AXES) sidev.fetch(p, w.head, lo, hi, lane);
       for (int t = 0; ok && t < w.tiles; ++t) {
-        ok = claim<DP, ROWS, 1>(tails, q_empty, (owns & 1) ^ 1, ring, land, kv_full, wait, site(K_ATTN_FWD, 2, 0), owns, lane);
+        ok = claim<DP, CW, 1>(tails, q_empty, (owns & 1) ^ 1, ring, land, kv_full, wait, site(K_ATTN_FWD, 2, 0), owns, lane);
         if (!ok) break;
         if (lane == 0) {
-          expect_bytes(q_full, C::TILE);
+          expect_bytes(q_full, C::OWN);
           tma_rows<DP, ROWS>(smem, &maps.m[0], w.head, w.first + t * p.hint * ROWS, q_full);
         }
         mbar_arrive(q_full);
         ++owns;
         for (int j = 0; ok && j < key_tiles; ++j) {
-          const int c0 = lo + j * ROWS, nc = min(hi - c0, ROWS);
+          const int c0 = lo + j * CW, nc = min(hi - c0, CW);
 #pragma unroll 1
           for (int kv = 0; ok && kv < 2; ++kv) {
             const uint32_t slot = item % C::SLOTS;
-            ok = claim<DP, ROWS, 1>(tails, kv_empty + slot, ((item / C::SLOTS) & 1) ^ 1, ring, land, kv_full, wait,
+            ok = claim<DP, CW, 1>(tails, kv_empty + slot, ((item / C::SLOTS) & 1) ^ 1, ring, land, kv_full, wait,
                                     site(K_ATTN_FWD, 2, 1), item, lane);
             if (!ok) break;
             // positions go with V: its slot is free once the softmax has used them
             if (AXES && kv) {
-              sidev.store(spos + (slot >> 1) * kMaxAxes * ROWS, 0.f, 0.f, lane);
+              sidev.store(spos + (slot >> 1) * kMaxAxes * CW, 0.f, 0.f, lane);
               if (j + 1 < key_tiles || t + 1 < w.tiles)
-                sidev.fetch(p, w.head, j + 1 < key_tiles ? c0 + ROWS : lo, hi, lane);
+                sidev.fetch(p, w.head, j + 1 < key_tiles ? c0 + CW : lo, hi, lane);
             }
-            ok = bring<DP, ROWS, 1>(tails, slot, ring, land, kv_full, &maps.m[1 + kv], kv_head, c0, nc, wait,
+            ok = bring<DP, CW, 1>(tails, slot, ring, land, kv_full, &maps.m[1 + kv], kv_head, c0, nc, wait,
                                     site(K_ATTN_FWD, 2, 2), lane);
             ++item;
           }
         }
       }
     }
-    if (ok) ok = settle<DP, ROWS, 1>(tails, tails.count, ring, land, kv_full, wait, site(K_ATTN_FWD, 2, 2), lane);
+    if (ok) ok = settle<DP, CW, 1>(tails, tails.count, ring, land, kv_full, wait, site(K_ATTN_FWD, 2, 2), lane);
     if (!ok && lane == 0) raise_abort(abort_flag, err);
     drain_loads(tails, land, q_full, owns, kv_full, item, C::SLOTS);
   } else if (warp == MMA_WARP) {
@@ -156,25 +168,23 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
     bool ok = true;
     int lo = 0, hi = 0;
     const uint64_t q_desc = smem_desc(smem_u32(smem), 128);
-    const uint32_t q_lo = lo32(q_desc), k_hi = hi32(q_desc), v_hi = hi32(smem_desc_mn(0, PANEL, 1024));
-    const uint32_t ring_k = lo32(smem_desc(smem_u32(ring), 128)), ring_v = lo32(smem_desc_mn(smem_u32(ring), PANEL, 1024));
+    const uint32_t q_lo = lo32(q_desc), k_hi = hi32(q_desc), v_hi = hi32(smem_desc_mn(0, C::MOV_PANEL, 1024));
+    const uint32_t ring_k = lo32(smem_desc(smem_u32(ring), 128)), ring_v = lo32(smem_desc_mn(smem_u32(ring), C::MOV_PANEL, 1024));
     const uint32_t id_o = idesc_f16(Pair<E>::fmt, (uint32_t)(16 * d16)) | kBTransposed;
     // scores of key tile j, step n, whose K is item `it`
     auto qk = [&](int j, uint32_t it, uint32_t n) -> bool {
       const int slot = it % C::SLOTS;
       if (!wwait_all(kv_full + slot, (it / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 1), it)) return false;
-      // S is free once every thread has read the previous scores (P over S: once P, and with it PV, is issued)
-      if (!C::OVER && !wwait_all(s_free, (n & 1) ^ 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 2), n)) return false;
+      // S is free once every thread has read the previous scores (P over S: once PV, in order, is issued)
+      if (C::SEP && !wwait_all(s_free, (n & 1) ^ 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 2), n)) return false;
       tc_fence_after();
-      const int nc = min(hi - lo - j * ROWS, ROWS);
-      const uint32_t id = idesc_f16(Pair<E>::fmt, (uint32_t)((nc + 15) & ~15));
-      const uint32_t k_lo = ring_k + slot * (C::TILE >> 4);
+      const uint32_t id = idesc_f16(Pair<E>::fmt, (uint32_t)((min(hi - lo - j * CW, CW) + 15) & ~15));
+      const uint32_t k_lo = ring_k + slot * (C::MOV >> 4);
 #pragma unroll
       for (int d = 0; d < DP / 16; ++d)
-        if (d < d16) {
-          const uint32_t off = ((d >> 2) * PANEL + (d & 3) * 32) >> 4;
-          mma_ss(leader, tmem, q_lo + off, k_lo + off, k_hi, id, d > 0);
-        }
+        if (d < d16)
+          mma_ss(leader, tmem, q_lo + (((d >> 2) * PANEL + (d & 3) * 32) >> 4),
+                 k_lo + (((d >> 2) * C::MOV_PANEL + (d & 3) * 32) >> 4), k_hi, id, d > 0);
       commit(leader, s_full);
       commit(leader, kv_empty + slot);
       return true;
@@ -183,12 +193,12 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
       const Item w = item_of<true>(p, work, p.H);
       lo = w.lo;
       hi = w.hi;
-      const int key_tiles = (hi - lo - 1) / ROWS + 1;
+      const int key_tiles = (hi - lo - 1) / CW + 1;
       for (int t = 0; ok && t < w.tiles; ++t, ++owns) {
         ok = wwait_all(q_full, owns & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 0), owns) && qk(0, item, step);
         for (int j = 0; ok && j < key_tiles; ++j, item += 2, ++step) {
           const bool more = j + 1 < key_tiles;
-          if (!C::OVER && more) ok = qk(j + 1, item + 2, step + 1);
+          if (C::SEP && more) ok = qk(j + 1, item + 2, step + 1);
           if (!more) commit(leader, q_empty);                 // every product with this Q is issued
           const uint32_t vi = item + 1;
           const int slot = vi % C::SLOTS;
@@ -196,16 +206,16 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
                wwait_all(p_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 3), step);
           if (!ok) break;
           tc_fence_after();
-          const int steps = (min(hi - lo - j * ROWS, ROWS) + 15) / 16;
-          const uint32_t v_lo = ring_v + slot * (C::TILE >> 4);
+          const int steps = (min(hi - lo - j * CW, CW) + 15) / 16;
+          const uint32_t v_lo = ring_v + slot * (C::MOV >> 4);
 #pragma unroll
-          for (int s = 0; s < ROWS / 16; ++s)
+          for (int s = 0; s < CW / 16; ++s)
             if (s < steps)
-              mma_ts(leader, tmem + C::O_COL, tmem + C::P_COL + s * 8, v_lo + s * (2048 >> 4), v_hi, id_o,
+              mma_ts(leader, tmem + C::O_COL, tmem + (C::SEP ? C::P_COL + 8 * s : 32 * (s >> 1) + 8 * (s & 1)), v_lo + s * (2048 >> 4), v_hi, id_o,
                      j > 0 || s > 0);
           commit(leader, o_full);
           commit(leader, kv_empty + slot);
-          if (C::OVER && more) ok = qk(j + 1, item + 2, step + 1);
+          if (!C::SEP && more) ok = qk(j + 1, item + 2, step + 1);   // in order behind the product that reads P
         }
       }
     }
@@ -219,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
     bool ok = true;
     for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
       const Item w = item_of<false>(p, work, p.H);
-      const int lo = w.lo, hi = w.hi, key_tiles = (hi - lo - 1) / ROWS + 1;
+      const int lo = w.lo, hi = w.hi, key_tiles = (hi - lo - 1) / CW + 1;
       const int64_t qh = (int64_t)w.head * p.D;
       const Score sc = score_of(p, w.head);
       for (int t = 0; ok && t < w.tiles; ++t) {
@@ -231,87 +241,122 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
         for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
         float m = -INFINITY, l = 0.f;                           // m in base-2 units
         for (int j = 0; j < key_tiles; ++j, ++step) {
-          const int nc = min(hi - lo - j * ROWS, ROWS);
+          const int nc = min(hi - lo - j * CW, CW);
+          // S is there; without SEP with it, in order, every earlier product
           ok = wwait_all(s_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 0), step);
-          if (AXES && ok) {
-            const uint32_t vi = 2 * step + 1;
+          const uint32_t vi = 2 * step + 1;
+          if (AXES && ok)
             ok = wwait_all(kv_full + vi % C::SLOTS, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 1), step);
-          }
           if (!ok) break;
           tc_fence_after();
-          uint32_t raw[ROWS];
+          uint32_t raw[CW];
           float* s = reinterpret_cast<float*>(raw);
           if (any) {
+            const float* pos = spos + ((vi % C::SLOTS) >> 1) * kMaxAxes * CW;
+            auto load = [&] {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (c * 32 < nc) tmem_ld32(my + c * 32, raw + c * 32);
-            tmem_wait_ld();
+              for (int c = 0; c < CW / 32; ++c)
+                if (c * 32 < nc) tmem_ld32(my + c * 32, raw + c * 32);
+              tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tie32(raw + c * 32);
+              for (int c = 0; c < CW / 32; ++c) tie32(raw + c * 32);
+            };
+            // cap, bias and -inf past the document's end for one chunk of which `left` columns are inside
+            auto chunk = [&](float* v, int c, int left) {
+              if (CAP && left < 32) {                         // what lies past the end must not choose the tanh
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (i >= left) v[i] = 0.f;
+              }
+              transform32<AXES, CAP, CW>(v, pos, c * 32, own, sc, CAP && all_small<32>(v, sc, live));
+              if (left < 32) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                  if (i >= left) v[i] = -INFINITY;
+              }
+            };
+            if constexpr (!C::SEP) {
+              load();
+#pragma unroll
+              for (int c = 0; c < CW / 32; ++c)
+                if (c * 32 < nc) chunk(s + c * 32, c, nc - c * 32);
+            } else {
+              bool fast = nc == CW;
+              if (fast) {
+                load();
+                if (CAP) fast = all_small<CW>(s, sc, live);
+              }
+              if (fast) {
+#pragma unroll
+                for (int c = 0; c < CW / 32; ++c) transform32<AXES, CAP, CW>(s + c * 32, pos, c * 32, own, sc, true);
+              } else {
+                // a document's last tile, or scores near the cap: through TMEM in a rolled loop (both forms of the
+                // tanh unrolled over 128 columns would not fit the instruction cache)
+#pragma unroll 1
+                for (int c = 0; c * 32 < nc; ++c) {
+                  uint32_t r[32];
+                  tmem_ld32(my + c * 32, r);
+                  tmem_wait_ld();
+                  tie32(r);
+                  chunk(reinterpret_cast<float*>(r), c, nc - c * 32);
+                  tmem_st_32x32b_x16(my + c * 32, r);
+                  tmem_st_32x32b_x16(my + c * 32 + 16, r + 16);
+                }
+                tmem_wait_st();
+                load();
+              }
+            }
           }
-          if (!C::OVER) {
+          if (C::SEP) {
             tc_fence_before();
             mbar_arrive(s_free);
           }
           float top = -INFINITY;
           if (any) {
-            const float* pos = spos + (((2 * step + 1) % C::SLOTS) >> 1) * kMaxAxes * ROWS;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < CW / 32; ++c) {
               if (c * 32 >= nc) continue;
-              const bool edge = c * 32 + 32 > nc;             // the document ends in this chunk
-              if (CAP && edge) {                              // what lies past it must not choose the tanh
+              const float* v = s + c * 32;
+              float t0 = top, t1 = v[0];
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (c * 32 + i >= nc) s[c * 32 + i] = 0.f;
+              for (int i = 1; i < 31; i += 3) {               // three-way maxima, two chains
+                t0 = fmaxf(fmaxf(t0, v[i]), v[i + 1]);
+                t1 = fmaxf(t1, v[i + 2]);
               }
-              transform32<AXES, CAP>(s + c * 32, pos, c * 32, own, sc, live);
-              if (edge) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (c * 32 + i >= nc) s[c * 32 + i] = -INFINITY;
-              }
-              float t0 = top, t1 = s[c * 32];
-#pragma unroll
-              for (int i = 1; i < 31; i += 3) {                 // three-way maxima, two chains
-                t0 = fmaxf(fmaxf(t0, s[c * 32 + i]), s[c * 32 + i + 1]);
-                t1 = fmaxf(t1, s[c * 32 + i + 2]);
-              }
-              top = fmaxf(fmaxf(t0, t1), s[c * 32 + 31]);
+              top = fmaxf(fmaxf(t0, t1), v[31]);
             }
-            top *= sc.scale2;                                   // scale > 0
+            top *= sc.scale2;                                 // scale > 0
           }
-          // P's columns, and O, are free once the previous product is done
-          if (j > 0) {
+          if (C::SEP && j > 0) {                              // P's columns, and O, are free once the last product is done
             ok = wwait_all(o_full, (step - 1) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 2), step);
             if (!ok) break;
             tc_fence_after();
-            const bool grow = top > m + kLag;
-            if (__any_sync(0xffffffffu, grow)) {
-              const float fix = grow ? ex2(m - top) : 1.f;
-              l *= fix;
-              if (grow) m = top;
-#pragma unroll
-              for (int c = 0; c < DP / 16; ++c) {
-                if (c >= d16) continue;
-                uint32_t o[16];
-                tmem_ld_32x32b_x16(my + C::O_COL + c * 16, o);
-                tmem_wait_ld();
-                tie16(o);
-#pragma unroll
-                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
-                tmem_st_32x32b_x16(my + C::O_COL + c * 16, o);
-              }
-              tmem_wait_st();
-            }
-          } else {
-            m = top;
           }
           if (any) {
+            if (j == 0) {
+              m = top;
+            } else {
+              const bool grow = top > m + kLag;
+              if (__any_sync(0xffffffffu, grow)) {
+                const float fix = grow ? ex2(m - top) : 1.f;
+                l *= fix;
+                if (grow) m = top;
+#pragma unroll 1
+                for (int c = 0; c < d16; ++c) {
+                  uint32_t o[16];
+                  tmem_ld_32x32b_x16(my + C::O_COL + c * 16, o);
+                  tmem_wait_ld();
+                  tie16(o);
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+                  tmem_st_32x32b_x16(my + C::O_COL + c * 16, o);
+                }
+              }
+            }
             const uint64_t k2 = pk2(sc.scale2, sc.scale2), off = pk2(-m, -m);
             uint64_t l0 = 0, l1 = 0;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < CW / 32; ++c) {
               if (c * 32 >= nc) continue;
               uint32_t pk[16];
 #pragma unroll
@@ -328,7 +373,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
                 pk[i / 2] = Pair<E>::pack(a, b);
                 pk[i / 2 + 1] = Pair<E>::pack(d, e);
               }
-              tmem_st_32x32b_x16(my + C::P_COL + c * 16, pk);
+              tmem_st_32x32b_x16(my + (C::SEP ? C::P_COL + c * 16 : c * 32), pk);
             }
             float a, b;
             unpk2(add2(l0, l1), a, b);
@@ -370,29 +415,31 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
   if (warp == MMA_WARP) tmem_dealloc(tmem, C::TMEM);
 }
 
-template <int DP, typename E, bool CAP>
+template <int DP, int CW, typename E, bool CAP>
 cudaError_t forward_axes(const Params& p, const Maps& maps, cudaStream_t st) {
-  constexpr int smem = FwdCfg<DP>::SMEM;
+  constexpr int smem = FwdCfg<DP, CW>::SMEM;
   switch (p.axes) {
-    case 0: return launch_rows(attn_tc_fwd_kernel<DP, E, 0, CAP>, smem, p, maps, p.H, kThreads, 2, st);
-    case 1: return launch_rows(attn_tc_fwd_kernel<DP, E, 1, CAP>, smem, p, maps, p.H, kThreads, 2, st);
-    case 2: return launch_rows(attn_tc_fwd_kernel<DP, E, 2, CAP>, smem, p, maps, p.H, kThreads, 2, st);
-    default: return launch_rows(attn_tc_fwd_kernel<DP, E, 3, CAP>, smem, p, maps, p.H, kThreads, 2, st);
+    case 0: return launch_rows(attn_tc_fwd_kernel<DP, CW, E, 0, CAP>, smem, p, maps, p.H, kThreads, 2, st);
+    case 1: return launch_rows(attn_tc_fwd_kernel<DP, CW, E, 1, CAP>, smem, p, maps, p.H, kThreads, 2, st);
+    case 2: return launch_rows(attn_tc_fwd_kernel<DP, CW, E, 2, CAP>, smem, p, maps, p.H, kThreads, 2, st);
+    default: return launch_rows(attn_tc_fwd_kernel<DP, CW, E, 3, CAP>, smem, p, maps, p.H, kThreads, 2, st);
   }
 }
-template <int DP, typename E>
+template <int DP, int CW, typename E>
 cudaError_t forward_cap(const Params& p, cudaStream_t st) {
   Maps maps;
   cudaError_t e = make_map(&maps.m[0], p.q, Pair<E>::fmt, p, p.H, p.qs, ROWS);
-  if (e == cudaSuccess) e = make_map(&maps.m[1], p.k, Pair<E>::fmt, p, p.K, p.ks, ROWS);
-  if (e == cudaSuccess) e = make_map(&maps.m[2], p.v, Pair<E>::fmt, p, p.K, p.vs, ROWS);
+  if (e == cudaSuccess) e = make_map(&maps.m[1], p.k, Pair<E>::fmt, p, p.K, p.ks, CW);
+  if (e == cudaSuccess) e = make_map(&maps.m[2], p.v, Pair<E>::fmt, p, p.K, p.vs, CW);
   if (e != cudaSuccess) return e;
   maps.m[3] = maps.m[0];
-  return p.cap > 0.f ? forward_axes<DP, E, true>(p, maps, st) : forward_axes<DP, E, false>(p, maps, st);
+  return p.cap > 0.f ? forward_axes<DP, CW, E, true>(p, maps, st) : forward_axes<DP, CW, E, false>(p, maps, st);
 }
 template <typename E>
 cudaError_t forward_dim(const Params& p, cudaStream_t st) {
-  return p.D <= 64 ? forward_cap<64, E>(p, st) : forward_cap<128, E>(p, st);
+  if (p.D > 64) return forward_cap<128, 64, E>(p, st);
+  // by the average length, not by max_len: results do not depend on that
+  return p.N >= kWideFrom * p.docs ? forward_cap<64, 128, E>(p, st) : forward_cap<64, 64, E>(p, st);
 }
 
 }  // namespace attn_tc

@@ -393,12 +393,13 @@ __device__ __forceinline__ uint64_t q_small2(uint64_t x) {      // tanh(x) / x
 __device__ __forceinline__ float tanh_any(float raw, const Score& s) {
   return fmaf(-2.f, rcp(1.f + ex2(raw * s.twoin)), 1.f);
 }
-// Are all the warp's 32 x 32 raw scores small enough for the polynomial?  Only
-// live rows count: results must not depend on what lies behind a document.
+// Are all of the warp's raw scores, N per row, small enough for the polynomial?
+// Only live rows count: results must not depend on what lies behind a document.
+template <int N>
 __device__ __forceinline__ bool all_small(const float* raw, const Score& s, bool live) {
   float a = fabsf(raw[0]), b = fabsf(raw[1]);
 #pragma unroll
-  for (int i = 2; i < 32; i += 2) {
+  for (int i = 2; i < N; i += 2) {
     a = fmaxf(a, fabsf(raw[i]));
     b = fmaxf(b, fabsf(raw[i + 1]));
   }
@@ -421,12 +422,12 @@ __device__ __forceinline__ void distances(const float* pos, int c0, const float*
   }
 }
 
-// Cap and bias of a row's 32 raw scores, in place.
-template <int AXES, bool CAP>
+// Cap and bias of a row's 32 raw scores, in place; `small` as all_small says.
+template <int AXES, bool CAP, int TILE_ROWS>
 __device__ __forceinline__ void transform32(float* s, const float* pos, int c0, const float* own, const Score& sc,
-                                            bool live) {
+                                            bool small) {
   if constexpr (CAP) {
-    if (all_small(s, sc, live)) {
+    if (small) {
       const uint64_t in = pk2(sc.in, sc.in);
 #pragma unroll
       for (int i = 0; i < 32; i += 2) {
@@ -443,7 +444,7 @@ __device__ __forceinline__ void transform32(float* s, const float* pos, int c0, 
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
       float d[4];
-      distances<AXES, ROWS>(pos, c0 + i, own, d);
+      distances<AXES, TILE_ROWS>(pos, c0 + i, own, d);
       unpk2(fma2(slope, pk2(d[0], d[1]), pk2(s[i], s[i + 1])), s[i], s[i + 1]);
       unpk2(fma2(slope, pk2(d[2], d[3]), pk2(s[i + 2], s[i + 3])), s[i + 2], s[i + 3]);
     }

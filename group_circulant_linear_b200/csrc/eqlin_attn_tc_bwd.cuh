@@ -380,7 +380,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
                       if (!KEYS) rd[k] = __float_as_uint(delta);
                     }
                 }
-                if (CAP && all_small(reinterpret_cast<const float*>(rs), sc, live))
+                if (CAP && all_small<32>(reinterpret_cast<const float*>(rs), sc, live))
                   grad32<AXES, CAP, KEYS, true, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);
                 else
                   grad32<AXES, CAP, KEYS, false, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);

@@ -342,16 +342,16 @@ class _On:
     def __init__(self, t: torch.Tensor, stream):
         if not isinstance(t, torch.Tensor) or not t.is_cuda:
             raise TypeError("expected a CUDA tensor")
-        self.device, self.stream = t.device, stream
+        self.index, self.stream = t.get_device(), stream
 
     def __enter__(self):
         cur = torch.cuda.current_device()
-        self.prev = cur if cur != self.device.index else None
+        self.prev = cur if cur != self.index else None
         if self.prev is not None:
-            torch.cuda.set_device(self.device)
+            torch.cuda.set_device(self.index)
         if self.stream is None:
-            return ctypes.c_void_p(torch.cuda.current_stream(self.device).cuda_stream)
-        return _stream(self.stream)
+            return torch.cuda.current_stream().cuda_stream
+        return self.stream.cuda_stream if hasattr(self.stream, "cuda_stream") else int(self.stream)
 
     def __exit__(self, *exc):
         if self.prev is not None:
@@ -359,15 +359,18 @@ class _On:
         return False
 
 
-def _ptr(t, dtype, shape, name, device):
-    p = _dev_ptr(t, dtype, shape, name)
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    return p
+def _ptr(t, dtype, shape, name, index):
+    """The address of a contiguous tensor on device `index`; small calls are bound by
+    their checks, so what is right is found out in four steps."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.is_contiguous() \
+            and (shape is None or t.shape == shape):
+        return t.data_ptr()
+    _dev_ptr(t, dtype, shape, name)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
-def _opt(t, dtype, shape, name, device):
-    return None if t is None else _ptr(t, dtype, shape, name, device)
+def _opt(t, dtype, shape, name, index):
+    return None if t is None else _ptr(t, dtype, shape, name, index)
 
 
 def _shape2(x, name):
@@ -385,7 +388,7 @@ def norm_forward(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor, y: torch.Ten
                  xsum: torch.Tensor | None = None, stream=None):
     """Group layer norm of x (or of x + res, which xsum receives); see eqlin_norm_forward."""
     N, F = _shape2(x, "x")
-    dt, dev, Cp = x.dtype, x.device, w.shape[0]
+    dt, dev, Cp = x.dtype, x.get_device(), w.shape[0]
     if Cp * T != F:
         raise ValueError(f"x has {F} features, w {Cp} channels of {T}")
     with _On(x, stream) as st:
@@ -409,14 +412,14 @@ def norm_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, mean: torc
                   res: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
     """Gradients of the norm of x (or of x + res); see eqlin_norm_backward."""
     N, F = _shape2(gy, "gy")
-    dt, dev, Cp = gy.dtype, gy.device, w.shape[0]
+    dt, dev, Cp = gy.dtype, gy.get_device(), w.shape[0]
     if Cp * T != F:
         raise ValueError(f"gy has {F} features, w {Cp} channels of {T}")
     with _On(gy, stream) as st:
         if workspace is None:
             if stream is not None:
                 raise ValueError("pass a workspace along with a stream")
-            workspace = norm_workspace(T, Cp, N, dev)
+            workspace = norm_workspace(T, Cp, N, gy.device)
         need = lib().eqlin_norm_workspace_bytes(T, Cp, N)
         if workspace.numel() * workspace.element_size() < need:
             raise ValueError(f"workspace holds {workspace.numel() * workspace.element_size()} bytes, needs {need}")
@@ -478,22 +481,22 @@ class Rope:
         return Rope, (self.T, self.Ch, self.sections, 1.0, self.freqs)
 
 
-def _heads(t, dtype, shape, name, device):
-    """A [N, heads, D] tensor whose heads lie one after the other: pointer and token stride."""
+def _heads(t, dtype, shape, name, index):
+    """A [N, heads, D] tensor whose heads lie one after the other: address and token stride."""
+    N, H, D = shape
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.get_device() == index and t.shape == shape:
+        s = t.stride()
+        if (s[2] == 1 or D == 1) and (s[1] == D or H == 1) or t.numel() == 0:
+            # a single token has no next one: its stride says nothing
+            return t.data_ptr(), (s[0] if N > 1 else H * D)
+        raise ValueError(f"{name}: the heads of a token must lie one after the other")
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    N, H, D = shape
-    s = t.stride()
-    if t.numel() and ((D > 1 and s[2] != 1) or (H > 1 and s[1] != D)):
-        raise ValueError(f"{name}: the heads of a token must lie one after the other")
-    # a single token has no next one: its stride says nothing
-    return ctypes.c_void_p(t.data_ptr()), (int(s[0]) if N > 1 else H * D)
+    raise ValueError(f"{name} is on {t.device}, expected cuda:{index}")
 
 
 def rope(r: Rope, pos: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, inverse: bool = False, stream=None):
@@ -507,9 +510,10 @@ def rope(r: Rope, pos: torch.Tensor, src: torch.Tensor, dst: torch.Tensor, inver
     if src.dtype not in _DT:
         raise TypeError(f"src must be float32, float16 or bfloat16, got {src.dtype}")
     with _On(src, stream) as st:
-        ps, ss = _heads(src, src.dtype, (N, H, D), "src", src.device)
-        pd, ds = _heads(dst, src.dtype, (N, H, D), "dst", src.device)
-        _check(lib().eqlin_rope_apply(r.ptr, _DT[src.dtype], _ptr(pos, torch.float32, (N, r.axes), "pos", src.device),
+        dev = src.get_device()
+        ps, ss = _heads(src, src.dtype, (N, H, D), "src", dev)
+        pd, ds = _heads(dst, src.dtype, (N, H, D), "dst", dev)
+        _check(lib().eqlin_rope_apply(r.ptr, _DT[src.dtype], _ptr(pos, torch.float32, (N, r.axes), "pos", dev),
                                       ps, ss, pd, ds, H, 1 if inverse else 0, N, st), "eqlin_rope_apply")
 
 
@@ -520,7 +524,7 @@ def _attention_desc(q, k, v, o, lse, docs, offsets, max_len, pos, slopes, scale,
         raise TypeError(f"q must be float32, float16 or bfloat16, got {q.dtype}")
     N, H, D = q.shape
     K = k.shape[1]
-    dev = q.device
+    dev = q.get_device()
     if offsets is not None:
         if offsets.dim() != 1 or offsets.numel() < 1:
             raise ValueError("offsets must be [docs + 1]")
@@ -532,16 +536,16 @@ def _attention_desc(q, k, v, o, lse, docs, offsets, max_len, pos, slopes, scale,
         if pos.dim() != 2 or pos.shape[1] < 1:
             raise ValueError("pos must be [N, axes]")
         axes = pos.shape[1]
-    ptrs, strides = zip(_heads(q, q.dtype, (N, H, D), "q", dev), _heads(k, q.dtype, (N, K, D), "k", dev),
-                        _heads(v, q.dtype, (N, K, D), "v", dev), _heads(o, q.dtype, (N, H, D), "o", dev))
-    desc = AttentionDesc(
-        tokens=N, heads=H, kv_heads=K, head_dim=D, q_stride=strides[0], k_stride=strides[1], v_stride=strides[2],
-        o_stride=strides[3], docs=int(docs), offsets=_opt(offsets, torch.int32, None, "offsets", dev),
-        max_len=int(max_len or 0), pos=_opt(pos, torch.float32, (N, axes), "pos", dev),
-        slopes=_opt(slopes, torch.float32, (H,), "slopes", dev), axes=axes,
-        scale=float(D ** -0.5 if scale is None else scale), cap=float(cap),
-        err=_opt(err, torch.int32, (4,), "err", dev), wait_limit=int(wait_limit))
-    return desc, ptrs, _ptr(lse, torch.float32, (H, N), "lse", dev)
+    pq, sq = _heads(q, q.dtype, (N, H, D), "q", dev)
+    pk, sk = _heads(k, q.dtype, (N, K, D), "k", dev)
+    pv, sv = _heads(v, q.dtype, (N, K, D), "v", dev)
+    po, so = _heads(o, q.dtype, (N, H, D), "o", dev)
+    desc = AttentionDesc(                  # in the structure's order
+        N, H, K, D, sq, sk, sv, so, int(docs), _opt(offsets, torch.int32, None, "offsets", dev), int(max_len or 0),
+        _opt(pos, torch.float32, (N, axes), "pos", dev), _opt(slopes, torch.float32, (H,), "slopes", dev), axes,
+        D ** -0.5 if scale is None else float(scale), float(cap), _opt(err, torch.int32, (4,), "err", dev),
+        int(wait_limit))
+    return desc, (pq, pk, pv, po), _ptr(lse, torch.float32, (H, N), "lse", dev)
 
 
 def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, o: torch.Tensor, lse: torch.Tensor, *,
@@ -573,7 +577,7 @@ def attention_backward(go: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
     with _On(q, stream) as st:
         desc, (pq, pk, pv, po), pl = _attention_desc(q, k, v, o, lse, docs, offsets, max_len, pos, slopes, scale, cap,
                                                      err, wait_limit)
-        dev, dt = q.device, q.dtype
+        dev, dt = q.get_device(), q.dtype
         pg, sg = _heads(go, dt, q.shape, "go", dev)
         pdq, sdq = _heads(dq, dt, q.shape, "dq", dev)
         pdk, sdk = _heads(dk, dt, k.shape, "dk", dev)

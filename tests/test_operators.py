@@ -372,6 +372,11 @@ ATTN_CASES = [  # lens, lead, tail, H, K, D, cap, axes
     ([513, 2, 640], 0, 70, 1, 1, 64, 0.0, 0),
     ([2, 3, 4] * 8, 0, 0, 1, 1, 24, 0.0, 0),
     ([385], 0, 0, 1, 1, 128, 0.0, 3),
+    # documents of 1024 tokens and more on average: the forward's wide form
+    ([1100], 0, 0, 1, 1, 64, 20.0, 2),
+    ([2177, 150], 3, 5, 1, 1, 32, 0.0, 3),
+    ([1024 + 65], 0, 0, 2, 1, 56, 0.0, 0),
+    ([1281], 0, 0, 1, 1, 64, 0.0, 0),
 ]
 
 
@@ -408,12 +413,15 @@ def test_attention_large_scores(dtype):
     # scores of several hundred units: the running maximum moves far, capped and not
     run_attention([190, 300], 0, 0, 2, 2, 64, 0.0, 0, dtype, q_std=60.0, seed=4)
     run_attention([190, 300], 0, 0, 2, 2, 64, 30.0, 0, dtype, q_std=60.0, seed=4)
+    run_attention([1150], 0, 0, 1, 1, 64, 30.0, 1, dtype, q_std=20.0, seed=4)   # some tiles near the cap, some not
+    run_attention([1150], 0, 0, 1, 1, 64, 0.0, 0, dtype, q_std=60.0, seed=4)
 
 
 @pytest.mark.gpu
-def test_attention_rising_scores():
+@pytest.mark.parametrize("N", [700, 1200])
+def test_attention_rising_scores(N):
     # keys ordered so that each tile's maximum is above the last one's
-    N, H, D = 700, 1, 64
+    H, D = 1, 64
     for dtype in ("bf16", "f32"):
         dt = DT[dtype]
         q = torch.full((N, H, D), 0.5)

@@ -92,9 +92,9 @@ __device__ __forceinline__ void outside_rows(const Params& p, int tile, F&& clea
 
 }  // namespace attn
 
-// f32 (and the reference for the other types): CUDA cores.
-cudaError_t launch_attn_simt_forward(const attn::Params& p, eqlin_dtype_t dt, cudaStream_t st);
-cudaError_t launch_attn_simt_backward(const attn::Params& p, eqlin_dtype_t dt, cudaStream_t st);
+// f32: CUDA cores.
+cudaError_t launch_attn_simt_forward(const attn::Params& p, cudaStream_t st);
+cudaError_t launch_attn_simt_backward(const attn::Params& p, cudaStream_t st);
 
 // f16 and bf16: tcgen05.
 cudaError_t launch_attn_tc_forward(const attn::Params& p, eqlin_dtype_t dt, cudaStream_t st);

@@ -82,7 +82,7 @@ extern "C" eqlin_status_t eqlin_attention_forward(const eqlin_attention_t* a, eq
   p.vs = a->v_stride;
   p.os = a->o_stride;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  return done(dtype == EQLIN_F32 ? launch_attn_simt_forward(p, dtype, cs) : launch_attn_tc_forward(p, dtype, cs));
+  return done(dtype == EQLIN_F32 ? launch_attn_simt_forward(p, cs) : launch_attn_tc_forward(p, dtype, cs));
 }
 
 extern "C" eqlin_status_t eqlin_attention_backward(const eqlin_attention_t* a, eqlin_dtype_t dtype, const void* go,
@@ -123,7 +123,7 @@ extern "C" eqlin_status_t eqlin_attention_backward(const eqlin_attention_t* a, e
   p.dks = dk_stride;
   p.dvs = dv_stride;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
-  if (dtype == EQLIN_F32) return done(launch_attn_simt_backward(p, dtype, cs));
+  if (dtype == EQLIN_F32) return done(launch_attn_simt_backward(p, cs));
   const cudaError_t e = launch_attn_tc_dq(p, dtype, cs);
   return done(e != cudaSuccess ? e : launch_attn_tc_dkv(p, dtype, cs));
 }

@@ -1,4 +1,4 @@
-// eqlin_attn_simt.cu -- document attention on the CUDA cores, in FP32.
+// eqlin_attn_simt.cu -- document attention of f32 tensors, on the CUDA cores.
 //
 // One block owns 64 rows of one head of one document and walks the other
 // side in tiles of 64, with one pass over it: the forward keeps each row's
@@ -11,8 +11,14 @@
 // 256 threads form a 16 x 16 grid; thread (ty, tx) owns rows 4ty .. 4ty+3
 // and, of a 64 x 64 product, columns tx + 16j: reads of the moving operand are
 // then 16 rows apart by D + 4 floats, free of bank conflicts, and those of the
-// rows broadcast.  Per four feature steps that is 8 16-byte shared loads for
-// 64 FMAs, which bounds the kernels (shared-memory issue, not FFMA).
+// rows broadcast.  Per four feature steps a warp's 8 16-byte reads take 12
+// shared-memory cycles and its 64 FMAs 64 scheduler cycles, of which an SM has
+// four: FFMA-bound, when loads and exponentials are out of the way.  Products
+// stop at a document's last column (in steps of 16, or 4) and warps without
+// rows skip them: the last tile of 197 tokens costs 5 columns, not 64.
+// A warp alone reads and writes its rows of P, so only tiles need block
+// barriers.  tanhf and expf, at some 60 instructions a score together, would
+// cost as much as one product each; tanh_fast and exp_fast take a third.
 #include "eqlin_attn.cuh"
 
 namespace eqlin {
@@ -30,31 +36,29 @@ template <int DP> struct Cfg {
   static constexpr int DC = (DP + 63) / 64;   // float4 groups of a thread's output columns
 };
 
-// Rows [r0, r0 + 64) of a head as FP32, zero past `hi` and past D.
-template <int DP, typename E>
+// Rows [r0, r0 + 64) of a head, zero past `hi` and past D.
+template <int DP>
 __device__ __forceinline__ void load_tile(float* dst, const void* src, int64_t stride, int64_t head_off, int64_t r0,
                                           int64_t hi, int D, float mul) {
-  constexpr int V = 16 / sizeof(E);
-  for (int i = threadIdx.x; i < B * (DP / V); i += kThreads) {
-    const int r = i / (DP / V), c = (i - r * (DP / V)) * V;
-    float f[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) f[e] = 0.f;
+#pragma unroll 4
+  for (int i = threadIdx.x; i < B * (DP / 4); i += kThreads) {
+    const int r = i / (DP / 4), c = (i - r * (DP / 4)) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     if (r0 + r < hi && c < D) {
-      const uint4 u = *reinterpret_cast<const uint4*>(static_cast<const E*>(src) + (r0 + r) * stride + head_off + c);
-      const E* e = reinterpret_cast<const E*>(&u);
-#pragma unroll
-      for (int k = 0; k < V; ++k) f[k] = Elem<E>::to_f(e[k]) * mul;
+      v = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + (r0 + r) * stride + head_off + c);
+      v.x *= mul;
+      v.y *= mul;
+      v.z *= mul;
+      v.w *= mul;
     }
-#pragma unroll
-    for (int k = 0; k < V; k += 4)
-      *reinterpret_cast<float4*>(dst + r * Cfg<DP>::LD + c + k) = make_float4(f[k], f[k + 1], f[k + 2], f[k + 3]);
+    *reinterpret_cast<float4*>(dst + r * Cfg<DP>::LD + c) = v;
   }
 }
 
-// acc[i][j] = A[row 4ty+i] . Bm[row tx+16j] over DP features
-template <int DP>
-__device__ __forceinline__ void mm_nt(const float* A, const float* Bm, float (&acc)[4][4]) {
+// acc[i][j] = A[row 4ty+i] . Bm[row tx+16j] over DP features; columns from
+// nc on are left at 0.
+template <int DP, int J>
+__device__ __forceinline__ void mm_nt_cols(const float* A, const float* Bm, float (&acc)[4][4]) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -62,15 +66,15 @@ __device__ __forceinline__ void mm_nt(const float* A, const float* Bm, float (&a
     for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
 #pragma unroll 4
   for (int d = 0; d < DP; d += 4) {
-    float4 a[4], b[4];
+    float4 a[4], b[J];
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * Cfg<DP>::LD + d);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) b[j] = *reinterpret_cast<const float4*>(Bm + (tx + 16 * j) * Cfg<DP>::LD + d);
+    for (int j = 0; j < J; ++j) b[j] = *reinterpret_cast<const float4*>(Bm + (tx + 16 * j) * Cfg<DP>::LD + d);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
+      for (int j = 0; j < J; ++j) {
         acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
         acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
         acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
@@ -79,13 +83,21 @@ __device__ __forceinline__ void mm_nt(const float* A, const float* Bm, float (&a
   }
 }
 
-// out[i][c] += sum_j P[4ty+i][j] M[j][4tx + 64c ..]
 template <int DP>
-__device__ __forceinline__ void mm_nn(const float* P, const float* M, float (&out)[4][Cfg<DP>::DC][4]) {
+__device__ __forceinline__ void mm_nt(const float* A, const float* Bm, int nc, float (&acc)[4][4]) {
+  if (nc > 48) mm_nt_cols<DP, 4>(A, Bm, acc);
+  else if (nc > 32) mm_nt_cols<DP, 3>(A, Bm, acc);
+  else if (nc > 16) mm_nt_cols<DP, 2>(A, Bm, acc);
+  else mm_nt_cols<DP, 1>(A, Bm, acc);
+}
+
+// out[i][c] += sum_j P[4ty+i][j] M[j][4tx + 64c ..] over the first nc rows of M
+template <int DP>
+__device__ __forceinline__ void mm_nn(const float* P, const float* M, int nc, float (&out)[4][Cfg<DP>::DC][4]) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   if (4 * tx >= DP) return;
 #pragma unroll 2
-  for (int j = 0; j < B; j += 4) {
+  for (int j = 0; j < nc; j += 4) {
     float4 a[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(P + (4 * ty + i) * LDP + j);
@@ -106,7 +118,7 @@ __device__ __forceinline__ void mm_nn(const float* P, const float* M, float (&ou
   }
 }
 
-template <int DP, typename E>
+template <int DP>
 __device__ __forceinline__ void store_rows(void* dst, int64_t stride, int64_t head_off, int64_t r0, int64_t hi, int D,
                                            const float (&v)[4][Cfg<DP>::DC][4]) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
@@ -118,17 +130,15 @@ __device__ __forceinline__ void store_rows(void* dst, int64_t stride, int64_t he
     for (int c = 0; c < Cfg<DP>::DC; ++c) {
       const int d = 4 * tx + 64 * c;
       if (d >= D) continue;               // D is a multiple of 4
-      E* o = static_cast<E*>(dst) + r * stride + head_off + d;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = Elem<E>::from_f(v[i][c][k]);
+      *reinterpret_cast<float4*>(static_cast<float*>(dst) + r * stride + head_off + d) =
+          make_float4(v[i][c][0], v[i][c][1], v[i][c][2], v[i][c][3]);
     }
   }
 }
 
-template <typename E>
 __device__ __forceinline__ void clear_row(void* dst, int64_t stride, int64_t head_off, int64_t r, int D) {
   for (int d = threadIdx.x; d < D; d += kThreads)
-    static_cast<E*>(dst)[r * stride + head_off + d] = Elem<E>::from_f(0.f);
+    static_cast<float*>(dst)[r * stride + head_off + d] = 0.f;
 }
 
 // Positions of tile rows: [axes][64].
@@ -144,9 +154,32 @@ __device__ __forceinline__ float distance(const float* pr, int r, const float* p
   return d;
 }
 
+// e^x for x <= 0 or so: the product with log2 e is taken to twice FP32's
+// precision, so that the error stays at ex2.approx's 2^-22 for any x; a third
+// of expf's instructions.
+__device__ __forceinline__ float exp_fast(float x) {
+  const float h = x * kLog2e, l = fmaf(x, kLog2e, -h) + x * 1.925963033500e-8f;
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(h));
+  // h = -inf (masked) leaves l a NaN
+  return y > 0.f ? fmaf(y, l * kLn2, y) : y;
+}
+// tanh: below 0.7 an odd polynomial, 4e-9 off at most (a weighted least-squares
+// fit of tanh(x)/x), the usual case below a cap; tanhf elsewhere.
+__device__ __forceinline__ float tanh_fast(float x) {
+  const float z = x * x;
+  if (z > 0.49f) return tanhf(x);
+  float q = fmaf(-0.004874242004007101f, z, 0.01973520778119564f);
+  q = fmaf(q, z, -0.053383808583021164f);
+  q = fmaf(q, z, 0.1332535296678543f);
+  q = fmaf(q, z, -0.33332860469818115f);
+  q = fmaf(q, z, 0.9999999403953552f);
+  return q * x;
+}
+
 // ------------------------------------------------------------------ forward
 
-template <int DP, typename E>
+template <int DP>
 __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) float sm[];
   float* Q = sm;
@@ -162,7 +195,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_co
   const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)(w.head / (p.H / p.K)) * p.D;
   if (w.doc == p.docs) {
     outside_rows(p, w.tile, [&](int64_t r) {
-      clear_row<E>(p.o, p.os, qh, r, p.D);
+      clear_row(p.o, p.os, qh, r, p.D);
       if (threadIdx.x == 0) p.lse[(int64_t)w.head * p.N + r] = 0.f;
     });
     return;
@@ -173,8 +206,9 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_co
   const float icap = p.cap > 0.f ? 1.f / p.cap : 0.f;
   for (int64_t r0 = lo + (int64_t)w.tile * B; r0 < hi; r0 += (int64_t)p.hint * B) {
     __syncthreads();
-    load_tile<DP, E>(Q, p.q, p.qs, qh, r0, hi, p.D, p.scale);
+    load_tile<DP>(Q, p.q, p.qs, qh, r0, hi, p.D, p.scale);
     load_pos(pq, p, r0, hi);
+    const bool busy = r0 + 8 * (threadIdx.x >> 5) < hi;       // does the warp have a row
     float m[4], l[4], o[4][Cfg<DP>::DC][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -187,18 +221,20 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_co
     }
     for (int64_t c0 = lo; c0 < hi; c0 += B) {
       __syncthreads();
-      load_tile<DP, E>(K, p.k, p.ks, kh, c0, hi, p.D, 1.f);
-      load_tile<DP, E>(V, p.v, p.vs, kh, c0, hi, p.D, 1.f);
+      load_tile<DP>(K, p.k, p.ks, kh, c0, hi, p.D, 1.f);
+      load_tile<DP>(V, p.v, p.vs, kh, c0, hi, p.D, 1.f);
       load_pos(pk, p, c0, hi);
       __syncthreads();
+      if (!busy) continue;
+      const int nc = (int)(hi - c0 < B ? hi - c0 : B);
       float s[4][4];
-      mm_nt<DP>(Q, K, s);
+      mm_nt<DP>(Q, K, nc, s);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float top = m[i];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          if (p.cap > 0.f) s[i][j] = p.cap * tanhf(s[i][j] * icap);
+          if (p.cap > 0.f) s[i][j] = p.cap * tanh_fast(s[i][j] * icap);
           if (p.axes) s[i][j] -= slope * distance(pq, 4 * ty + i, pk, tx + 16 * j, p.axes);
           if (c0 + tx + 16 * j >= hi) s[i][j] = -INFINITY;
           top = fmaxf(top, s[i][j]);
@@ -206,12 +242,12 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_co
 #pragma unroll
         for (int x = 8; x > 0; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
         const float base = top == -INFINITY ? 0.f : top;
-        const float fix = expf(m[i] - base);
+        const float fix = exp_fast(m[i] - base);
         m[i] = top;
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          s[i][j] = expf(s[i][j] - base);
+          s[i][j] = exp_fast(s[i][j] - base);
           sum += s[i][j];
           P[(4 * ty + i) * LDP + tx + 16 * j] = s[i][j];
         }
@@ -221,8 +257,9 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_co
 #pragma unroll
           for (int k = 0; k < 4; ++k) o[i][c][k] *= fix;
       }
-      __syncthreads();
-      mm_nn<DP>(P, V, o);
+      __syncwarp();
+      mm_nn<DP>(P, V, nc, o);
+      __syncwarp();
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -236,7 +273,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_co
       const int64_t r = r0 + 4 * ty + i;
       if (tx == 0 && r < hi) p.lse[(int64_t)w.head * p.N + r] = m[i] + logf(l[i]);
     }
-    store_rows<DP, E>(p.o, p.os, qh, r0, hi, p.D, o);
+    store_rows<DP>(p.o, p.os, qh, r0, hi, p.D, o);
   }
 }
 
@@ -248,16 +285,16 @@ __device__ __forceinline__ void tile_grad(const Params& p, float u, float dp, fl
                                           bool on, float icap, float slope, float& prob, float& du) {
   float slope_u = 1.f, s = u;
   if (p.cap > 0.f) {
-    const float t = tanhf(u * icap);
+    const float t = tanh_fast(u * icap);
     s = p.cap * t;
     slope_u = 1.f - t * t;
   }
   if (p.axes) s -= slope * dist;
-  prob = on ? expf(s - lse) : 0.f;
+  prob = on ? exp_fast(s - lse) : 0.f;
   du = on ? prob * (dp - delta) * slope_u : 0.f;
 }
 
-template <int DP, typename E>
+template <int DP>
 __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) float sm[];
   float* Q = sm;
@@ -274,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const __grid_con
   const Work w = work_of(p, blockIdx.x, p.H);
   const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)(w.head / (p.H / p.K)) * p.D;
   if (w.doc == p.docs) {
-    outside_rows(p, w.tile, [&](int64_t r) { clear_row<E>(p.dq, p.dqs, qh, r, p.D); });
+    outside_rows(p, w.tile, [&](int64_t r) { clear_row(p.dq, p.dqs, qh, r, p.D); });
     return;
   }
   int64_t lo, hi;
@@ -283,9 +320,9 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const __grid_con
   const float icap = p.cap > 0.f ? 1.f / p.cap : 0.f;
   for (int64_t r0 = lo + (int64_t)w.tile * B; r0 < hi; r0 += (int64_t)p.hint * B) {
     __syncthreads();
-    load_tile<DP, E>(K, p.o, p.os, qh, r0, hi, p.D, 1.f);   // o, for delta
-    load_tile<DP, E>(G, p.go, p.gos, qh, r0, hi, p.D, 1.f);
-    load_tile<DP, E>(Q, p.q, p.qs, qh, r0, hi, p.D, p.scale);
+    load_tile<DP>(K, p.o, p.os, qh, r0, hi, p.D, 1.f);   // o, for delta
+    load_tile<DP>(G, p.go, p.gos, qh, r0, hi, p.D, 1.f);
+    load_tile<DP>(Q, p.q, p.qs, qh, r0, hi, p.D, p.scale);
     load_pos(pq, p, r0, hi);
     __syncthreads();
     {   // delta of row t / 4, four threads a row
@@ -300,6 +337,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const __grid_con
       }
     }
     __syncthreads();
+    const bool busy = r0 + 8 * (threadIdx.x >> 5) < hi;
     float lse[4], delta[4], acc[4][Cfg<DP>::DC][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -313,13 +351,15 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const __grid_con
     }
     for (int64_t c0 = lo; c0 < hi; c0 += B) {
       __syncthreads();
-      load_tile<DP, E>(K, p.k, p.ks, kh, c0, hi, p.D, 1.f);
-      load_tile<DP, E>(V, p.v, p.vs, kh, c0, hi, p.D, 1.f);
+      load_tile<DP>(K, p.k, p.ks, kh, c0, hi, p.D, 1.f);
+      load_tile<DP>(V, p.v, p.vs, kh, c0, hi, p.D, 1.f);
       load_pos(pk, p, c0, hi);
       __syncthreads();
+      if (!busy) continue;
+      const int nc = (int)(hi - c0 < B ? hi - c0 : B);
       float u[4][4], dp[4][4];
-      mm_nt<DP>(Q, K, u);
-      mm_nt<DP>(G, V, dp);
+      mm_nt<DP>(Q, K, nc, u);
+      mm_nt<DP>(G, V, nc, dp);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -330,8 +370,9 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const __grid_con
                     r0 + r < hi && c0 + c < hi, icap, slope, prob, du);
           P[r * LDP + c] = du;
         }
-      __syncthreads();
-      mm_nn<DP>(P, K, acc);
+      __syncwarp();
+      mm_nn<DP>(P, K, nc, acc);
+      __syncwarp();
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -339,11 +380,11 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const __grid_con
       for (int c = 0; c < Cfg<DP>::DC; ++c)
 #pragma unroll
         for (int k = 0; k < 4; ++k) acc[i][c][k] *= p.scale;
-    store_rows<DP, E>(p.dq, p.dqs, qh, r0, hi, p.D, acc);
+    store_rows<DP>(p.dq, p.dqs, qh, r0, hi, p.D, acc);
   }
 }
 
-template <int DP, typename E>
+template <int DP>
 __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) float sm[];
   float* K = sm;
@@ -362,8 +403,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const __grid_co
   const int64_t kh = (int64_t)w.head * p.D;
   if (w.doc == p.docs) {
     outside_rows(p, w.tile, [&](int64_t r) {
-      clear_row<E>(p.dk, p.dks, kh, r, p.D);
-      clear_row<E>(p.dv, p.dvs, kh, r, p.D);
+      clear_row(p.dk, p.dks, kh, r, p.D);
+      clear_row(p.dv, p.dvs, kh, r, p.D);
     });
     return;
   }
@@ -372,9 +413,10 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const __grid_co
   const float icap = p.cap > 0.f ? 1.f / p.cap : 0.f;
   for (int64_t r0 = lo + (int64_t)w.tile * B; r0 < hi; r0 += (int64_t)p.hint * B) {
     __syncthreads();
-    load_tile<DP, E>(K, p.k, p.ks, kh, r0, hi, p.D, 1.f);
-    load_tile<DP, E>(V, p.v, p.vs, kh, r0, hi, p.D, 1.f);
+    load_tile<DP>(K, p.k, p.ks, kh, r0, hi, p.D, 1.f);
+    load_tile<DP>(V, p.v, p.vs, kh, r0, hi, p.D, 1.f);
     load_pos(pk, p, r0, hi);
+    const bool busy = r0 + 8 * (threadIdx.x >> 5) < hi;
     float dk[4][Cfg<DP>::DC][4], dv[4][Cfg<DP>::DC][4];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -388,8 +430,8 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const __grid_co
       const float slope = p.axes ? p.slopes[head] : 0.f;
       for (int64_t c0 = lo; c0 < hi; c0 += B) {
         __syncthreads();
-        load_tile<DP, E>(Q, p.q, p.qs, qh, c0, hi, p.D, p.scale);
-        load_tile<DP, E>(G, p.go, p.gos, qh, c0, hi, p.D, 1.f);
+        load_tile<DP>(Q, p.q, p.qs, qh, c0, hi, p.D, p.scale);
+        load_tile<DP>(G, p.go, p.gos, qh, c0, hi, p.D, 1.f);
         load_pos(pq, p, c0, hi);
         if (threadIdx.x < B) {
           const bool on = c0 + threadIdx.x < hi;
@@ -397,9 +439,11 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const __grid_co
           stat[B + threadIdx.x] = on ? p.delta[(int64_t)head * p.N + c0 + threadIdx.x] : 0.f;
         }
         __syncthreads();
+        if (!busy) continue;
+        const int nc = (int)(hi - c0 < B ? hi - c0 : B);
         float u[4][4], dp[4][4];
-        mm_nt<DP>(K, Q, u);
-        mm_nt<DP>(V, G, dp);
+        mm_nt<DP>(K, Q, nc, u);
+        mm_nt<DP>(V, G, nc, dp);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -411,19 +455,20 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const __grid_co
             P[r * LDP + c] = prob;
             dp[i][j] = du;
           }
-        __syncthreads();
-        mm_nn<DP>(P, G, dv);
-        __syncthreads();
+        __syncwarp();
+        mm_nn<DP>(P, G, nc, dv);
+        __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) P[(4 * ty + i) * LDP + tx + 16 * j] = dp[i][j];
-        __syncthreads();
-        mm_nn<DP>(P, Q, dk);               // Q carries the scale
+        __syncwarp();
+        mm_nn<DP>(P, Q, nc, dk);           // Q carries the scale
+        __syncwarp();
       }
     }
-    store_rows<DP, E>(p.dk, p.dks, kh, r0, hi, p.D, dk);
-    store_rows<DP, E>(p.dv, p.dvs, kh, r0, hi, p.D, dv);
+    store_rows<DP>(p.dk, p.dks, kh, r0, hi, p.D, dk);
+    store_rows<DP>(p.dv, p.dvs, kh, r0, hi, p.D, dv);
   }
 }
 
@@ -449,38 +494,25 @@ cudaError_t run(void (*k)(Params), int smem, Params p, int heads, cudaStream_t s
   return e;
 }
 
-template <int DP, typename E>
+template <int DP>
 cudaError_t forward(const Params& p, cudaStream_t st) {
-  return run(attn_simt_fwd_kernel<DP, E>, smem_bytes<DP>(3), p, p.H, st);
+  return run(attn_simt_fwd_kernel<DP>, smem_bytes<DP>(3), p, p.H, st);
 }
-template <int DP, typename E>
+template <int DP>
 cudaError_t backward(const Params& p, cudaStream_t st) {
-  const cudaError_t e = run(attn_simt_dq_kernel<DP, E>, smem_bytes<DP>(4), p, p.H, st);
-  return e != cudaSuccess ? e : run(attn_simt_dkv_kernel<DP, E>, smem_bytes<DP>(4), p, p.K, st);
+  const cudaError_t e = run(attn_simt_dq_kernel<DP>, smem_bytes<DP>(4), p, p.H, st);
+  return e != cudaSuccess ? e : run(attn_simt_dkv_kernel<DP>, smem_bytes<DP>(4), p, p.K, st);
 }
 
-template <typename E>
-cudaError_t pick(const Params& p, bool bwd, cudaStream_t st) {
-  if (p.D <= 32) return bwd ? backward<32, E>(p, st) : forward<32, E>(p, st);
-  if (p.D <= 64) return bwd ? backward<64, E>(p, st) : forward<64, E>(p, st);
-  return bwd ? backward<128, E>(p, st) : forward<128, E>(p, st);
-}
-
-cudaError_t dispatch(const Params& p, eqlin_dtype_t dt, bool bwd, cudaStream_t st) {
-  switch (dt) {
-    case EQLIN_F32: return pick<float>(p, bwd, st);
-    case EQLIN_F16: return pick<__half>(p, bwd, st);
-    default: return pick<__nv_bfloat16>(p, bwd, st);
-  }
+cudaError_t dispatch(const Params& p, bool bwd, cudaStream_t st) {
+  if (p.D <= 32) return bwd ? backward<32>(p, st) : forward<32>(p, st);
+  if (p.D <= 64) return bwd ? backward<64>(p, st) : forward<64>(p, st);
+  return bwd ? backward<128>(p, st) : forward<128>(p, st);
 }
 
 }  // namespace attn_simt
 
-cudaError_t launch_attn_simt_forward(const attn::Params& p, eqlin_dtype_t dt, cudaStream_t st) {
-  return attn_simt::dispatch(p, dt, false, st);
-}
-cudaError_t launch_attn_simt_backward(const attn::Params& p, eqlin_dtype_t dt, cudaStream_t st) {
-  return attn_simt::dispatch(p, dt, true, st);
-}
+cudaError_t launch_attn_simt_forward(const attn::Params& p, cudaStream_t st) { return attn_simt::dispatch(p, false, st); }
+cudaError_t launch_attn_simt_backward(const attn::Params& p, cudaStream_t st) { return attn_simt::dispatch(p, true, st); }
 
 }  // namespace eqlin

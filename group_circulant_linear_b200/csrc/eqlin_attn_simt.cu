@@ -20,11 +20,15 @@
 // barriers.  tanhf and expf, at some 60 instructions a score together, would
 // cost as much as one product each; tanh_fast and exp_fast take a third.
 #include "eqlin_attn.cuh"
+#include "eqlin_ptx.cuh"
 
 namespace eqlin {
 namespace attn_simt {
 
 using namespace attn;
+using ptx::fma2;
+using ptx::pk2;
+using ptx::unpk2;
 
 constexpr int B = 64;                     // rows and columns of a tile
 constexpr int kThreads = 256;
@@ -35,6 +39,19 @@ template <int DP> struct Cfg {
   static constexpr int TILE = B * LD;     // floats
   static constexpr int DC = (DP + 63) / 64;   // float4 groups of a thread's output columns
 };
+
+// A block's work: the first tile of every document and head before any second
+// one, so that the short last tiles fill the gaps of the last wave (197 tokens
+// of 16 images in 6 heads are 288 full tiles, one wave, and 96 of 5 rows).
+__device__ __forceinline__ Work work_of_row(const Params& p, int heads) {
+  const uint32_t each = p.items / (uint32_t)p.hint;
+  Work w;
+  w.tile = (int)(blockIdx.x / each);
+  const uint32_t rest = blockIdx.x - (uint32_t)w.tile * each, d = rest / (uint32_t)heads;
+  w.head = (int)(rest - d * (uint32_t)heads);
+  w.doc = d;
+  return w;
+}
 
 // Rows [r0, r0 + 64) of a head, zero past `hi` and past D.
 template <int DP>
@@ -60,27 +77,31 @@ __device__ __forceinline__ void load_tile(float* dst, const void* src, int64_t s
 template <int DP, int J>
 __device__ __forceinline__ void mm_nt_cols(const float* A, const float* Bm, float (&acc)[4][4]) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+  uint64_t sum[4][J];                      // even and odd features apart: one instruction for two products
 #pragma unroll
   for (int i = 0; i < 4; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.f;
+    for (int j = 0; j < J; ++j) sum[i][j] = 0;
 #pragma unroll 4
   for (int d = 0; d < DP; d += 4) {
-    float4 a[4], b[J];
+    ulonglong2 a[4], b[J];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(A + (4 * ty + i) * Cfg<DP>::LD + d);
+    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(A + (4 * ty + i) * Cfg<DP>::LD + d);
 #pragma unroll
-    for (int j = 0; j < J; ++j) b[j] = *reinterpret_cast<const float4*>(Bm + (tx + 16 * j) * Cfg<DP>::LD + d);
+    for (int j = 0; j < J; ++j) b[j] = *reinterpret_cast<const ulonglong2*>(Bm + (tx + 16 * j) * Cfg<DP>::LD + d);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
-      for (int j = 0; j < J; ++j) {
-        acc[i][j] = fmaf(a[i].x, b[j].x, acc[i][j]);
-        acc[i][j] = fmaf(a[i].y, b[j].y, acc[i][j]);
-        acc[i][j] = fmaf(a[i].z, b[j].z, acc[i][j]);
-        acc[i][j] = fmaf(a[i].w, b[j].w, acc[i][j]);
-      }
+      for (int j = 0; j < J; ++j) sum[i][j] = fma2(a[i].y, b[j].y, fma2(a[i].x, b[j].x, sum[i][j]));
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float x = 0.f, y = 0.f;
+      if (j < J) unpk2(sum[i][j], x, y);
+      acc[i][j] = x + y;
+    }
 }
 
 template <int DP>
@@ -93,7 +114,7 @@ __device__ __forceinline__ void mm_nt(const float* A, const float* Bm, int nc, f
 
 // out[i][c] += sum_j P[4ty+i][j] M[j][4tx + 64c ..] over the first nc rows of M
 template <int DP>
-__device__ __forceinline__ void mm_nn(const float* P, const float* M, int nc, float (&out)[4][Cfg<DP>::DC][4]) {
+__device__ __forceinline__ void mm_nn(const float* P, const float* M, int nc, uint64_t (&out)[4][Cfg<DP>::DC][2]) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   if (4 * tx >= DP) return;
 #pragma unroll 2
@@ -105,22 +126,22 @@ __device__ __forceinline__ void mm_nn(const float* P, const float* M, int nc, fl
     for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
       for (int c = 0; c < Cfg<DP>::DC; ++c) {
-        const float4 m = *reinterpret_cast<const float4*>(M + (j + jj) * Cfg<DP>::LD + 4 * tx + 64 * c);
+        const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(M + (j + jj) * Cfg<DP>::LD + 4 * tx + 64 * c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const float w = jj == 0 ? a[i].x : jj == 1 ? a[i].y : jj == 2 ? a[i].z : a[i].w;
-          out[i][c][0] = fmaf(w, m.x, out[i][c][0]);
-          out[i][c][1] = fmaf(w, m.y, out[i][c][1]);
-          out[i][c][2] = fmaf(w, m.z, out[i][c][2]);
-          out[i][c][3] = fmaf(w, m.w, out[i][c][3]);
+          const uint64_t w2 = pk2(w, w);
+          out[i][c][0] = fma2(w2, m.x, out[i][c][0]);
+          out[i][c][1] = fma2(w2, m.y, out[i][c][1]);
         }
       }
   }
 }
 
+// Row i times mul[i].
 template <int DP>
 __device__ __forceinline__ void store_rows(void* dst, int64_t stride, int64_t head_off, int64_t r0, int64_t hi, int D,
-                                           const float (&v)[4][Cfg<DP>::DC][4]) {
+                                           const uint64_t (&v)[4][Cfg<DP>::DC][2], const float (&mul)[4]) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -130,8 +151,14 @@ __device__ __forceinline__ void store_rows(void* dst, int64_t stride, int64_t he
     for (int c = 0; c < Cfg<DP>::DC; ++c) {
       const int d = 4 * tx + 64 * c;
       if (d >= D) continue;               // D is a multiple of 4
-      *reinterpret_cast<float4*>(static_cast<float*>(dst) + r * stride + head_off + d) =
-          make_float4(v[i][c][0], v[i][c][1], v[i][c][2], v[i][c][3]);
+      float4 f;
+      unpk2(v[i][c][0], f.x, f.y);
+      unpk2(v[i][c][1], f.z, f.w);
+      f.x *= mul[i];
+      f.y *= mul[i];
+      f.z *= mul[i];
+      f.w *= mul[i];
+      *reinterpret_cast<float4*>(static_cast<float*>(dst) + r * stride + head_off + d) = f;
     }
   }
 }
@@ -148,11 +175,35 @@ __device__ __forceinline__ void load_pos(float* dst, const Params& p, int64_t r0
     dst[i] = r0 + r < hi ? p.pos[(r0 + r) * p.axes + a] : 0.f;
   }
 }
-__device__ __forceinline__ float distance(const float* pr, int r, const float* pc, int c, int axes) {
-  float d = 0.f;
-  for (int a = 0; a < axes; ++a) d += fabsf(pr[a * B + r] - pc[a * B + c]);
-  return d;
+// City-block distances of the thread's 4 x 4 scores, times mul.
+__device__ __forceinline__ void distances(const Params& p, const float* pr, const float* pc, float mul, float (&d)[4][4]) {
+  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
+#pragma unroll
+  for (int a = 0; a < kMaxAxes; ++a) {
+    if (a >= p.axes) break;
+    const float4 r = *reinterpret_cast<const float4*>(pr + a * B + 4 * ty);
+    float c[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = pc[a * B + tx + 16 * j];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      d[0][j] += fabsf(r.x - c[j]);
+      d[1][j] += fabsf(r.y - c[j]);
+      d[2][j] += fabsf(r.z - c[j]);
+      d[3][j] += fabsf(r.w - c[j]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) d[i][j] *= mul;
 }
+
+// ------------------------------------------------------------- exponentials
 
 // e^x for x <= 0 or so: the product with log2 e is taken to twice FP32's
 // precision, so that the error stays at ex2.approx's 2^-22 for any x; a third
@@ -180,7 +231,7 @@ __device__ __forceinline__ float tanh_fast(float x) {
 // ------------------------------------------------------------------ forward
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_fwd_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) float sm[];
   float* Q = sm;
   float* K = Q + Cfg<DP>::TILE;
@@ -191,7 +242,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_co
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   grid_dep_launch();
   grid_dep_wait();
-  const Work w = work_of(p, blockIdx.x, p.H);
+  const Work w = work_of_row(p, p.H);
   const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)(w.head / (p.H / p.K)) * p.D;
   if (w.doc == p.docs) {
     outside_rows(p, w.tile, [&](int64_t r) {
@@ -209,15 +260,14 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_co
     load_tile<DP>(Q, p.q, p.qs, qh, r0, hi, p.D, p.scale);
     load_pos(pq, p, r0, hi);
     const bool busy = r0 + 8 * (threadIdx.x >> 5) < hi;       // does the warp have a row
-    float m[4], l[4], o[4][Cfg<DP>::DC][4];
+    float m[4], l[4];
+    uint64_t o[4][Cfg<DP>::DC][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
-      for (int c = 0; c < Cfg<DP>::DC; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[i][c][k] = 0.f;
+      for (int c = 0; c < Cfg<DP>::DC; ++c) o[i][c][0] = o[i][c][1] = 0;
     }
     for (int64_t c0 = lo; c0 < hi; c0 += B) {
       __syncthreads();
@@ -229,13 +279,15 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_co
       const int nc = (int)(hi - c0 < B ? hi - c0 : B);
       float s[4][4];
       mm_nt<DP>(Q, K, nc, s);
+      float bias[4][4];
+      distances(p, pq, pk, slope, bias);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         float top = m[i];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (p.cap > 0.f) s[i][j] = p.cap * tanh_fast(s[i][j] * icap);
-          if (p.axes) s[i][j] -= slope * distance(pq, 4 * ty + i, pk, tx + 16 * j, p.axes);
+          s[i][j] -= bias[i][j];
           if (c0 + tx + 16 * j >= hi) s[i][j] = -INFINITY;
           top = fmaxf(top, s[i][j]);
         }
@@ -252,28 +304,26 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_co
           P[(4 * ty + i) * LDP + tx + 16 * j] = s[i][j];
         }
         l[i] = l[i] * fix + sum;          // this thread's columns; joined at the end
+        const uint64_t fix2 = pk2(fix, fix);
 #pragma unroll
         for (int c = 0; c < Cfg<DP>::DC; ++c)
 #pragma unroll
-          for (int k = 0; k < 4; ++k) o[i][c][k] *= fix;
+          for (int k = 0; k < 2; ++k) o[i][c][k] = ptx::mul2(o[i][c][k], fix2);
       }
       __syncwarp();
       mm_nn<DP>(P, V, nc, o);
       __syncwarp();
     }
+    float inv[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
       for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
-      const float inv = 1.f / l[i];
-#pragma unroll
-      for (int c = 0; c < Cfg<DP>::DC; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[i][c][k] *= inv;
+      inv[i] = 1.f / l[i];
       const int64_t r = r0 + 4 * ty + i;
       if (tx == 0 && r < hi) p.lse[(int64_t)w.head * p.N + r] = m[i] + logf(l[i]);
     }
-    store_rows<DP>(p.o, p.os, qh, r0, hi, p.D, o);
+    store_rows<DP>(p.o, p.os, qh, r0, hi, p.D, o, inv);
   }
 }
 
@@ -281,21 +331,21 @@ __global__ void __launch_bounds__(kThreads) attn_simt_fwd_kernel(const __grid_co
 
 // P and du of one 64 x 64 tile from its raw products u (rows and columns as in
 // mm_nt), dP, and the softmax statistics of the query side.
-__device__ __forceinline__ void tile_grad(const Params& p, float u, float dp, float dist, float lse, float delta,
-                                          bool on, float icap, float slope, float& prob, float& du) {
+__device__ __forceinline__ void tile_grad(const Params& p, float u, float dp, float bias, float lse, float delta,
+                                          bool on, float icap, float& prob, float& du) {
   float slope_u = 1.f, s = u;
   if (p.cap > 0.f) {
     const float t = tanh_fast(u * icap);
     s = p.cap * t;
     slope_u = 1.f - t * t;
   }
-  if (p.axes) s -= slope * dist;
+  s -= bias;
   prob = on ? exp_fast(s - lse) : 0.f;
   du = on ? prob * (dp - delta) * slope_u : 0.f;
 }
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_dq_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) float sm[];
   float* Q = sm;
   float* G = Q + Cfg<DP>::TILE;
@@ -308,7 +358,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const __grid_con
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   grid_dep_launch();
   grid_dep_wait();
-  const Work w = work_of(p, blockIdx.x, p.H);
+  const Work w = work_of_row(p, p.H);
   const int64_t qh = (int64_t)w.head * p.D, kh = (int64_t)(w.head / (p.H / p.K)) * p.D;
   if (w.doc == p.docs) {
     outside_rows(p, w.tile, [&](int64_t r) { clear_row(p.dq, p.dqs, qh, r, p.D); });
@@ -338,16 +388,15 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const __grid_con
     }
     __syncthreads();
     const bool busy = r0 + 8 * (threadIdx.x >> 5) < hi;
-    float lse[4], delta[4], acc[4][Cfg<DP>::DC][4];
+    float lse[4], delta[4];
+    uint64_t acc[4][Cfg<DP>::DC][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int64_t r = r0 + 4 * ty + i;
       lse[i] = r < hi ? p.lse[(int64_t)w.head * p.N + r] : 0.f;
       delta[i] = dl[4 * ty + i];
 #pragma unroll
-      for (int c = 0; c < Cfg<DP>::DC; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][c][k] = 0.f;
+      for (int c = 0; c < Cfg<DP>::DC; ++c) acc[i][c][0] = acc[i][c][1] = 0;
     }
     for (int64_t c0 = lo; c0 < hi; c0 += B) {
       __syncthreads();
@@ -360,32 +409,28 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dq_kernel(const __grid_con
       float u[4][4], dp[4][4];
       mm_nt<DP>(Q, K, nc, u);
       mm_nt<DP>(G, V, nc, dp);
+      float bias[4][4];
+      distances(p, pq, pk, slope, bias);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int c = tx + 16 * j, r = 4 * ty + i;
           float prob, du;
-          tile_grad(p, u[i][j], dp[i][j], distance(pq, r, pk, c, p.axes), lse[i], delta[i],
-                    r0 + r < hi && c0 + c < hi, icap, slope, prob, du);
+          tile_grad(p, u[i][j], dp[i][j], bias[i][j], lse[i], delta[i], r0 + r < hi && c0 + c < hi, icap, prob, du);
           P[r * LDP + c] = du;
         }
       __syncwarp();
       mm_nn<DP>(P, K, nc, acc);
       __syncwarp();
     }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int c = 0; c < Cfg<DP>::DC; ++c)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) acc[i][c][k] *= p.scale;
-    store_rows<DP>(p.dq, p.dqs, qh, r0, hi, p.D, acc);
+    const float mul[4] = {p.scale, p.scale, p.scale, p.scale};
+    store_rows<DP>(p.dq, p.dqs, qh, r0, hi, p.D, acc, mul);
   }
 }
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_dkv_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) float sm[];
   float* K = sm;
   float* V = K + Cfg<DP>::TILE;
@@ -398,7 +443,7 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const __grid_co
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   grid_dep_launch();
   grid_dep_wait();
-  const Work w = work_of(p, blockIdx.x, p.K);
+  const Work w = work_of_row(p, p.K);
   const int rep = p.H / p.K;
   const int64_t kh = (int64_t)w.head * p.D;
   if (w.doc == p.docs) {
@@ -417,13 +462,13 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const __grid_co
     load_tile<DP>(V, p.v, p.vs, kh, r0, hi, p.D, 1.f);
     load_pos(pk, p, r0, hi);
     const bool busy = r0 + 8 * (threadIdx.x >> 5) < hi;
-    float dk[4][Cfg<DP>::DC][4], dv[4][Cfg<DP>::DC][4];
+    uint64_t dk[4][Cfg<DP>::DC][2], dv[4][Cfg<DP>::DC][2];
 #pragma unroll
     for (int i = 0; i < 4; ++i)
 #pragma unroll
       for (int c = 0; c < Cfg<DP>::DC; ++c)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) dk[i][c][k] = dv[i][c][k] = 0.f;
+        for (int k = 0; k < 2; ++k) dk[i][c][k] = dv[i][c][k] = 0;
     for (int g = 0; g < rep; ++g) {
       const int head = w.head * rep + g;
       const int64_t qh = (int64_t)head * p.D;
@@ -444,14 +489,16 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const __grid_co
         float u[4][4], dp[4][4];
         mm_nt<DP>(K, Q, nc, u);
         mm_nt<DP>(V, G, nc, dp);
+        float bias[4][4];
+        distances(p, pk, pq, slope, bias);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const int c = tx + 16 * j, r = 4 * ty + i;
             float prob, du;
-            tile_grad(p, u[i][j], dp[i][j], distance(pk, r, pq, c, p.axes), stat[c], stat[B + c],
-                      r0 + r < hi && c0 + c < hi, icap, slope, prob, du);
+            tile_grad(p, u[i][j], dp[i][j], bias[i][j], stat[c], stat[B + c], r0 + r < hi && c0 + c < hi, icap, prob,
+                      du);
             P[r * LDP + c] = prob;
             dp[i][j] = du;
           }
@@ -467,8 +514,9 @@ __global__ void __launch_bounds__(kThreads) attn_simt_dkv_kernel(const __grid_co
         __syncwarp();
       }
     }
-    store_rows<DP>(p.dk, p.dks, kh, r0, hi, p.D, dk);
-    store_rows<DP>(p.dv, p.dvs, kh, r0, hi, p.D, dv);
+    const float one[4] = {1.f, 1.f, 1.f, 1.f};
+    store_rows<DP>(p.dk, p.dks, kh, r0, hi, p.D, dk, one);
+    store_rows<DP>(p.dv, p.dvs, kh, r0, hi, p.D, dv, one);
   }
 }
 

@@ -21,7 +21,7 @@
 // The work is bound by memory: a row is read once into registers (16-byte
 // vectors, kept packed in the element type) and everything follows from there.
 // A row belongs to `lpr` lanes of a warp (a power of two) holding VPT vectors
-// each, or to a whole block when it is longer than 32 lanes x 4 vectors.  lpr
+// each, or to a whole block when it is longer than 32 lanes hold.  lpr
 // and VPT are the pair that leaves the fewest lanes idle (F = 96 in 16 bits:
 // 12 vectors = 4 lanes x 3; 768: 32 x 3), so short rows share a warp.  Each
 // thread keeps the same columns over all its rows, so w and b are read once
@@ -31,8 +31,12 @@
 namespace eqlin {
 namespace norm {
 
-constexpr int kThreads = 256;
-constexpr int kMaxVpt = 4;
+// Forward blocks per SM: what the registers of two rows leave.  12608 x 768
+// with a residual, inputs beyond L2: 15.8 us at 5 blocks, 19.5 at 8 (spilled);
+// 50000 x 120: 9.3 us at 8, 12.8 at 5.
+constexpr int kFwdThreads = 128;
+constexpr int fwd_blocks(int vpt) { return vpt == 1 ? 8 : vpt == 2 ? 6 : 5; }
+constexpr int kBwdThreads = 128, kBwdBlocks = 3;   // backward: room for two rows in registers, 12 warps an SM
 // Threads of a block that shares one row, at most: 4 vectors each cover 8192
 // features, and the backward's column sums fit its registers.
 template <typename E> constexpr int kBlockThreads = sizeof(E) == 4 ? 512 : 256;
@@ -140,7 +144,7 @@ __device__ __forceinline__ Place place(const Params& p) {
 // 4 divides T (w, b and the column sums then take a quarter of the registers),
 // else 1.
 template <typename E, int VPT, int TT, bool BLOCK>
-__global__ void __launch_bounds__(BLOCK ? kBlockThreads<E> : kThreads)
+__global__ void __launch_bounds__(BLOCK ? kBlockThreads<E> : kFwdThreads, BLOCK ? 1 : fwd_blocks(VPT))
 norm_fwd_kernel(const __grid_constant__ Params p) {
   constexpr int V = 16 / sizeof(E), CG = V / TT;
   __shared__ float red[32];
@@ -161,25 +165,36 @@ norm_fwd_kernel(const __grid_constant__ Params p) {
   const float inv = 1.f / (float)p.F;
   // the loop's trip count is the same for all threads of a warp: shuffles stay whole
   const int64_t first = at.row - (BLOCK ? 0 : (threadIdx.x & 31) / p.lpr);
+  // the next row is on its way while this one is worked on: a warp's own loads
+  // are what keeps memory busy
+  uint4 x[VPT], r[VPT];
+  auto load = [&](int64_t row) {
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int vec = at.lane + j * p.lpr;
+      const int64_t off = row * p.nvec + vec;
+      x[j] = r[j] = make_uint4(0, 0, 0, 0);
+      if (row < p.N && vec < p.nvec) {
+        x[j] = ld_stream(static_cast<const uint4*>(p.x) + off);
+        if (p.res) r[j] = ld_stream(static_cast<const uint4*>(p.res) + off);
+      }
+    }
+  };
+  load(at.row);
   for (int64_t base = first, row = at.row; base < p.N; base += at.step, row += at.step) {
     const bool live = row < p.N;
     float s[VPT][V];
     float acc[1] = {0.f};
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
-      const int vec = at.lane + j * p.lpr;
-      const bool on = live && vec < p.nvec;
-      uint4 u = make_uint4(0, 0, 0, 0);
-      const int64_t off = row * p.nvec + vec;
-      if (on) u = ld_stream(static_cast<const uint4*>(p.x) + off);
-      unpack<E>(u, s[j]);
-      if (p.res && on) {
-        float r[V];
-        unpack<E>(ld_stream(static_cast<const uint4*>(p.res) + off), r);
+      unpack<E>(x[j], s[j]);
+      if (p.res) add<E>(r[j], s[j]);
+    }
+    load(row + at.step);
 #pragma unroll
-        for (int i = 0; i < V; ++i) s[j][i] += r[i];
-        static_cast<uint4*>(p.sum)[off] = pack<E>(s[j]);
-      }
+    for (int j = 0; j < VPT; ++j) {
+      const int vec = at.lane + j * p.lpr;
+      if (p.res && live && vec < p.nvec) static_cast<uint4*>(p.sum)[row * p.nvec + vec] = pack<E>(s[j]);
 #pragma unroll
       for (int i = 0; i < V; ++i) acc[0] += s[j][i];
     }
@@ -211,8 +226,33 @@ norm_fwd_kernel(const __grid_constant__ Params p) {
   }
 }
 
+// What the backward reads of a row: x, gy, and where given res and gs.
+template <int VPT, bool RES> struct Row {
+  uint4 x[VPT], g[VPT], s[VPT], r[RES ? VPT : 1];
+  float mean, rstd;
+  __device__ __forceinline__ void load(const Params& p, int64_t row, int lane) {
+    const bool live = row < p.N;
+    mean = live ? p.mean[row] : 0.f;
+    rstd = live ? p.rstd[row] : 0.f;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+      const int vec = lane + j * p.lpr;
+      const int64_t at = row * p.nvec + vec;
+      x[j] = g[j] = s[j] = make_uint4(0, 0, 0, 0);
+      if (RES) r[j] = x[j];
+      if (live && vec < p.nvec) {
+        x[j] = ld_stream(static_cast<const uint4*>(p.x) + at);
+        g[j] = ld_stream(static_cast<const uint4*>(p.gy) + at);
+        if (RES) r[j] = ld_stream(static_cast<const uint4*>(p.res) + at);
+        if (p.gs) s[j] = ld_stream(static_cast<const uint4*>(p.gs) + at);
+      }
+    }
+  }
+};
+
 template <typename E, int VPT, int TT, bool BLOCK, bool RES>
-__global__ void __launch_bounds__(BLOCK ? kBlockThreads<E> : kThreads)
+__global__ void __launch_bounds__(BLOCK ? kBlockThreads<E> : kBwdThreads,
+                                  BLOCK ? (sizeof(E) == 2 && VPT <= 2 ? 2 : 1) : kBwdBlocks)
 norm_bwd_kernel(const __grid_constant__ Params p) {
   constexpr int V = 16 / sizeof(E), CG = V / TT;
   extern __shared__ float colsum[];        // [2][F / TT]: dw, db of this block
@@ -233,28 +273,22 @@ norm_bwd_kernel(const __grid_constant__ Params p) {
   }
   const float inv = 1.f / (float)p.F;
   const int64_t first = at.row - (BLOCK ? 0 : (threadIdx.x & 31) / p.lpr);
+  // Rows are kept packed, and the next one is on its way while this one is
+  // worked on: a warp's own loads are what keeps memory busy.
+  Row<VPT, RES> cur, nxt;
+  cur.load(p, at.row, at.lane);
   for (int64_t base = first, row = at.row; base < p.N; base += at.step, row += at.step) {
     const bool live = row < p.N;
-    uint4 ug[VPT], ux[VPT], ur[VPT];       // kept packed between the two passes over them
-    const float mu = live ? p.mean[row] : 0.f, rstd = live ? p.rstd[row] : 0.f;
-#pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-      const int vec = at.lane + j * p.lpr;
-      ux[j] = ug[j] = ur[j] = make_uint4(0, 0, 0, 0);
-      if (live && vec < p.nvec) {
-        if (RES) ur[j] = ld_stream(static_cast<const uint4*>(p.res) + row * p.nvec + vec);
-        ux[j] = ld_stream(static_cast<const uint4*>(p.x) + row * p.nvec + vec);
-        ug[j] = ld_stream(static_cast<const uint4*>(p.gy) + row * p.nvec + vec);
-      }
-    }
+    nxt.load(p, row + at.step, at.lane);
+    const float mu = cur.mean, rstd = cur.rstd;
     float m[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
       if (!(live && at.lane + j * p.lpr < p.nvec)) continue;
       float x[V], g[V];
-      unpack<E>(ux[j], x);
-      if (RES) add<E>(ur[j], x);
-      unpack<E>(ug[j], g);
+      unpack<E>(cur.x[j], x);
+      if (RES) add<E>(cur.r[j], x);
+      unpack<E>(cur.g[j], g);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float xh = (x[i] - mu) * rstd, gw = g[i] * w[j][i / TT];
@@ -272,21 +306,18 @@ norm_bwd_kernel(const __grid_constant__ Params p) {
       const int vec = at.lane + j * p.lpr;
       if (!(live && vec < p.nvec)) continue;
       float x[V], g[V];
-      unpack<E>(ux[j], x);
-      if (RES) add<E>(ur[j], x);
-      unpack<E>(ug[j], g);
+      unpack<E>(cur.x[j], x);
+      if (RES) add<E>(cur.r[j], x);
+      unpack<E>(cur.g[j], g);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float xh = (x[i] - mu) * rstd;
         x[i] = rstd * (fmaf(g[i], w[j][i / TT], -m[0]) - xh * m[1]);
       }
-      if (p.gs) {
-        unpack<E>(ld_stream(static_cast<const uint4*>(p.gs) + row * p.nvec + vec), g);
-#pragma unroll
-        for (int i = 0; i < V; ++i) x[i] += g[i];
-      }
+      if (p.gs) add<E>(cur.s[j], x);
       static_cast<uint4*>(p.y)[row * p.nvec + vec] = pack<E>(x);
     }
+    cur = nxt;
   }
   // Column sums of the block in a fixed order: rows that share a warp by
   // shuffles, then the warps one after the other.
@@ -365,19 +396,21 @@ __global__ void __launch_bounds__(1024) norm_cols_kernel(const float* part, int 
 // ------------------------------------------------------------------ launch
 
 constexpr int kMaxF = 8192;
-// Blocks of the backward at most: 2 per SM of a B200 (its registers allow
-// that); the partial sums are as many rows.
-constexpr int kMaxParts = 296;
+// Blocks of the backward at most, kBwdBlocks for each SM of a B200; the
+// partial sums are as many rows.
+constexpr int kMaxParts = 148 * kBwdBlocks;
 
 struct Shape {
   int vpt, lpr;
   bool block;
 };
-inline Shape shape_of(int nvec, int max_threads) {
+inline Shape shape_of(int nvec, int T, int max_threads) {
+  // vectors per thread whose two rows and column sums fit the backward's registers
+  const int most = T % 4 == 0 ? 3 : 2;
   Shape best{0, 0, false};
-  if (nvec <= 32 * kMaxVpt) {
+  if (nvec <= 32 * most) {
     int waste = 1 << 30;
-    for (int vpt = 1; vpt <= kMaxVpt; ++vpt) {
+    for (int vpt = 1; vpt <= most; ++vpt) {
       int lpr = 1;
       while (lpr * vpt < nvec) lpr *= 2;
       if (lpr > 32) continue;
@@ -404,7 +437,7 @@ int sm_count() {
 
 template <typename E, int TT, int VPT>
 cudaError_t launch_vpt(const Params& p, const Shape& s, bool bwd, int blocks, cudaStream_t st) {
-  const int threads = s.block ? s.lpr : kThreads;
+  const int threads = s.block ? s.lpr : bwd ? kBwdThreads : kFwdThreads;
   const size_t smem = bwd ? (size_t)2 * (p.F / TT) * sizeof(float) : 0;
   void (*k)(Params) = bwd ? (p.res ? (s.block ? norm_bwd_kernel<E, VPT, TT, true, true>
                                               : norm_bwd_kernel<E, VPT, TT, false, true>)
@@ -426,7 +459,7 @@ cudaError_t launch_tt(const Params& p, const Shape& s, bool bwd, int blocks, cud
     case 1: return launch_vpt<E, TT, 1>(p, s, bwd, blocks, st);
     case 2: return launch_vpt<E, TT, 2>(p, s, bwd, blocks, st);
     case 3: return launch_vpt<E, TT, 3>(p, s, bwd, blocks, st);
-    default: return launch_vpt<E, TT, 4>(p, s, bwd, blocks, st);
+    default: return launch_vpt<E, TT, 4>(p, s, bwd, blocks, st);   // a block per row
   }
 }
 
@@ -489,10 +522,10 @@ extern "C" eqlin_status_t eqlin_norm_forward(int T, int64_t Cp, eqlin_dtype_t dt
   p.mean = mean;
   p.rstd = rstd;
   p.eps = eps;
-  const norm::Shape s = norm::shape_of(p.nvec, norm::block_threads(dtype));
+  const norm::Shape s = norm::shape_of(p.nvec, T, norm::block_threads(dtype));
   p.lpr = s.lpr;
-  const int64_t rows = s.block ? 1 : norm::kThreads / s.lpr;
-  const int64_t want = (N + rows - 1) / rows, cap = 8 * (int64_t)norm::sm_count();
+  const int64_t rows = s.block ? 1 : norm::kFwdThreads / s.lpr;
+  const int64_t want = (N + rows - 1) / rows, cap = norm::fwd_blocks(s.vpt) * (int64_t)norm::sm_count();
   if (cap == 0) return EQLIN_ERR_CUDA;
   const cudaError_t e = norm::dispatch(dtype, p, s, false, (int)(want < cap ? want : cap),
                                        static_cast<cudaStream_t>(stream));
@@ -530,9 +563,9 @@ extern "C" eqlin_status_t eqlin_norm_backward(int T, int64_t Cp, eqlin_dtype_t d
   p.rstd = const_cast<float*>(rstd);
   p.y = dx;
   p.part = static_cast<float*>(workspace);
-  const norm::Shape s = norm::shape_of(p.nvec, norm::block_threads(dtype));
+  const norm::Shape s = norm::shape_of(p.nvec, T, norm::block_threads(dtype));
   p.lpr = s.lpr;
-  const int64_t rows = s.block ? 1 : norm::kThreads / s.lpr;
+  const int64_t rows = s.block ? 1 : norm::kBwdThreads / s.lpr;
   const int64_t want = (N + rows - 1) / rows, cap = norm::kMaxParts;
   const int blocks = (int)(want < cap ? want : cap);
   cudaError_t e = norm::dispatch(dtype, p, s, true, blocks, cs);

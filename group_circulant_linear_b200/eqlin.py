@@ -350,7 +350,8 @@ class _On:
         if self.prev is not None:
             torch.cuda.set_device(self.index)
         if self.stream is None:
-            return torch.cuda.current_stream().cuda_stream
+            # torch.cuda.current_stream().cuda_stream, without the 3 us of building a Stream
+            return torch._C._cuda_getCurrentRawStream(self.index)
         return self.stream.cuda_stream if hasattr(self.stream, "cuda_stream") else int(self.stream)
 
     def __exit__(self, *exc):

@@ -45,28 +45,13 @@ struct Params {
   const float* slopes;    // [H]
   int axes;               // 0: no bias
   int H, K, D;
-  int hint;               // work items per (document, head); each walks the tiles hint apart
+  int hint;               // f32: blocks per (document, head), each walks the tiles hint apart;
+                          // else tiles per document (equal lengths) or 128-token slots (packed)
   uint32_t items;         // work items in all
   float scale, cap;
   int* err;               // error record (eqlin_wait.cuh), or null
   uint32_t wait_limit;
 };
-
-// A work item's document, head and first tile: tiles vary fastest, so that
-// blocks which share keys run together.
-struct Work {
-  int64_t doc;
-  int head, tile;
-};
-__device__ __forceinline__ Work work_of(const Params& p, uint32_t item, int heads) {
-  const uint32_t rest = item / (uint32_t)p.hint;
-  Work w;
-  w.tile = (int)(item - rest * (uint32_t)p.hint);
-  const uint32_t d = rest / (uint32_t)heads;
-  w.head = (int)(rest - d * (uint32_t)heads);
-  w.doc = d;
-  return w;
-}
 
 // A document's tokens [lo, hi).  Offsets are forced into [0, N] and into
 // order, so that wrong ones cannot lead out of the tensors.
@@ -78,16 +63,6 @@ __device__ __forceinline__ void doc_range(const Params& p, int64_t doc, int64_t&
   }
   lo = min(max((int64_t)p.offsets[doc], (int64_t)0), p.N);
   hi = min(max((int64_t)p.offsets[doc + 1], lo), p.N);
-}
-
-// Items whose document index is `docs` (packed calls only) clear the rows
-// outside all documents: [0, first offset) and [last offset, N).
-template <typename F>
-__device__ __forceinline__ void outside_rows(const Params& p, int tile, F&& clear) {
-  const int64_t a = min(max((int64_t)p.offsets[0], (int64_t)0), p.N);
-  const int64_t b = min(max((int64_t)p.offsets[p.docs], a), p.N);
-  for (int64_t r = tile; r < a; r += p.hint) clear(r);
-  for (int64_t r = b + tile; r < p.N; r += p.hint) clear(r);
 }
 
 }  // namespace attn

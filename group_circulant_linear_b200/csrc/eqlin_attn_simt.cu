@@ -40,6 +40,20 @@ template <int DP> struct Cfg {
   static constexpr int DC = (DP + 63) / 64;   // float4 groups of a thread's output columns
 };
 
+// Blocks whose document index is `docs` (packed calls only) clear the rows
+// outside all documents: [0, first offset) and [last offset, N).
+template <typename F>
+__device__ __forceinline__ void outside_rows(const Params& p, int tile, F&& clear) {
+  const int64_t a = min(max((int64_t)p.offsets[0], (int64_t)0), p.N);
+  const int64_t b = min(max((int64_t)p.offsets[p.docs], a), p.N);
+  for (int64_t r = tile; r < a; r += p.hint) clear(r);
+  for (int64_t r = b + tile; r < p.N; r += p.hint) clear(r);
+}
+
+struct Work {
+  int64_t doc;
+  int head, tile;
+};
 // A block's work: the first tile of every document and head before any second
 // one, so that the short last tiles fill the gaps of the last wave (197 tokens
 // of 16 images in 6 heads are 288 full tiles, one wave, and 96 of 5 rows).

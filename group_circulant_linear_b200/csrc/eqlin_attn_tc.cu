@@ -40,7 +40,7 @@ template <int DP, int CW_> struct FwdCfg {
   static constexpr int P_COL = SEP ? CW : 0, O_COL = SEP ? CW + CW / 2 : CW;
   static constexpr int TMEM = O_COL + DP <= 128 ? 128 : 256;
   static constexpr int POS = (SLOTS / 2) * kMaxAxes * CW * 4;
-  static constexpr int SMEM = OWN + SLOTS * MOV + POS + 4 * STAGE + NBAR * 8 + 64 + 1024;
+  static constexpr int SMEM = OWN + SLOTS * MOV + POS + 4 * STAGE + NBAR * 8 + 32 + kListInts * 4 + 1024;
   static_assert(O_COL + DP <= TMEM, "TMEM columns");
   static_assert(2 * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
@@ -69,21 +69,16 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
   int* local_err = abort_word + 1;
+  int* list = local_err + 4;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
-  if (p.offsets) {                                            // one item per block: it may have nothing to do
-    const Work w = work_of(p, blockIdx.x, p.H);
-    if (w.doc == p.docs) {
-      const int64_t qh = (int64_t)w.head * p.D;
-      outside_rows(p, w.tile, [&](int64_t r) {
-        for (int d = threadIdx.x; d < p.D; d += kThreads) static_cast<E*>(p.o)[r * p.os + qh + d] = Elem<E>::from_f(0.f);
-        if (threadIdx.x == 0) p.lse[(int64_t)w.head * p.N + r] = 0.f;
+  const uint32_t count = begin(p, p.H, list, [&](int head, int64_t r) {
+        for (int d = threadIdx.x; d < p.D; d += kThreads)
+          static_cast<E*>(p.o)[r * p.os + (int64_t)head * p.D + d] = Elem<E>::from_f(0.f);
+        if (threadIdx.x == 0) p.lse[(int64_t)head * p.N + r] = 0.f;
       });
-      return;
-    }
-    if (item_of<false>(p, blockIdx.x, p.H).tiles == 0) return;
-  }
+  if (count == 0) return;
   const int rep = p.H / p.K;
 
   if (threadIdx.x == 0) {
@@ -125,37 +120,34 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
     Side<AXES, false, CW> sidev;
     uint32_t item = 0, owns = 0;
     bool ok = true;
-    for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
-      const Item w = item_of<false>(p, work, p.H);
+    for (uint32_t i = 0; ok && i < count; ++i) {
+      const Tile w = tile_at(p, p.H, list, i);
       const int lo = w.lo, hi = w.hi, kv_head = w.head / rep, key_tiles = (hi - lo - 1) / CW + 1;
       if (AXES) sidev.fetch(p, w.head, lo, hi, lane);
-      for (int t = 0; ok && t < w.tiles; ++t) {
-        ok = claim<DP, CW, 1>(tails, q_empty, (owns & 1) ^ 1, ring, land, kv_full, wait, site(K_ATTN_FWD, 2, 0), owns, lane);
-        if (!ok) break;
-        if (lane == 0) {
-          expect_bytes(q_full, C::OWN);
-          tma_rows<DP, ROWS>(smem, &maps.m[0], w.head, w.first + t * p.hint * ROWS, q_full);
-        }
-        mbar_arrive(q_full);
-        ++owns;
-        for (int j = 0; ok && j < key_tiles; ++j) {
-          const int c0 = lo + j * CW, nc = min(hi - c0, CW);
+      ok = claim<DP, CW, 1>(tails, q_empty, (owns & 1) ^ 1, ring, land, kv_full, wait, site(K_ATTN_FWD, 2, 0), owns, lane);
+      if (!ok) break;
+      if (lane == 0) {
+        expect_bytes(q_full, C::OWN);
+        tma_rows<DP, ROWS>(smem, &maps.m[0], w.head, w.first, q_full);
+      }
+      mbar_arrive(q_full);
+      ++owns;
+      for (int j = 0; ok && j < key_tiles; ++j) {
+        const int c0 = lo + j * CW, nc = min(hi - c0, CW);
 #pragma unroll 1
-          for (int kv = 0; ok && kv < 2; ++kv) {
-            const uint32_t slot = item % C::SLOTS;
-            ok = claim<DP, CW, 1>(tails, kv_empty + slot, ((item / C::SLOTS) & 1) ^ 1, ring, land, kv_full, wait,
-                                    site(K_ATTN_FWD, 2, 1), item, lane);
-            if (!ok) break;
-            // positions go with V: its slot is free once the softmax has used them
-            if (AXES && kv) {
-              sidev.store(spos + (slot >> 1) * kMaxAxes * CW, 0.f, 0.f, lane);
-              if (j + 1 < key_tiles || t + 1 < w.tiles)
-                sidev.fetch(p, w.head, j + 1 < key_tiles ? c0 + CW : lo, hi, lane);
-            }
-            ok = bring<DP, CW, 1>(tails, slot, ring, land, kv_full, &maps.m[1 + kv], kv_head, c0, nc, wait,
-                                    site(K_ATTN_FWD, 2, 2), lane);
-            ++item;
+        for (int kv = 0; ok && kv < 2; ++kv) {
+          const uint32_t slot = item % C::SLOTS;
+          ok = claim<DP, CW, 1>(tails, kv_empty + slot, ((item / C::SLOTS) & 1) ^ 1, ring, land, kv_full, wait,
+                                  site(K_ATTN_FWD, 2, 1), item, lane);
+          if (!ok) break;
+          // positions go with V: its slot is free once the softmax has used them
+          if (AXES && kv) {
+            sidev.store(spos + (slot >> 1) * kMaxAxes * CW, 0.f, 0.f, lane);
+            if (j + 1 < key_tiles) sidev.fetch(p, w.head, c0 + CW, hi, lane);
           }
+          ok = bring<DP, CW, 1>(tails, slot, ring, land, kv_full, &maps.m[1 + kv], kv_head, c0, nc, wait,
+                                  site(K_ATTN_FWD, 2, 2), lane);
+          ++item;
         }
       }
     }
@@ -189,34 +181,32 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
       commit(leader, kv_empty + slot);
       return true;
     };
-    for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
-      const Item w = item_of<true>(p, work, p.H);
+    for (; ok && owns < count; ++owns) {
+      const Tile w = tile_at(p, p.H, list, owns);
       lo = w.lo;
       hi = w.hi;
       const int key_tiles = (hi - lo - 1) / CW + 1;
-      for (int t = 0; ok && t < w.tiles; ++t, ++owns) {
-        ok = wwait_all(q_full, owns & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 0), owns) && qk(0, item, step);
-        for (int j = 0; ok && j < key_tiles; ++j, item += 2, ++step) {
-          const bool more = j + 1 < key_tiles;
-          if (C::SEP && more) ok = qk(j + 1, item + 2, step + 1);
-          if (!more) commit(leader, q_empty);                 // every product with this Q is issued
-          const uint32_t vi = item + 1;
-          const int slot = vi % C::SLOTS;
-          ok = ok && wwait_all(kv_full + slot, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 1), vi) &&
-               wwait_all(p_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 3), step);
-          if (!ok) break;
-          tc_fence_after();
-          const int steps = (min(hi - lo - j * CW, CW) + 15) / 16;
-          const uint32_t v_lo = ring_v + slot * (C::MOV >> 4);
+      ok = wwait_all(q_full, owns & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 0), owns) && qk(0, item, step);
+      for (int j = 0; ok && j < key_tiles; ++j, item += 2, ++step) {
+        const bool more = j + 1 < key_tiles;
+        if (C::SEP && more) ok = qk(j + 1, item + 2, step + 1);
+        if (!more) commit(leader, q_empty);                 // every product with this Q is issued
+        const uint32_t vi = item + 1;
+        const int slot = vi % C::SLOTS;
+        ok = ok && wwait_all(kv_full + slot, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 1), vi) &&
+             wwait_all(p_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 1, 3), step);
+        if (!ok) break;
+        tc_fence_after();
+        const int steps = (min(hi - lo - j * CW, CW) + 15) / 16;
+        const uint32_t v_lo = ring_v + slot * (C::MOV >> 4);
 #pragma unroll
-          for (int s = 0; s < CW / 16; ++s)
-            if (s < steps)
-              mma_ts(leader, tmem + C::O_COL, tmem + (C::SEP ? C::P_COL + 8 * s : 32 * (s >> 1) + 8 * (s & 1)), v_lo + s * (2048 >> 4), v_hi, id_o,
-                     j > 0 || s > 0);
-          commit(leader, o_full);
-          commit(leader, kv_empty + slot);
-          if (!C::SEP && more) ok = qk(j + 1, item + 2, step + 1);   // in order behind the product that reads P
-        }
+        for (int s = 0; s < CW / 16; ++s)
+          if (s < steps)
+            mma_ts(leader, tmem + C::O_COL, tmem + (C::SEP ? C::P_COL + 8 * s : 32 * (s >> 1) + 8 * (s & 1)), v_lo + s * (2048 >> 4), v_hi, id_o,
+                   j > 0 || s > 0);
+        commit(leader, o_full);
+        commit(leader, kv_empty + slot);
+        if (!C::SEP && more) ok = qk(j + 1, item + 2, step + 1);   // in order behind the product that reads P
       }
     }
     if (!ok && lane == 0) raise_abort(abort_flag, err);
@@ -227,185 +217,183 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
     const uint32_t my = tmem + ((uint32_t)(warp * 32) << 16);
     uint32_t step = 0;
     bool ok = true;
-    for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
-      const Item w = item_of<false>(p, work, p.H);
+    for (uint32_t i = 0; ok && i < count; ++i) {
+      const Tile w = tile_at(p, p.H, list, i);
       const int lo = w.lo, hi = w.hi, key_tiles = (hi - lo - 1) / CW + 1;
       const int64_t qh = (int64_t)w.head * p.D;
       const Score sc = score_of(p, w.head);
-      for (int t = 0; ok && t < w.tiles; ++t) {
-        const int r0 = w.first + t * p.hint * ROWS + warp * 32;   // the warp's first row
-        const bool any = r0 < hi, live = lane < hi - r0;
-        const int64_t row = (int64_t)r0 + lane;
-        float own[AXES ? AXES : 1];
+      const int r0 = w.first + warp * 32;   // the warp's first row
+      const bool any = r0 < hi, live = lane < hi - r0;
+      const int64_t row = (int64_t)r0 + lane;
+      float own[AXES ? AXES : 1];
 #pragma unroll
-        for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
-        float m = -INFINITY, l = 0.f;                           // m in base-2 units
-        for (int j = 0; j < key_tiles; ++j, ++step) {
-          const int nc = min(hi - lo - j * CW, CW);
-          // S is there; without SEP with it, in order, every earlier product
-          ok = wwait_all(s_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 0), step);
-          const uint32_t vi = 2 * step + 1;
-          if (AXES && ok)
-            ok = wwait_all(kv_full + vi % C::SLOTS, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 1), step);
-          if (!ok) break;
-          tc_fence_after();
-          uint32_t raw[CW];
-          float* s = reinterpret_cast<float*>(raw);
-          if (any) {
-            const float* pos = spos + ((vi % C::SLOTS) >> 1) * kMaxAxes * CW;
-            auto load = [&] {
-#pragma unroll
-              for (int c = 0; c < CW / 32; ++c)
-                if (c * 32 < nc) tmem_ld32(my + c * 32, raw + c * 32);
-              tmem_wait_ld();
-#pragma unroll
-              for (int c = 0; c < CW / 32; ++c) tie32(raw + c * 32);
-            };
-            // cap, bias and -inf past the document's end for one chunk of which `left` columns are inside
-            auto chunk = [&](float* v, int c, int left) {
-              if (CAP && left < 32) {                         // what lies past the end must not choose the tanh
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (i >= left) v[i] = 0.f;
-              }
-              transform32<AXES, CAP, CW>(v, pos, c * 32, own, sc, CAP && all_small<32>(v, sc, live));
-              if (left < 32) {
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (i >= left) v[i] = -INFINITY;
-              }
-            };
-            if constexpr (!C::SEP) {
-              load();
-#pragma unroll
-              for (int c = 0; c < CW / 32; ++c)
-                if (c * 32 < nc) chunk(s + c * 32, c, nc - c * 32);
-            } else {
-              bool fast = nc == CW;
-              if (fast) {
-                load();
-                if (CAP) fast = all_small<CW>(s, sc, live);
-              }
-              if (fast) {
-#pragma unroll
-                for (int c = 0; c < CW / 32; ++c) transform32<AXES, CAP, CW>(s + c * 32, pos, c * 32, own, sc, true);
-              } else {
-                // a document's last tile, or scores near the cap: through TMEM in a rolled loop (both forms of the
-                // tanh unrolled over 128 columns would not fit the instruction cache)
-#pragma unroll 1
-                for (int c = 0; c * 32 < nc; ++c) {
-                  uint32_t r[32];
-                  tmem_ld32(my + c * 32, r);
-                  tmem_wait_ld();
-                  tie32(r);
-                  chunk(reinterpret_cast<float*>(r), c, nc - c * 32);
-                  tmem_st_32x32b_x16(my + c * 32, r);
-                  tmem_st_32x32b_x16(my + c * 32 + 16, r + 16);
-                }
-                tmem_wait_st();
-                load();
-              }
-            }
-          }
-          if (C::SEP) {
-            tc_fence_before();
-            mbar_arrive(s_free);
-          }
-          float top = -INFINITY;
-          if (any) {
-#pragma unroll
-            for (int c = 0; c < CW / 32; ++c) {
-              if (c * 32 >= nc) continue;
-              const float* v = s + c * 32;
-              float t0 = top, t1 = v[0];
-#pragma unroll
-              for (int i = 1; i < 31; i += 3) {               // three-way maxima, two chains
-                t0 = fmaxf(fmaxf(t0, v[i]), v[i + 1]);
-                t1 = fmaxf(t1, v[i + 2]);
-              }
-              top = fmaxf(fmaxf(t0, t1), v[31]);
-            }
-            top *= sc.scale2;                                 // scale > 0
-          }
-          if (C::SEP && j > 0) {                              // P's columns, and O, are free once the last product is done
-            ok = wwait_all(o_full, (step - 1) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 2), step);
-            if (!ok) break;
-            tc_fence_after();
-          }
-          if (any) {
-            if (j == 0) {
-              m = top;
-            } else {
-              const bool grow = top > m + kLag;
-              if (__any_sync(0xffffffffu, grow)) {
-                const float fix = grow ? ex2(m - top) : 1.f;
-                l *= fix;
-                if (grow) m = top;
-#pragma unroll 1
-                for (int c = 0; c < d16; ++c) {
-                  uint32_t o[16];
-                  tmem_ld_32x32b_x16(my + C::O_COL + c * 16, o);
-                  tmem_wait_ld();
-                  tie16(o);
-#pragma unroll
-                  for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
-                  tmem_st_32x32b_x16(my + C::O_COL + c * 16, o);
-                }
-              }
-            }
-            const uint64_t k2 = pk2(sc.scale2, sc.scale2), off = pk2(-m, -m);
-            uint64_t l0 = 0, l1 = 0;
-#pragma unroll
-            for (int c = 0; c < CW / 32; ++c) {
-              if (c * 32 >= nc) continue;
-              uint32_t pk[16];
-#pragma unroll
-              for (int i = 0; i < 32; i += 4) {
-                float a, b, d, e;
-                unpk2(fma2(pk2(s[c * 32 + i], s[c * 32 + i + 1]), k2, off), a, b);
-                unpk2(fma2(pk2(s[c * 32 + i + 2], s[c * 32 + i + 3]), k2, off), d, e);
-                a = ex2(a);
-                b = ex2(b);
-                d = ex2(d);
-                e = ex2(e);
-                l0 = add2(l0, pk2(a, b));
-                l1 = add2(l1, pk2(d, e));
-                pk[i / 2] = Pair<E>::pack(a, b);
-                pk[i / 2 + 1] = Pair<E>::pack(d, e);
-              }
-              tmem_st_32x32b_x16(my + (C::SEP ? C::P_COL + c * 16 : c * 32), pk);
-            }
-            float a, b;
-            unpk2(add2(l0, l1), a, b);
-            l += a + b;
-            tmem_wait_st();
-          }
-          tc_fence_before();
-          mbar_arrive(p_full);
-        }
-        if (!ok) break;
-        ok = wwait_all(o_full, (step - 1) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 3), step);
+      for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
+      float m = -INFINITY, l = 0.f;                           // m in base-2 units
+      for (int j = 0; j < key_tiles; ++j, ++step) {
+        const int nc = min(hi - lo - j * CW, CW);
+        // S is there; without SEP with it, in order, every earlier product
+        ok = wwait_all(s_full, step & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 0), step);
+        const uint32_t vi = 2 * step + 1;
+        if (AXES && ok)
+          ok = wwait_all(kv_full + vi % C::SLOTS, (vi / C::SLOTS) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 1), step);
         if (!ok) break;
         tc_fence_after();
+        uint32_t raw[CW];
+        float* s = reinterpret_cast<float*>(raw);
         if (any) {
-          const float inv = 1.f / l;
-          E* out = static_cast<E*>(p.o) + (int64_t)r0 * p.os + qh;
+          const float* pos = spos + ((vi % C::SLOTS) >> 1) * kMaxAxes * CW;
+          auto load = [&] {
 #pragma unroll
-          for (int c = 0; c < DP / 32; ++c) {
-            if (c * 32 >= p.D) continue;
-            uint32_t o[32], pk[16];
-            tmem_ld32(my + C::O_COL + c * 32, o);
+            for (int c = 0; c < CW / 32; ++c)
+              if (c * 32 < nc) tmem_ld32(my + c * 32, raw + c * 32);
             tmem_wait_ld();
-            tie32(o);
 #pragma unroll
-            for (int i = 0; i < 32; i += 2)
-              pk[i / 2] = Pair<E>::pack(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
-            store32(stage + warp * STAGE, pk, out, p.os, hi - r0, c * 32, p.D, lane);
+            for (int c = 0; c < CW / 32; ++c) tie32(raw + c * 32);
+          };
+          // cap, bias and -inf past the document's end for one chunk of which `left` columns are inside
+          auto chunk = [&](float* v, int c, int left) {
+            if (CAP && left < 32) {                         // what lies past the end must not choose the tanh
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i >= left) v[i] = 0.f;
+            }
+            transform32<AXES, CAP, CW>(v, pos, c * 32, own, sc, CAP && all_small<32>(v, sc, live));
+            if (left < 32) {
+#pragma unroll
+              for (int i = 0; i < 32; ++i)
+                if (i >= left) v[i] = -INFINITY;
+            }
+          };
+          if constexpr (!C::SEP) {
+            load();
+#pragma unroll
+            for (int c = 0; c < CW / 32; ++c)
+              if (c * 32 < nc) chunk(s + c * 32, c, nc - c * 32);
+          } else {
+            bool fast = nc == CW;
+            if (fast) {
+              load();
+              if (CAP) fast = all_small<CW>(s, sc, live);
+            }
+            if (fast) {
+#pragma unroll
+              for (int c = 0; c < CW / 32; ++c) transform32<AXES, CAP, CW>(s + c * 32, pos, c * 32, own, sc, true);
+            } else {
+              // a document's last tile, or scores near the cap: through TMEM in a rolled loop (both forms of the
+              // tanh unrolled over 128 columns would not fit the instruction cache)
+#pragma unroll 1
+              for (int c = 0; c * 32 < nc; ++c) {
+                uint32_t r[32];
+                tmem_ld32(my + c * 32, r);
+                tmem_wait_ld();
+                tie32(r);
+                chunk(reinterpret_cast<float*>(r), c, nc - c * 32);
+                tmem_st_32x32b_x16(my + c * 32, r);
+                tmem_st_32x32b_x16(my + c * 32 + 16, r + 16);
+              }
+              tmem_wait_st();
+              load();
+            }
           }
-          if (live) p.lse[(int64_t)w.head * p.N + row] = (m + log2f(l)) * kLn2;
+        }
+        if (C::SEP) {
+          tc_fence_before();
+          mbar_arrive(s_free);
+        }
+        float top = -INFINITY;
+        if (any) {
+#pragma unroll
+          for (int c = 0; c < CW / 32; ++c) {
+            if (c * 32 >= nc) continue;
+            const float* v = s + c * 32;
+            float t0 = top, t1 = v[0];
+#pragma unroll
+            for (int i = 1; i < 31; i += 3) {               // three-way maxima, two chains
+              t0 = fmaxf(fmaxf(t0, v[i]), v[i + 1]);
+              t1 = fmaxf(t1, v[i + 2]);
+            }
+            top = fmaxf(fmaxf(t0, t1), v[31]);
+          }
+          top *= sc.scale2;                                 // scale > 0
+        }
+        if (C::SEP && j > 0) {                              // P's columns, and O, are free once the last product is done
+          ok = wwait_all(o_full, (step - 1) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 2), step);
+          if (!ok) break;
+          tc_fence_after();
+        }
+        if (any) {
+          if (j == 0) {
+            m = top;
+          } else {
+            const bool grow = top > m + kLag;
+            if (__any_sync(0xffffffffu, grow)) {
+              const float fix = grow ? ex2(m - top) : 1.f;
+              l *= fix;
+              if (grow) m = top;
+#pragma unroll 1
+              for (int c = 0; c < d16; ++c) {
+                uint32_t o[16];
+                tmem_ld_32x32b_x16(my + C::O_COL + c * 16, o);
+                tmem_wait_ld();
+                tie16(o);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * fix);
+                tmem_st_32x32b_x16(my + C::O_COL + c * 16, o);
+              }
+            }
+          }
+          const uint64_t k2 = pk2(sc.scale2, sc.scale2), off = pk2(-m, -m);
+          uint64_t l0 = 0, l1 = 0;
+#pragma unroll
+          for (int c = 0; c < CW / 32; ++c) {
+            if (c * 32 >= nc) continue;
+            uint32_t pk[16];
+#pragma unroll
+            for (int i = 0; i < 32; i += 4) {
+              float a, b, d, e;
+              unpk2(fma2(pk2(s[c * 32 + i], s[c * 32 + i + 1]), k2, off), a, b);
+              unpk2(fma2(pk2(s[c * 32 + i + 2], s[c * 32 + i + 3]), k2, off), d, e);
+              a = ex2(a);
+              b = ex2(b);
+              d = ex2(d);
+              e = ex2(e);
+              l0 = add2(l0, pk2(a, b));
+              l1 = add2(l1, pk2(d, e));
+              pk[i / 2] = Pair<E>::pack(a, b);
+              pk[i / 2 + 1] = Pair<E>::pack(d, e);
+            }
+            tmem_st_32x32b_x16(my + (C::SEP ? C::P_COL + c * 16 : c * 32), pk);
+          }
+          float a, b;
+          unpk2(add2(l0, l1), a, b);
+          l += a + b;
+          tmem_wait_st();
         }
         tc_fence_before();
+        mbar_arrive(p_full);
       }
+      if (!ok) break;
+      ok = wwait_all(o_full, (step - 1) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 3), step);
+      if (!ok) break;
+      tc_fence_after();
+      if (any) {
+        const float inv = 1.f / l;
+        E* out = static_cast<E*>(p.o) + (int64_t)r0 * p.os + qh;
+#pragma unroll
+        for (int c = 0; c < DP / 32; ++c) {
+          if (c * 32 >= p.D) continue;
+          uint32_t o[32], pk[16];
+          tmem_ld32(my + C::O_COL + c * 32, o);
+          tmem_wait_ld();
+          tie32(o);
+#pragma unroll
+          for (int i = 0; i < 32; i += 2)
+            pk[i / 2] = Pair<E>::pack(__uint_as_float(o[i]) * inv, __uint_as_float(o[i + 1]) * inv);
+          store32(stage + warp * STAGE, pk, out, p.os, hi - r0, c * 32, p.D, lane);
+        }
+        if (live) p.lse[(int64_t)w.head * p.N + row] = (m + log2f(l)) * kLn2;
+      }
+      tc_fence_before();
     }
     if (!ok && lane == 0) raise_abort(abort_flag, err);
   }

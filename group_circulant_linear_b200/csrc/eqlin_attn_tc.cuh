@@ -450,43 +450,120 @@ inline cudaError_t make_map(CUtensorMap* map, const void* base, uint32_t fmt, co
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// A work item in the kernels' 32-bit coordinates: own rows first, first + step,
-// ... below hi (`tiles` of them) of the document [lo, hi).
-struct Item {
-  int head, lo, hi, first, tiles;
+// One own tile: rows from `first` on of the document [lo, hi), first < hi.
+struct Tile {
+  int head, lo, hi, first;
 };
-template <bool UNIFORM>
-__device__ __forceinline__ Item item_of(const Params& p, uint32_t item, int heads) {
-  const Work w = work_of(p, item, heads);
-  int64_t lo, hi;
-  doc_range(p, w.doc, lo, hi);
-  Item i;
-  i.head = w.head;
-  i.lo = UNIFORM ? (int)uniform((uint32_t)lo) : (int)lo;
-  i.hi = UNIFORM ? (int)uniform((uint32_t)hi) : (int)hi;
-  const int64_t first = lo + (int64_t)w.tile * ROWS, step = (int64_t)p.hint * ROWS;
-  i.first = first < hi ? (int)first : (int)hi;
-  i.tiles = (int)((hi - i.first + step - 1) / step);
-  if (UNIFORM) {
-    i.first = (int)uniform((uint32_t)i.first);
-    i.tiles = (int)uniform((uint32_t)i.tiles);
+
+// The own tiles of a block, in the order in which every role meets them.
+//
+// Documents of one length: item = (document, head, tile), tiles fastest, so
+// that blocks which share keys run together; as many blocks as fit the SMs
+// walk all items, and one item's loads run under the previous one's products
+// and stores.
+//
+// Packed documents: item = (slot, head), a slot being 128 tokens of the packed
+// sequence, a block per item.  Its own tiles are those that start in the slot:
+// at most one of a document that began earlier, and the first one of every
+// document that begins there.  So the grid is as large as the work, whatever
+// the lengths are, and short documents share a block.  Warp 0 lists them in
+// shared memory, finding the first document by a search over the offsets, 32
+// ways at a time.  (The roles' own loops stay free of data-dependent control
+// flow: with it the compiler keeps the MMA warp's descriptors out of uniform
+// registers, a tenth of the backward's time.)  Offsets are forced into [0, N]
+// and into order, so that wrong ones cannot lead out of the tensors.
+constexpr int kListInts = 1 + 3 * (ROWS + 1);        // count; lo, hi, first of each
+__device__ __forceinline__ int offset_at(const Params& p, int64_t i) { return min(max(p.offsets[i], 0), (int)p.N); }
+
+// First of the docs + 1 offsets that is at least `from`; for a whole warp.
+__device__ __forceinline__ int64_t first_offset(const Params& p, int from) {
+  const int lane = threadIdx.x & 31;
+  int64_t l = 0, r = p.docs + 1;
+  while (l < r) {
+    const int64_t step = (r - l + 31) / 32, at = l + lane * step;
+    const bool below = at < r && p.offsets[at] < from;
+    const int c = __popc(__ballot_sync(0xffffffffu, below));
+    if (c == 0) break;
+    const int64_t next = l + c * step;               // not below, if there is one
+    l += (c - 1) * step + 1;
+    if (next < r) r = next;
   }
-  return i;
+  return l;
+}
+// Warp 0: the own tiles that start in tokens [from, to).
+__device__ __forceinline__ void list_tiles(const Params& p, int from, int to, int* list) {
+  const int lane = threadIdx.x & 31;
+  int64_t doc = first_offset(p, from);
+  int n = 0;
+  if (doc >= 1 && doc <= p.docs) {                   // the document that began before the slot
+    const int lo = offset_at(p, doc - 1), hi = max(offset_at(p, doc), lo);
+    const int first = lo + (from - lo + ROWS - 1) / ROWS * ROWS;
+    if (first >= from && first < to && first < hi) {
+      if (lane == 0) {
+        list[1] = lo;
+        list[2] = hi;
+        list[3] = first;
+      }
+      n = 1;
+    }
+  }
+  for (; doc < p.docs; doc += 32) {
+    const int64_t d = doc + lane;
+    const int lo = d < p.docs ? offset_at(p, d) : to, hi = d < p.docs ? max(offset_at(p, d + 1), lo) : to;
+    const bool inside = lo >= from && lo < to;
+    const uint32_t mask = __ballot_sync(0xffffffffu, inside && hi > lo);
+    const int at = n + __popc(mask & ((1u << lane) - 1u));
+    if (inside && hi > lo && at <= ROWS) {           // at most one tile a token, unless offsets are out of order
+      list[1 + 3 * at] = lo;
+      list[2 + 3 * at] = hi;
+      list[3 + 3 * at] = lo;
+    }
+    n = min(n + __popc(mask), ROWS + 1);
+    if (!__all_sync(0xffffffffu, inside)) break;
+  }
+  if (lane == 0) list[0] = n;
 }
 
-// Documents of one length: as many blocks as fit the SMs walk all items, so
-// that one item's loads run under the previous one's products and its stores.
-// Packed documents: a block per item, many of which may be empty.
+// Before anything else, by the whole block: the number of its own tiles.
+// Packed calls also clear the rows of the slot that no document holds.
+template <typename F>
+__device__ __forceinline__ uint32_t begin(const Params& p, int heads, int* list, F&& clear) {
+  if (!p.offsets) return (p.items - blockIdx.x + gridDim.x - 1) / gridDim.x;
+  const int slot = (int)(blockIdx.x / (uint32_t)heads), head = (int)(blockIdx.x - (uint32_t)slot * (uint32_t)heads);
+  const int from = slot * ROWS, to = min(from + ROWS, (int)p.N);
+  const int a = offset_at(p, 0), b = max(offset_at(p, p.docs), a);
+  for (int r = from; r < min(to, a); ++r) clear(head, (int64_t)r);
+  for (int r = max(from, b); r < to; ++r) clear(head, (int64_t)r);
+  if (threadIdx.x < 32) list_tiles(p, from, to, list);
+  __syncthreads();
+  return uniform((uint32_t)list[0]);
+}
+// Own tile i of the block, in warp-uniform values.
+__device__ __forceinline__ Tile tile_at(const Params& p, int heads, const int* list, uint32_t i) {
+  uint32_t head, lo, hi, first;
+  if (p.offsets) {
+    head = blockIdx.x % (uint32_t)heads;
+    lo = (uint32_t)list[1 + 3 * i];
+    hi = (uint32_t)list[2 + 3 * i];
+    first = (uint32_t)list[3 + 3 * i];
+  } else {
+    const uint32_t work = blockIdx.x + i * gridDim.x, rest = work / (uint32_t)p.hint, d = rest / (uint32_t)heads;
+    head = rest - d * (uint32_t)heads;
+    lo = d * (uint32_t)p.len;
+    hi = lo + (uint32_t)p.len;
+    first = lo + (work - rest * (uint32_t)p.hint) * ROWS;
+  }
+  return Tile{(int)uniform(head), (int)uniform(lo), (int)uniform(hi), (int)uniform(first)};
+}
+
 inline cudaError_t launch_rows(void (*k)(Params, Maps), int smem, Params p, const Maps& maps, int heads, int threads,
                                int blocks_per_sm, cudaStream_t st) {
-  int64_t tiles = (p.len + ROWS - 1) / ROWS;
-  if (tiles < 1) tiles = 1;
-  const int64_t items = (p.docs + (p.offsets ? 1 : 0)) * heads;
+  // tiles of a document, or slots of the packed sequence
+  p.hint = (int)(((p.offsets ? p.N : p.len) + ROWS - 1) / ROWS);
+  const int64_t items = (p.offsets ? 1 : p.docs) * heads * (int64_t)p.hint;
   if (items == 0) return cudaSuccess;
   if (items > 0x7fffffff) return cudaErrorInvalidValue;
-  const int64_t room = 0x7fffffff / items;
-  p.hint = (int)(tiles < room ? tiles : room);
-  p.items = (uint32_t)(items * p.hint);
+  p.items = (uint32_t)items;
   uint32_t grid = p.items;
   if (!p.offsets) {
     int dev = 0, sms = 0;

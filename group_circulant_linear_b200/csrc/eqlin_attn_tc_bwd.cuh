@@ -53,7 +53,7 @@ template <int DP, bool KEYS> struct BwdCfg {
   static constexpr int SIDE = (kMaxAxes + (KEYS ? 2 : 0)) * CW * 4;            // positions, lse, delta of a slot
   static constexpr int NBAR = 2 + 3 * SLOTS + 4;
   static constexpr int EPS = NWG == 2 ? 2 * ROWS * 4 : 0;       // eps of the two warpgroups
-  static constexpr int SMEM = 2 * OWN + SLOTS * (2 * MOV + SIDE) + EPS + NWG * 4 * STAGE + NBAR * 8 + 64 + 1024;
+  static constexpr int SMEM = 2 * OWN + SLOTS * (2 * MOV + SIDE) + EPS + NWG * 4 * STAGE + NBAR * 8 + 32 + kListInts * 4 + 1024;
   static_assert(ACC1 + DP <= TMEM, "TMEM columns");
   static_assert(BLOCKS * SMEM <= 227 * 1024, "shared memory");
 };
@@ -153,29 +153,24 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
   int* local_err = abort_word + 1;
+  int* list = local_err + 4;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   grid_dep_wait();
   const int rep = p.H / p.K, heads = KEYS ? p.K : p.H;
   const int passes = KEYS ? rep : 1;                 // query heads that pass by
-  if (p.offsets) {                                   // one item per block: it may have nothing to do
-    const Work w = work_of(p, blockIdx.x, heads);
-    if (w.doc == p.docs) {
-      const int64_t at = (int64_t)w.head * p.D;
-      outside_rows(p, w.tile, [&](int64_t r) {
+  const uint32_t count = begin(p, heads, list, [&](int head, int64_t r) {
         for (int d = threadIdx.x; d < p.D; d += C::THREADS) {
+          const int64_t at = (int64_t)head * p.D + d;
           if (KEYS) {
-            static_cast<E*>(p.dk)[r * p.dks + at + d] = Elem<E>::from_f(0.f);
-            static_cast<E*>(p.dv)[r * p.dvs + at + d] = Elem<E>::from_f(0.f);
+            static_cast<E*>(p.dk)[r * p.dks + at] = Elem<E>::from_f(0.f);
+            static_cast<E*>(p.dv)[r * p.dvs + at] = Elem<E>::from_f(0.f);
           } else {
-            static_cast<E*>(p.dq)[r * p.dqs + at + d] = Elem<E>::from_f(0.f);
+            static_cast<E*>(p.dq)[r * p.dqs + at] = Elem<E>::from_f(0.f);
           }
         }
       });
-      return;
-    }
-    if (item_of<false>(p, blockIdx.x, heads).tiles == 0) return;
-  }
+  if (count == 0) return;
 
   if (threadIdx.x == 0) {
     mbar_init(own_full, 32);
@@ -213,40 +208,37 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
     Side<AXES, KEYS, CW> sides;
     uint32_t item = 0, owns = 0;
     bool ok = true;
-    for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
-      const Item w = item_of<false>(p, work, heads);
+    for (uint32_t i = 0; ok && i < count; ++i) {
+      const Tile w = tile_at(p, heads, list, i);
       const int kv_head = KEYS ? w.head : w.head / rep, q_head = KEYS ? w.head * rep : w.head;
       const int lo = w.lo, hi = w.hi, tiles = (hi - lo - 1) / CW + 1;   // moving tiles of one head
       sides.fetch(p, q_head, lo, hi, lane);
-      for (int t = 0; ok && t < w.tiles; ++t) {
-        ok = claim<DP, CW, 2>(tails, own_empty, (owns & 1) ^ 1, ring, land, full, wait, site(KID, 2, 0), owns, lane);
-        if (!ok) break;
-        if (lane == 0) {
-          const int r0 = w.first + t * p.hint * ROWS, head = KEYS ? kv_head : q_head;
-          expect_bytes(own_full, 2 * C::OWN);
-          tma_rows<DP, ROWS>(smem, &maps.m[0], head, r0, own_full);
-          tma_rows<DP, ROWS>(smem + C::OWN, &maps.m[1], head, r0, own_full);
-        }
-        mbar_arrive(own_full);
-        ++owns;
-        for (int g = 0; ok && g < passes; ++g)
-          for (int j = 0; ok && j < tiles; ++j) {
-            const int c0 = lo + j * CW, nc = min(hi - c0, CW);
-            const uint32_t slot = item % C::SLOTS;
-            ok = claim<DP, CW, 2>(tails, empty + slot, ((item / C::SLOTS) & 1) ^ 1, ring, land, full, wait,
-                                  site(KID, 2, 1), item, lane);
-            if (!ok) break;
-            if (AXES || KEYS) {
-              sides.store(side + slot * SIDE_F, kUp, kDown, lane);
-              const bool last = j + 1 == tiles;
-              if (!last || g + 1 < passes || t + 1 < w.tiles)
-                sides.fetch(p, q_head + (last ? (g + 1 < passes ? g + 1 : 0) : g), last ? lo : c0 + CW, hi, lane);
-            }
-            ok = bring<DP, CW, 2>(tails, slot, ring, land, full, &maps.m[2], KEYS ? q_head + g : kv_head, c0, nc, wait,
-                                  site(KID, 2, 2), lane);
-            ++item;
-          }
+      ok = claim<DP, CW, 2>(tails, own_empty, (owns & 1) ^ 1, ring, land, full, wait, site(KID, 2, 0), owns, lane);
+      if (!ok) break;
+      if (lane == 0) {
+        const int head = KEYS ? kv_head : q_head;
+        expect_bytes(own_full, 2 * C::OWN);
+        tma_rows<DP, ROWS>(smem, &maps.m[0], head, w.first, own_full);
+        tma_rows<DP, ROWS>(smem + C::OWN, &maps.m[1], head, w.first, own_full);
       }
+      mbar_arrive(own_full);
+      ++owns;
+      for (int g = 0; ok && g < passes; ++g)
+        for (int j = 0; ok && j < tiles; ++j) {
+          const int c0 = lo + j * CW, nc = min(hi - c0, CW);
+          const uint32_t slot = item % C::SLOTS;
+          ok = claim<DP, CW, 2>(tails, empty + slot, ((item / C::SLOTS) & 1) ^ 1, ring, land, full, wait,
+                                site(KID, 2, 1), item, lane);
+          if (!ok) break;
+          if (AXES || KEYS) {
+            sides.store(side + slot * SIDE_F, kUp, kDown, lane);
+            const bool last = j + 1 == tiles;
+            if (!last || g + 1 < passes) sides.fetch(p, q_head + g + (last ? 1 : 0), last ? lo : c0 + CW, hi, lane);
+          }
+          ok = bring<DP, CW, 2>(tails, slot, ring, land, full, &maps.m[2], KEYS ? q_head + g : kv_head, c0, nc, wait,
+                                site(KID, 2, 2), lane);
+          ++item;
+        }
     }
     if (ok) ok = settle<DP, CW, 2>(tails, tails.count, ring, land, full, wait, site(KID, 2, 2), lane);
     if (!ok && lane == 0) raise_abort(abort_flag, err);
@@ -283,42 +275,40 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
       commit(leader, s_full);
       return true;
     };
-    for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
-      const Item w = item_of<true>(p, work, heads);
+    for (; ok && owns < count; ++owns) {
+      const Tile w = tile_at(p, heads, list, owns);
       lo = w.lo;
       hi = w.hi;
       const int tiles = (hi - lo - 1) / CW + 1;      // moving tiles of one head
-      for (int t = 0; ok && t < w.tiles; ++t, ++owns) {
-        ok = wwait_all(own_full, owns & 1, limit, abort_flag, err, site(KID, 1, 0), owns) && scores(item, 0);
-        const int all = passes * tiles;
-        if (ok && all == 1) commit(leader, own_empty);
-        int j = 0;                                     // moving tile of the present pass
-        for (int i = 0; ok && i < all; ++i, ++item) {
-          const bool more = i + 1 < all;
-          const int next = j + 1 < tiles ? j + 1 : 0;
-          ok = wwait_all(p_full, item & 1, limit, abort_flag, err, site(KID, 1, 3), item);
-          if (!ok) break;
-          tc_fence_after();
-          const int steps = (min(hi - lo - j * CW, CW) + 15) / 16, slot = item % C::SLOTS;
-          const uint32_t x = ring_mn + slot * (2 * C::MOV >> 4), y = x + (C::MOV >> 4);
-          // P and du lie over the scores' chunks
-          const uint32_t b0 = KEYS ? y : x;
+      ok = wwait_all(own_full, owns & 1, limit, abort_flag, err, site(KID, 1, 0), owns) && scores(item, 0);
+      const int all = passes * tiles;
+      if (ok && all == 1) commit(leader, own_empty);
+      int j = 0;                                     // moving tile of the present pass
+      for (int i = 0; ok && i < all; ++i, ++item) {
+        const bool more = i + 1 < all;
+        const int next = j + 1 < tiles ? j + 1 : 0;
+        ok = wwait_all(p_full, item & 1, limit, abort_flag, err, site(KID, 1, 3), item);
+        if (!ok) break;
+        tc_fence_after();
+        const int steps = (min(hi - lo - j * CW, CW) + 15) / 16, slot = item % C::SLOTS;
+        const uint32_t x = ring_mn + slot * (2 * C::MOV >> 4), y = x + (C::MOV >> 4);
+        // P and du lie over the scores' chunks
+        const uint32_t b0 = KEYS ? y : x;
 #pragma unroll
-          for (int s = 0; s < CW / 16; ++s)
-            if (s < steps)
-              mma_ts(leader, tmem + C::ACC0, tmem + C::S_COL + 32 * (s >> 1) + 8 * (s & 1),
-                     b0 + s * (2048 >> 4), mn_hi, id_acc, i > 0 || s > 0);
+        for (int s = 0; s < CW / 16; ++s)
+          if (s < steps)
+            mma_ts(leader, tmem + C::ACC0, tmem + C::S_COL + 32 * (s >> 1) + 8 * (s & 1),
+                   b0 + s * (2048 >> 4), mn_hi, id_acc, i > 0 || s > 0);
 #pragma unroll
-          for (int s = 0; s < CW / 16; ++s)
-            if (s < steps)
-              mma_ts(leader, tmem + C::ACC1, tmem + C::DP_COL + 32 * (s >> 1) + 8 * (s & 1),
-                     x + s * (2048 >> 4), mn_hi, id_acc, i > 0 || s > 0);
-          commit(leader, acc_full);
-          commit(leader, empty + slot);
-          if (more) ok = scores(item + 1, next);   // in order behind the products that read P and du
-          if (i + 2 == all) commit(leader, own_empty);   // every product with the own tiles is issued
-          j = next;
-        }
+        for (int s = 0; s < CW / 16; ++s)
+          if (s < steps)
+            mma_ts(leader, tmem + C::ACC1, tmem + C::DP_COL + 32 * (s >> 1) + 8 * (s & 1),
+                   x + s * (2048 >> 4), mn_hi, id_acc, i > 0 || s > 0);
+        commit(leader, acc_full);
+        commit(leader, empty + slot);
+        if (more) ok = scores(item + 1, next);   // in order behind the products that read P and du
+        if (i + 2 == all) commit(leader, own_empty);   // every product with the own tiles is issued
+        j = next;
       }
     }
     if (!ok && lane == 0) raise_abort(abort_flag, err);
@@ -330,118 +320,116 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
     const uint32_t my = tmem + ((uint32_t)(quarter * 32) << 16);
     uint32_t item = 0;
     bool ok = true;
-    for (uint32_t work = blockIdx.x; ok && work < p.items; work += gridDim.x) {
-      const Item w = item_of<false>(p, work, heads);
+    for (uint32_t i = 0; ok && i < count; ++i) {
+      const Tile w = tile_at(p, heads, list, i);
       const int kv_head = KEYS ? w.head : w.head / rep, q_head = KEYS ? w.head * rep : w.head;
       const int64_t kh = (int64_t)kv_head * p.D, qh0 = (int64_t)q_head * p.D;
       const int lo = w.lo, hi = w.hi, tiles = (hi - lo - 1) / CW + 1;   // moving tiles of one head
-      for (int t = 0; ok && t < w.tiles; ++t) {
-        const int r0 = w.first + t * p.hint * ROWS + quarter * 32;
-        const bool any = r0 < hi, live = lane < hi - r0;
-        const int64_t row = (int64_t)r0 + lane;
-        float own[AXES ? AXES : 1];
+      const int r0 = w.first + quarter * 32;
+      const bool any = r0 < hi, live = lane < hi - r0;
+      const int64_t row = (int64_t)r0 + lane;
+      float own[AXES ? AXES : 1];
 #pragma unroll
-        for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
-        float lse2 = 0.f, delta = 0.f;                 // of the own row (queries own)
-        if (!KEYS && any) {
-          delta = row_dots(static_cast<const E*>(p.go) + (int64_t)r0 * p.gos + qh0, p.gos,
-                           static_cast<const E*>(p.o) + (int64_t)r0 * p.os + qh0, p.os, hi - r0, p.D, lane);
-          if (live) lse2 = p.lse[(int64_t)w.head * p.N + row] * kLog2e;
-        }
-        uint64_t eps2 = 0;
-        for (int g = 0; ok && g < passes; ++g) {
-          const Score sc = score_of(p, q_head + g);
-          for (int j = 0; j < tiles; ++j, ++item) {
-            const int nc = min(hi - lo - j * CW, CW), slot = item % C::SLOTS;
-            ok = wwait_all(s_full, item & 1, limit, abort_flag, err, site(KID, 0, 0), item);
-            if ((AXES || KEYS) && ok)
-              ok = wwait_all(full + slot, (item / C::SLOTS) & 1, limit, abort_flag, err, site(KID, 0, 1), item);
-            if (!ok) break;
-            tc_fence_after();
-            if (any) {
-              const float* sd = side + slot * SIDE_F;
-              // this warpgroup's chunks: wg, wg + NWG
-#pragma unroll 1
-              for (int c = wg; c * 32 < nc; c += NWG) {
-                uint32_t rs[32], rd[32], pp[16], pd[16];
-                tmem_ld32(my + C::S_COL + c * 32, rs);
-                tmem_ld32(my + C::DP_COL + c * 32, rd);
-                tmem_wait_ld();
-                tie32(rs);
-                tie32(rd);
-                // Past the document's end: P = 0 and dP = delta, so that nothing adds to eps or du.  Under a cap
-                // P is what -cap gives, at most 1, and its product with g is 0.  KEYS: lse is +inf there, so any
-                // finite score will do.
-                if ((!KEYS || CAP) && c * 32 + 32 > nc) {
-#pragma unroll
-                  for (int k = 0; k < 32; ++k)
-                    if (c * 32 + k >= nc) {
-                      rs[k] = KEYS ? 0u : __float_as_uint(-INFINITY);
-                      if (!KEYS) rd[k] = __float_as_uint(delta);
-                    }
-                }
-                if (CAP && all_small<32>(reinterpret_cast<const float*>(rs), sc, live))
-                  grad32<AXES, CAP, KEYS, true, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);
-                else
-                  grad32<AXES, CAP, KEYS, false, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);
-                tmem_st_32x32b_x16(my + C::S_COL + c * 32, pp);
-                tmem_st_32x32b_x16(my + C::DP_COL + c * 32, pd);
-              }
-              tmem_wait_st();
-            }
-            tc_fence_before();
-            mbar_arrive(p_full);
-          }
-        }
-        if (!ok) break;
-        ok = wwait_all(acc_full, (item - 1) & 1, limit, abort_flag, err, site(KID, 0, 3), item);
-        if (!ok) break;
-        tc_fence_after();
-        float eps = 0.f;
-        if (!KEYS) {
-          float a, b;
-          unpk2(eps2, a, b);
-          eps = a + b;
-          if (NWG == 2) {                              // the two halves of the row's columns
-            eps_sum[wg * ROWS + quarter * 32 + lane] = eps;
-            named_bar_sync(1, NWG * 128);
-            eps = eps_sum[quarter * 32 + lane] + eps_sum[ROWS + quarter * 32 + lane];
-            named_bar_sync(1, NWG * 128);
-          }
-          if (live && wg == 0) p.delta[(int64_t)w.head * p.N + row] = delta + eps;
-        }
-        if (any) {
-#pragma unroll
-          for (int c = 0; c < DP / 32; ++c) {
-            if (c * 32 >= p.D || c % NWG != wg) continue;
-            uint32_t x[32], y[32], pk[16];
-            tmem_ld32(my + C::ACC0 + c * 32, x);
-            tmem_ld32(my + C::ACC1 + c * 32, y);
-            tmem_wait_ld();
-            tie32(x);
-            tie32(y);
-            uint8_t* st = stage + warp * STAGE;
-            if (KEYS) {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2)
-                pk[i / 2] = Pair<E>::pack(__uint_as_float(x[i]) * kDown, __uint_as_float(x[i + 1]) * kDown);
-              store32(st, pk, static_cast<E*>(p.dv) + (int64_t)r0 * p.dvs + kh, p.dvs, hi - r0, c * 32, p.D, lane);
-            }
-#pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              float a = __uint_as_float(y[i]), b = __uint_as_float(y[i + 1]);
-              if (!KEYS) {
-                a = fmaf(-eps, __uint_as_float(x[i]), a);
-                b = fmaf(-eps, __uint_as_float(x[i + 1]), b);
-              }
-              pk[i / 2] = Pair<E>::pack(a * p.scale, b * p.scale);
-            }
-            if (KEYS) store32(st, pk, static_cast<E*>(p.dk) + (int64_t)r0 * p.dks + kh, p.dks, hi - r0, c * 32, p.D, lane);
-            else store32(st, pk, static_cast<E*>(p.dq) + (int64_t)r0 * p.dqs + qh0, p.dqs, hi - r0, c * 32, p.D, lane);
-          }
-        }
-        tc_fence_before();
+      for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
+      float lse2 = 0.f, delta = 0.f;                 // of the own row (queries own)
+      if (!KEYS && any) {
+        delta = row_dots(static_cast<const E*>(p.go) + (int64_t)r0 * p.gos + qh0, p.gos,
+                         static_cast<const E*>(p.o) + (int64_t)r0 * p.os + qh0, p.os, hi - r0, p.D, lane);
+        if (live) lse2 = p.lse[(int64_t)w.head * p.N + row] * kLog2e;
       }
+      uint64_t eps2 = 0;
+      for (int g = 0; ok && g < passes; ++g) {
+        const Score sc = score_of(p, q_head + g);
+        for (int j = 0; j < tiles; ++j, ++item) {
+          const int nc = min(hi - lo - j * CW, CW), slot = item % C::SLOTS;
+          ok = wwait_all(s_full, item & 1, limit, abort_flag, err, site(KID, 0, 0), item);
+          if ((AXES || KEYS) && ok)
+            ok = wwait_all(full + slot, (item / C::SLOTS) & 1, limit, abort_flag, err, site(KID, 0, 1), item);
+          if (!ok) break;
+          tc_fence_after();
+          if (any) {
+            const float* sd = side + slot * SIDE_F;
+            // this warpgroup's chunks: wg, wg + NWG
+#pragma unroll 1
+            for (int c = wg; c * 32 < nc; c += NWG) {
+              uint32_t rs[32], rd[32], pp[16], pd[16];
+              tmem_ld32(my + C::S_COL + c * 32, rs);
+              tmem_ld32(my + C::DP_COL + c * 32, rd);
+              tmem_wait_ld();
+              tie32(rs);
+              tie32(rd);
+              // Past the document's end: P = 0 and dP = delta, so that nothing adds to eps or du.  Under a cap
+              // P is what -cap gives, at most 1, and its product with g is 0.  KEYS: lse is +inf there, so any
+              // finite score will do.
+              if ((!KEYS || CAP) && c * 32 + 32 > nc) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k)
+                  if (c * 32 + k >= nc) {
+                    rs[k] = KEYS ? 0u : __float_as_uint(-INFINITY);
+                    if (!KEYS) rd[k] = __float_as_uint(delta);
+                  }
+              }
+              if (CAP && all_small<32>(reinterpret_cast<const float*>(rs), sc, live))
+                grad32<AXES, CAP, KEYS, true, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);
+              else
+                grad32<AXES, CAP, KEYS, false, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);
+              tmem_st_32x32b_x16(my + C::S_COL + c * 32, pp);
+              tmem_st_32x32b_x16(my + C::DP_COL + c * 32, pd);
+            }
+            tmem_wait_st();
+          }
+          tc_fence_before();
+          mbar_arrive(p_full);
+        }
+      }
+      if (!ok) break;
+      ok = wwait_all(acc_full, (item - 1) & 1, limit, abort_flag, err, site(KID, 0, 3), item);
+      if (!ok) break;
+      tc_fence_after();
+      float eps = 0.f;
+      if (!KEYS) {
+        float a, b;
+        unpk2(eps2, a, b);
+        eps = a + b;
+        if (NWG == 2) {                              // the two halves of the row's columns
+          eps_sum[wg * ROWS + quarter * 32 + lane] = eps;
+          named_bar_sync(1, NWG * 128);
+          eps = eps_sum[quarter * 32 + lane] + eps_sum[ROWS + quarter * 32 + lane];
+          named_bar_sync(1, NWG * 128);
+        }
+        if (live && wg == 0) p.delta[(int64_t)w.head * p.N + row] = delta + eps;
+      }
+      if (any) {
+#pragma unroll
+        for (int c = 0; c < DP / 32; ++c) {
+          if (c * 32 >= p.D || c % NWG != wg) continue;
+          uint32_t x[32], y[32], pk[16];
+          tmem_ld32(my + C::ACC0 + c * 32, x);
+          tmem_ld32(my + C::ACC1 + c * 32, y);
+          tmem_wait_ld();
+          tie32(x);
+          tie32(y);
+          uint8_t* st = stage + warp * STAGE;
+          if (KEYS) {
+#pragma unroll
+            for (int i = 0; i < 32; i += 2)
+              pk[i / 2] = Pair<E>::pack(__uint_as_float(x[i]) * kDown, __uint_as_float(x[i + 1]) * kDown);
+            store32(st, pk, static_cast<E*>(p.dv) + (int64_t)r0 * p.dvs + kh, p.dvs, hi - r0, c * 32, p.D, lane);
+          }
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            float a = __uint_as_float(y[i]), b = __uint_as_float(y[i + 1]);
+            if (!KEYS) {
+              a = fmaf(-eps, __uint_as_float(x[i]), a);
+              b = fmaf(-eps, __uint_as_float(x[i + 1]), b);
+            }
+            pk[i / 2] = Pair<E>::pack(a * p.scale, b * p.scale);
+          }
+          if (KEYS) store32(st, pk, static_cast<E*>(p.dk) + (int64_t)r0 * p.dks + kh, p.dks, hi - r0, c * 32, p.D, lane);
+          else store32(st, pk, static_cast<E*>(p.dq) + (int64_t)r0 * p.dqs + qh0, p.dqs, hi - r0, c * 32, p.D, lane);
+        }
+      }
+      tc_fence_before();
     }
     if (!ok && lane == 0) raise_abort(abort_flag, err);
   }

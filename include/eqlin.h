@@ -364,7 +364,7 @@ typedef struct {
     int64_t docs;             /* documents; without offsets they have tokens / docs tokens each */
     const int32_t *offsets;   /* device, [docs + 1], ascending, 0 <= offsets <= tokens; or NULL */
     int64_t max_len;          /* length of the longest document if known, else 0: it spreads the
-                                 work, and every value gives the same results */
+                                 work of f32 calls, and every value gives the same results */
     const float *pos;         /* device, [tokens, axes], or NULL with axes = 0 */
     const float *slopes;      /* device, [heads] */
     int axes;                 /* 0 (no bias) to 3 */

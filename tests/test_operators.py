@@ -372,6 +372,9 @@ ATTN_CASES = [  # lens, lead, tail, H, K, D, cap, axes
     ([513, 2, 640], 0, 70, 1, 1, 64, 0.0, 0),
     ([2, 3, 4] * 8, 0, 0, 1, 1, 24, 0.0, 0),
     ([385], 0, 0, 1, 1, 128, 0.0, 3),
+    # many documents in a block's 128 tokens, runs of empty ones, whole blocks outside
+    ([1] * 150 + [0] * 70 + [3] * 20 + [0] * 3 + [130, 0, 1], 140, 150, 2, 1, 64, 0.0, 1),
+    ([0] * 40 + [127, 1, 128, 129], 128, 1, 1, 1, 32, 9.0, 0),
     # documents of 1024 tokens and more on average: the forward's wide form
     ([1100], 0, 0, 1, 1, 64, 20.0, 2),
     ([2177, 150], 3, 5, 1, 1, 32, 0.0, 3),
@@ -405,6 +408,41 @@ def test_attention_results_do_not_depend_on_max_len(max_len, dtype):
     a, b = run_attention(*args), run_attention(*args, max_len=max_len)
     for n in a:
         assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("lens,tail", [([], 9), ([], 200), ([0, 0, 0], 5)])
+def test_attention_without_documents(lens, tail, dtype):
+    run_attention(lens, 3, tail, 2, 2, 64, 0.0, 0, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("cap", [0.0, 6.0])
+def test_attention_documents_do_not_see_each_other(dtype, cap):
+    # a document's results, bit for bit, whatever its neighbours in the same tiles hold
+    dt = DT[dtype]
+    lens, H, D = [37, 100, 70, 5], 2, 64
+    N = sum(lens)
+    off = torch.tensor([0, 37, 137, 207, 212], dtype=torch.int32, device="cuda")
+    g = torch.Generator().manual_seed(12)
+    base = torch.randn((4, N, H, D), generator=g).to(dt).cuda()
+    outs = []
+    for fill in (None, float("nan"), float("inf"), 3.0e4):
+        t = base.clone()
+        if fill is not None:
+            t[:, :37] = fill
+            t[:, 137:] = fill
+        q, k, v, go = t
+        o, dq, dk, dv = (torch.empty_like(q) for _ in range(4))
+        lse, delta = torch.empty((H, N), device="cuda"), torch.empty((H, N), device="cuda")
+        eqlin.attention_forward(q, k, v, o, lse, offsets=off, cap=cap)
+        eqlin.attention_backward(go, q, k, v, o, lse, dq, dk, dv, delta, offsets=off, cap=cap)
+        outs.append([x[37:137].clone() for x in (o, dq, dk, dv)] + [lse[:, 37:137].clone()])
+    for other in outs[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(outs[0], other))
+    assert all(torch.isfinite(x).all() for x in outs[0])
 
 
 @pytest.mark.gpu

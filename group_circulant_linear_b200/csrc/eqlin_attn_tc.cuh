@@ -143,7 +143,7 @@ __device__ __forceinline__ void expect_bytes(uint64_t* bar, uint32_t bytes) {
 }
 
 // What a tile needs beside its operands, one row per lane and round: negated
-// positions [axes][rows] and, for moving queries, lse (base 2) and delta.  The
+// positions [axes][rows] and, for moving queries, -lse (base 2) and delta.  The
 // loads are issued a tile ahead and stored when the slot is free.
 template <int AXES, bool STAT, int TILE_ROWS> struct Side {
   static constexpr int R = TILE_ROWS / 32;
@@ -167,8 +167,8 @@ template <int AXES, bool STAT, int TILE_ROWS> struct Side {
 #pragma unroll
       for (int a = 0; a < AXES; ++a) dst[a * TILE_ROWS + lane + 32 * i] = -pos[a * R + i];
       if (STAT) {
-        // past the document's end +inf: P = 0 there
-        dst[kMaxAxes * TILE_ROWS + lane + 32 * i] = fmaf(lse[i], kLog2e, -up);
+        // past the document's end lse is +inf: P = 0 there
+        dst[kMaxAxes * TILE_ROWS + lane + 32 * i] = fmaf(lse[i], -kLog2e, up);
         dst[(kMaxAxes + 1) * TILE_ROWS + lane + 32 * i] = delta[i] * down;
       }
     }
@@ -336,6 +336,7 @@ __device__ __forceinline__ float row_dots(const E* a, int64_t as, const E* b, in
 struct Score {
   float scale2;
   float in, out;          // scale / cap, cap / scale
+  float cap2, slope2;     // cap log2 e, slope log2 e
   float twoin;            // 2 log2 e scale / cap: e^{2u/cap} = 2^(raw twoin)
   float slope;            // slope / scale
 };
@@ -345,27 +346,29 @@ __device__ __forceinline__ Score score_of(const Params& p, int head) {
   s.in = p.cap > 0.f ? p.scale / p.cap : 0.f;
   s.out = p.cap > 0.f ? p.cap / p.scale : 0.f;
   s.twoin = 2.f * kLog2e * s.in;
+  s.cap2 = p.cap * kLog2e;
   s.slope = p.axes ? p.slopes[head] / p.scale : 0.f;
+  s.slope2 = p.axes ? p.slopes[head] * kLog2e : 0.f;
   return s;
 }
 
 // tanh, for two arguments.  Where all of a warp's arguments are small (|x| <=
-// kSmall, the usual case below a cap) an odd polynomial, x q(x^2): 4e-9 off at
-// most (coefficients: a weighted least-squares fit of tanh(x)/x refined to
-// equal ripple), 3.5 instructions per score on the FMA pipes.  Otherwise
-// 1 - 2 / (1 + e^{2x}), a few 2^-24 off in absolute terms everywhere, which is
-// what a score needs; its two MUFU operations (8 cycles of a scheduler each)
-// would otherwise be two thirds of the softmax's time.  tanh.approx would be
-// one, but is only good to 2^-11.
-constexpr float kSmall = 0.7f;
+// kSmall, the usual case below a cap) an odd polynomial, x q(x^2): 2e-8 off at
+// most, a third of a score's own rounding under a cap of 30 (coefficients: a
+// weighted least-squares fit of tanh(x)/x refined to equal ripple), 3
+// instructions per score on the FMA pipes.  Otherwise 1 - 2 / (1 + e^{2x}), a
+// few 2^-24 off in absolute terms everywhere, which is what a score needs; its
+// two MUFU operations (8 cycles of a scheduler each) would otherwise be two
+// thirds of the softmax's time.  tanh.approx would be one, but is only good to
+// 2^-11.
+constexpr float kSmall = 0.6f;
 __device__ __forceinline__ uint64_t q_small2(uint64_t x) {      // tanh(x) / x
   const uint64_t z = mul2(x, x);
-  uint64_t q = pk2(-0.004874242004007101f, -0.004874242004007101f);
-  q = fma2(q, z, pk2(0.01973520778119564f, 0.01973520778119564f));
-  q = fma2(q, z, pk2(-0.053383808583021164f, -0.053383808583021164f));
-  q = fma2(q, z, pk2(0.1332535296678543f, 0.1332535296678543f));
-  q = fma2(q, z, pk2(-0.33332860469818115f, -0.33332860469818115f));
-  return fma2(q, z, pk2(0.9999999403953552f, 0.9999999403953552f));
+  uint64_t q = pk2(0.01497695967555046f, 0.01497695967555046f);
+  q = fma2(q, z, pk2(-0.051696743816137314f, -0.051696743816137314f));
+  q = fma2(q, z, pk2(0.13299210369586945f, 0.13299210369586945f));
+  q = fma2(q, z, pk2(-0.33331209421157837f, -0.33331209421157837f));
+  return fma2(q, z, pk2(0.9999996423721313f, 0.9999996423721313f));
 }
 __device__ __forceinline__ float tanh_any(float raw, const Score& s) {
   return fmaf(-2.f, rcp(1.f + ex2(raw * s.twoin)), 1.f);

@@ -59,17 +59,22 @@ template <int DP, bool KEYS> struct BwdCfg {
 };
 
 // One 32-column chunk of a row: raw scores rs and dP rd in, packed P and du out.
-//   KEYS: lse and delta belong to the columns (ls, dl in shared memory, already
-//   in base 2 and scaled), else to the row.
+//   KEYS: -lse and delta belong to the columns (in shared memory, in base 2 and
+//   scaled), else to the row.
+// In FMA-pipe operations per element, which bound this under a cap: tanh 8 (16
+// halves), bias 2 + axes, the rest 5.  Two signs cancel to save two more: diff
+// is delta - dP and gain tanh^2 - 1, so that du is right, while eps and P g
+// (KEYS = false) come out negated, and so does not their product.
 template <int AXES, bool CAP, bool KEYS, bool SMALL, int CW, typename E>
 __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, const float* side, int c0, const float* own,
                                        float lse2, float delta, const Score& sc, uint64_t& eps, uint32_t* pp,
                                        uint32_t* pd) {
   constexpr bool F16 = Pair<E>::fmt == 0;
   constexpr float kDown = F16 ? 1.f / 256.f : 1.f;
-  const uint64_t k2 = pk2(sc.scale2, sc.scale2), in = pk2(sc.in, sc.in), slope = pk2(-sc.slope, -sc.slope);
-  const uint64_t one = pk2(1.f, 1.f), neg = pk2(-1.f, -1.f), down = pk2(kDown, kDown);
-  const uint64_t row_off = pk2(-lse2, -lse2), row_delta = pk2(-delta, -delta);
+  const uint64_t k2 = CAP ? pk2(sc.cap2, sc.cap2) : pk2(sc.scale2, sc.scale2);
+  const uint64_t in = pk2(sc.in, sc.in), slope = pk2(-sc.slope2, -sc.slope2);
+  const uint64_t minus = pk2(-1.f, -1.f), down = pk2(-kDown, -kDown);
+  const uint64_t row_off = pk2(-lse2, -lse2), row_delta = pk2(CAP ? delta : -delta, CAP ? delta : -delta);
 #pragma unroll
   for (int j = 0; j < 32; j += 4) {
     float d[4];
@@ -84,31 +89,32 @@ __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, c
       const int i = j + 2 * h;
       uint64_t x = pk2(__uint_as_float(rs[i]), __uint_as_float(rs[i + 1]));
       const uint64_t dp = pk2(__uint_as_float(rd[i]), __uint_as_float(rd[i + 1]));
-      uint64_t gain = one;                           // 1 - tanh^2
+      uint64_t gain = minus;                         // tanh^2 - 1
       if (CAP) {
         if (SMALL) {
-          const uint64_t u = mul2(x, in), q = q_small2(u), t = mul2(u, q);
-          x = mul2(x, q);
-          gain = fma2(mul2(t, neg), t, one);
+          x = mul2(x, in);
+          x = mul2(x, q_small2(x));
         } else {
           float a, b;
           unpk2(x, a, b);
-          a = tanh_any(a, sc);
-          b = tanh_any(b, sc);
-          const uint64_t t = pk2(a, b);
-          x = pk2(sc.out * a, sc.out * b);
-          gain = fma2(mul2(t, neg), t, one);
+          x = pk2(tanh_any(a, sc), tanh_any(b, sc));
         }
+        gain = fma2(x, x, minus);
       }
-      if (AXES) x = fma2(slope, pk2(d[2 * h], d[2 * h + 1]), x);
-      const uint64_t lse_h = KEYS ? mul2(h ? ls.y : ls.x, neg) : row_off;
+      uint64_t off = KEYS ? (h ? ls.y : ls.x) : row_off;
+      if (AXES) off = fma2(slope, pk2(d[2 * h], d[2 * h + 1]), off);
       float a, b;
-      unpk2(fma2(x, k2, lse_h), a, b);
+      unpk2(fma2(x, k2, off), a, b);
       a = ex2(a);
       b = ex2(b);
+      // delta - dP under a cap, else dP - delta
       uint64_t diff;
-      if (KEYS) diff = fma2(h ? dl.y : dl.x, neg, F16 ? mul2(dp, down) : dp);
-      else diff = add2(dp, row_delta);
+      if (KEYS) {
+        if (CAP) diff = F16 ? fma2(dp, down, h ? dl.y : dl.x) : fma2(dp, minus, h ? dl.y : dl.x);
+        else diff = fma2(h ? dl.y : dl.x, minus, F16 ? mul2(dp, mul2(down, minus)) : dp);
+      } else {
+        diff = CAP ? fma2(dp, minus, row_delta) : add2(dp, row_delta);
+      }
       uint64_t prob = pk2(a, b);
       if (!KEYS) eps = fma2(prob, diff, eps);
       if (!KEYS && CAP) prob = mul2(prob, gain);     // KEYS: dv takes P itself
@@ -397,7 +403,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
           eps = eps_sum[quarter * 32 + lane] + eps_sum[ROWS + quarter * 32 + lane];
           named_bar_sync(1, NWG * 128);
         }
-        if (live && wg == 0) p.delta[(int64_t)w.head * p.N + row] = delta + eps;
+        if (live && wg == 0) p.delta[(int64_t)w.head * p.N + row] = CAP ? delta - eps : delta + eps;
       }
       if (any) {
 #pragma unroll

@@ -19,9 +19,10 @@
 //              formed; half the hand-overs, but its 128 scores per thread only
 //              stay in registers for whole tiles away from the cap.
 // CW = 128 is taken for heads of up to 64 features (its columns need them) in
-// documents of 1024 tokens and more on average: 12544 tokens, 6 heads of 64
-// take 400 us against 534 (616 against 786 capped), 64 x 197 tokens, 12 heads
-// 103 us against 66, windows of 49 127 against 67.
+// documents of 512 tokens and more on average.  CW 128 against 64, heads of 64:
+// 12544 tokens, 6 heads 379 us against 534 (595 against 786 capped); 30 x 600
+// tokens, 6 heads 47 against 57 (96 against 93 capped and biased); 64 x 197
+// tokens, 12 heads 48 against 40 (103 against 65); windows of 49 127 against 64.
 #include "eqlin_attn_tc.cuh"
 
 namespace eqlin {
@@ -44,7 +45,7 @@ template <int DP, int CW_> struct FwdCfg {
   static_assert(O_COL + DP <= TMEM, "TMEM columns");
   static_assert(2 * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
-constexpr int kWideFrom = 1024;                               // average tokens of a document
+constexpr int kWideFrom = 512;                                // average tokens of a document
 
 template <int DP, int CW, typename E, int AXES, bool CAP>
 __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_constant__ Params p,

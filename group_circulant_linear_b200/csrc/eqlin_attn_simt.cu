@@ -8,14 +8,12 @@
 // (dq, and delta on the way), the other key rows (dk, dv, over all query
 // heads that share them).
 //
-// 256 threads form a 16 x 16 grid; thread (ty, tx) owns rows 4ty .. 4ty+3
-// and, of a 64 x 64 product, columns tx + 16j: reads of the moving operand are
-// then 16 rows apart by D + 4 floats, free of bank conflicts, and those of the
-// rows broadcast.  Per four feature steps a warp's 8 16-byte reads take 12
-// shared-memory cycles and its 64 FMAs 64 scheduler cycles, of which an SM has
-// four: FFMA-bound, when loads and exponentials are out of the way.  Products
-// stop at a document's last column (in steps of 16, or 4) and warps without
-// rows skip them: the last tile of 197 tokens costs 5 columns, not 64.
+// Threads form a grid 16 wide; thread (ty, tx) owns R rows from R ty on and,
+// of a 64 x 64 product, columns tx + 16j: reads of the moving operand are then
+// 16 rows apart by D + 4 floats, free of bank conflicts, and those of the rows
+// broadcast.  Products take two FMAs an instruction, stop at a document's last
+// column (in steps of 16, or 4), and warps without rows skip them: the last
+// tile of 197 tokens costs 5 columns, not 64.
 // A warp alone reads and writes its rows of P, so only tiles need block
 // barriers.  tanhf and expf, at some 60 instructions a score together, would
 // cost as much as one product each; tanh_fast and exp_fast take a third.
@@ -31,10 +29,16 @@ using ptx::pk2;
 using ptx::unpk2;
 
 constexpr int B = 64;                     // rows and columns of a tile
-constexpr int kThreads = 256;
 constexpr int LDP = B + 4;
 
+// AHEAD: the next moving tile is read into registers while this one is worked
+// on.  Not at 64 features: two blocks of 128 registers hide the reads better
+// than the spills cost (16 x 197 tokens, 6 heads of 64: backward 165 us against
+// 188; 512 windows of 49, 3 heads of 32: 135 with, 156 without).
 template <int DP> struct Cfg {
+  static constexpr int R = 4;              // rows per thread
+  static constexpr int THREADS = 16 * (B / R);
+  static constexpr bool AHEAD = DP != 64;
   static constexpr int LD = DP + 4;
   static constexpr int TILE = B * LD;     // floats
   static constexpr int DC = (DP + 63) / 64;   // float4 groups of a thread's output columns
@@ -67,49 +71,62 @@ __device__ __forceinline__ Work work_of_row(const Params& p, int heads) {
   return w;
 }
 
-// Rows [r0, r0 + 64) of a head, zero past `hi` and past D.
+// Rows [r0, r0 + 64) of a head, zero past `hi` and past D: global to registers
+// and registers to shared memory.
+template <int DP> struct Rows {
+  static constexpr int N = B * (DP / 4) / Cfg<DP>::THREADS;
+  float4 v[N];
+  __device__ __forceinline__ void read(const void* src, int64_t stride, int64_t head_off, int64_t r0, int64_t hi, int D) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + k * Cfg<DP>::THREADS, r = i / (DP / 4), c = (i - r * (DP / 4)) * 4;
+      v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r0 + r < hi && c < D)
+        v[k] = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + (r0 + r) * stride + head_off + c);
+    }
+  }
+  __device__ __forceinline__ void write(float* dst, float mul) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + k * Cfg<DP>::THREADS, r = i / (DP / 4), c = (i - r * (DP / 4)) * 4;
+      *reinterpret_cast<float4*>(dst + r * Cfg<DP>::LD + c) =
+          make_float4(v[k].x * mul, v[k].y * mul, v[k].z * mul, v[k].w * mul);
+    }
+  }
+};
 template <int DP>
 __device__ __forceinline__ void load_tile(float* dst, const void* src, int64_t stride, int64_t head_off, int64_t r0,
                                           int64_t hi, int D, float mul) {
-#pragma unroll 4
-  for (int i = threadIdx.x; i < B * (DP / 4); i += kThreads) {
-    const int r = i / (DP / 4), c = (i - r * (DP / 4)) * 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (r0 + r < hi && c < D) {
-      v = *reinterpret_cast<const float4*>(static_cast<const float*>(src) + (r0 + r) * stride + head_off + c);
-      v.x *= mul;
-      v.y *= mul;
-      v.z *= mul;
-      v.w *= mul;
-    }
-    *reinterpret_cast<float4*>(dst + r * Cfg<DP>::LD + c) = v;
-  }
+  Rows<DP> rows;
+  rows.read(src, stride, head_off, r0, hi, D);
+  rows.write(dst, mul);
 }
 
-// acc[i][j] = A[row 4ty+i] . Bm[row tx+16j] over DP features; columns from
+// acc[i][j] = A[row R ty + i] . Bm[row tx + 16j] over DP features; columns from
 // nc on are left at 0.
 template <int DP, int J>
-__device__ __forceinline__ void mm_nt_cols(const float* A, const float* Bm, float (&acc)[4][4]) {
+__device__ __forceinline__ void mm_nt_cols(const float* A, const float* Bm, float (&acc)[Cfg<DP>::R][4]) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  uint64_t sum[4][J];                      // even and odd features apart: one instruction for two products
+  constexpr int R = Cfg<DP>::R;
+  uint64_t sum[R][J];                      // even and odd features apart: one instruction for two products
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int j = 0; j < J; ++j) sum[i][j] = 0;
 #pragma unroll 4
   for (int d = 0; d < DP; d += 4) {
-    ulonglong2 a[4], b[J];
+    ulonglong2 a[R], b[J];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(A + (4 * ty + i) * Cfg<DP>::LD + d);
+    for (int i = 0; i < R; ++i) a[i] = *reinterpret_cast<const ulonglong2*>(A + (R * ty + i) * Cfg<DP>::LD + d);
 #pragma unroll
     for (int j = 0; j < J; ++j) b[j] = *reinterpret_cast<const ulonglong2*>(Bm + (tx + 16 * j) * Cfg<DP>::LD + d);
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < J; ++j) sum[i][j] = fma2(a[i].y, b[j].y, fma2(a[i].x, b[j].x, sum[i][j]));
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float x = 0.f, y = 0.f;
@@ -119,30 +136,31 @@ __device__ __forceinline__ void mm_nt_cols(const float* A, const float* Bm, floa
 }
 
 template <int DP>
-__device__ __forceinline__ void mm_nt(const float* A, const float* Bm, int nc, float (&acc)[4][4]) {
+__device__ __forceinline__ void mm_nt(const float* A, const float* Bm, int nc, float (&acc)[Cfg<DP>::R][4]) {
   if (nc > 48) mm_nt_cols<DP, 4>(A, Bm, acc);
   else if (nc > 32) mm_nt_cols<DP, 3>(A, Bm, acc);
   else if (nc > 16) mm_nt_cols<DP, 2>(A, Bm, acc);
   else mm_nt_cols<DP, 1>(A, Bm, acc);
 }
 
-// out[i][c] += sum_j P[4ty+i][j] M[j][4tx + 64c ..] over the first nc rows of M
+// out[i][c] += sum_j P[R ty + i][j] M[j][4tx + 64c ..] over the first nc rows of M
 template <int DP>
-__device__ __forceinline__ void mm_nn(const float* P, const float* M, int nc, uint64_t (&out)[4][Cfg<DP>::DC][2]) {
+__device__ __forceinline__ void mm_nn(const float* P, const float* M, int nc, uint64_t (&out)[Cfg<DP>::R][Cfg<DP>::DC][2]) {
+  constexpr int R = Cfg<DP>::R;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   if (4 * tx >= DP) return;
 #pragma unroll 2
   for (int j = 0; j < nc; j += 4) {
-    float4 a[4];
+    float4 a[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) a[i] = *reinterpret_cast<const float4*>(P + (4 * ty + i) * LDP + j);
+    for (int i = 0; i < R; ++i) a[i] = *reinterpret_cast<const float4*>(P + (R * ty + i) * LDP + j);
 #pragma unroll
     for (int jj = 0; jj < 4; ++jj)
 #pragma unroll
       for (int c = 0; c < Cfg<DP>::DC; ++c) {
         const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(M + (j + jj) * Cfg<DP>::LD + 4 * tx + 64 * c);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < R; ++i) {
           const float w = jj == 0 ? a[i].x : jj == 1 ? a[i].y : jj == 2 ? a[i].z : a[i].w;
           const uint64_t w2 = pk2(w, w);
           out[i][c][0] = fma2(w2, m.x, out[i][c][0]);
@@ -155,11 +173,12 @@ __device__ __forceinline__ void mm_nn(const float* P, const float* M, int nc, ui
 // Row i times mul[i].
 template <int DP>
 __device__ __forceinline__ void store_rows(void* dst, int64_t stride, int64_t head_off, int64_t r0, int64_t hi, int D,
-                                           const uint64_t (&v)[4][Cfg<DP>::DC][2], const float (&mul)[4]) {
+                                           const uint64_t (&v)[Cfg<DP>::R][Cfg<DP>::DC][2], const float (&mul)[Cfg<DP>::R]) {
+  constexpr int R = Cfg<DP>::R;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int64_t r = r0 + 4 * ty + i;
+  for (int i = 0; i < R; ++i) {
+    const int64_t r = r0 + R * ty + i;
     if (r >= hi) continue;
 #pragma unroll
     for (int c = 0; c < Cfg<DP>::DC; ++c) {
@@ -178,41 +197,59 @@ __device__ __forceinline__ void store_rows(void* dst, int64_t stride, int64_t he
 }
 
 __device__ __forceinline__ void clear_row(void* dst, int64_t stride, int64_t head_off, int64_t r, int D) {
-  for (int d = threadIdx.x; d < D; d += kThreads)
-    static_cast<float*>(dst)[r * stride + head_off + d] = 0.f;
+  for (int d = threadIdx.x; d < D; d += blockDim.x) static_cast<float*>(dst)[r * stride + head_off + d] = 0.f;
 }
 
-// Positions of tile rows: [axes][64].
-__device__ __forceinline__ void load_pos(float* dst, const Params& p, int64_t r0, int64_t hi) {
-  for (int i = threadIdx.x; i < B * p.axes; i += kThreads) {
-    const int a = i / B, r = i - a * B;
-    dst[i] = r0 + r < hi ? p.pos[(r0 + r) * p.axes + a] : 0.f;
+// What goes with a tile's rows: positions [axes][64] and, for moving queries,
+// lse [64] and delta [64].
+template <int DP, bool STAT> struct Side {
+  static constexpr int T = Cfg<DP>::THREADS, N = (kMaxAxes * B + T - 1) / T;
+  float pos[N], lse, delta;
+  __device__ __forceinline__ void read(const Params& p, int head, int64_t r0, int64_t hi) {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int i = threadIdx.x + k * T, a = i / B, r = i - a * B;
+      pos[k] = a < p.axes && r0 + r < hi ? p.pos[(r0 + r) * p.axes + a] : 0.f;
+    }
+    if (STAT) {
+      const bool on = threadIdx.x < B && r0 + threadIdx.x < hi;
+      lse = on ? p.lse[(int64_t)head * p.N + r0 + threadIdx.x] : 0.f;
+      delta = on ? p.delta[(int64_t)head * p.N + r0 + threadIdx.x] : 0.f;
+    }
   }
-}
-// City-block distances of the thread's 4 x 4 scores, times mul.
-__device__ __forceinline__ void distances(const Params& p, const float* pr, const float* pc, float mul, float (&d)[4][4]) {
+  __device__ __forceinline__ void write(float* dst, float* stat) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (threadIdx.x + k * T < kMaxAxes * B) dst[threadIdx.x + k * T] = pos[k];
+    if (STAT && threadIdx.x < B) {
+      stat[threadIdx.x] = lse;
+      stat[B + threadIdx.x] = delta;
+    }
+  }
+};
+// City-block distances of the thread's R x 4 scores, times mul.
+template <int R>
+__device__ __forceinline__ void distances(const Params& p, const float* pr, const float* pc, float mul, float (&d)[R][4]) {
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
 #pragma unroll
   for (int a = 0; a < kMaxAxes; ++a) {
     if (a >= p.axes) break;
-    const float4 r = *reinterpret_cast<const float4*>(pr + a * B + 4 * ty);
     float c[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[j] = pc[a * B + tx + 16 * j];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      d[0][j] += fabsf(r.x - c[j]);
-      d[1][j] += fabsf(r.y - c[j]);
-      d[2][j] += fabsf(r.z - c[j]);
-      d[3][j] += fabsf(r.w - c[j]);
+    for (int i = 0; i < R; ++i) {
+      const float r = pr[a * B + R * ty + i];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) d[i][j] += fabsf(r - c[j]);
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < R; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) d[i][j] *= mul;
 }
@@ -245,7 +282,7 @@ __device__ __forceinline__ float tanh_fast(float x) {
 // ------------------------------------------------------------------ forward
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_fwd_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Cfg<DP>::THREADS, DP > 64 ? 1 : 2) attn_simt_fwd_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) float sm[];
   float* Q = sm;
   float* K = Q + Cfg<DP>::TILE;
@@ -253,6 +290,7 @@ __global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_fwd_kerne
   float* P = V + Cfg<DP>::TILE;
   float* pq = P + B * LDP;
   float* pk = pq + kMaxAxes * B;
+  constexpr int R = Cfg<DP>::R;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   grid_dep_launch();
   grid_dep_wait();
@@ -272,31 +310,42 @@ __global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_fwd_kerne
   for (int64_t r0 = lo + (int64_t)w.tile * B; r0 < hi; r0 += (int64_t)p.hint * B) {
     __syncthreads();
     load_tile<DP>(Q, p.q, p.qs, qh, r0, hi, p.D, p.scale);
-    load_pos(pq, p, r0, hi);
-    const bool busy = r0 + 8 * (threadIdx.x >> 5) < hi;       // does the warp have a row
-    float m[4], l[4];
-    uint64_t o[4][Cfg<DP>::DC][2];
+    Side<DP, false> side;
+    side.read(p, w.head, r0, hi);
+    side.write(pq, nullptr);
+    const bool busy = r0 + 2 * R * (threadIdx.x >> 5) < hi;       // does the warp have a row
+    float m[R], l[R];
+    uint64_t o[R][Cfg<DP>::DC][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
       m[i] = -INFINITY;
       l[i] = 0.f;
 #pragma unroll
       for (int c = 0; c < Cfg<DP>::DC; ++c) o[i][c][0] = o[i][c][1] = 0;
     }
+    Rows<DP> kr, vr;                       // the next moving tile
+    auto read = [&](int64_t c0) {
+      kr.read(p.k, p.ks, kh, c0, hi, p.D);
+      vr.read(p.v, p.vs, kh, c0, hi, p.D);
+      side.read(p, w.head, c0, hi);
+    };
+    if (Cfg<DP>::AHEAD) read(lo);
     for (int64_t c0 = lo; c0 < hi; c0 += B) {
       __syncthreads();
-      load_tile<DP>(K, p.k, p.ks, kh, c0, hi, p.D, 1.f);
-      load_tile<DP>(V, p.v, p.vs, kh, c0, hi, p.D, 1.f);
-      load_pos(pk, p, c0, hi);
+      if (!Cfg<DP>::AHEAD) read(c0);
+      kr.write(K, 1.f);
+      vr.write(V, 1.f);
+      side.write(pk, nullptr);
       __syncthreads();
+      if (Cfg<DP>::AHEAD && c0 + B < hi) read(c0 + B);
       if (!busy) continue;
       const int nc = (int)(hi - c0 < B ? hi - c0 : B);
-      float s[4][4];
+      float s[R][4];
       mm_nt<DP>(Q, K, nc, s);
-      float bias[4][4];
+      float bias[R][4];
       distances(p, pq, pk, slope, bias);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < R; ++i) {
         float top = m[i];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -315,7 +364,7 @@ __global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_fwd_kerne
         for (int j = 0; j < 4; ++j) {
           s[i][j] = exp_fast(s[i][j] - base);
           sum += s[i][j];
-          P[(4 * ty + i) * LDP + tx + 16 * j] = s[i][j];
+          P[(R * ty + i) * LDP + tx + 16 * j] = s[i][j];
         }
         l[i] = l[i] * fix + sum;          // this thread's columns; joined at the end
         const uint64_t fix2 = pk2(fix, fix);
@@ -328,13 +377,13 @@ __global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_fwd_kerne
       mm_nn<DP>(P, V, nc, o);
       __syncwarp();
     }
-    float inv[4];
+    float inv[R];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < R; ++i) {
 #pragma unroll
       for (int x = 8; x > 0; x >>= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], x);
       inv[i] = 1.f / l[i];
-      const int64_t r = r0 + 4 * ty + i;
+      const int64_t r = r0 + R * ty + i;
       if (tx == 0 && r < hi) p.lse[(int64_t)w.head * p.N + r] = m[i] + logf(l[i]);
     }
     store_rows<DP>(p.o, p.os, qh, r0, hi, p.D, o, inv);
@@ -359,7 +408,7 @@ __device__ __forceinline__ void tile_grad(const Params& p, float u, float dp, fl
 }
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_dq_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Cfg<DP>::THREADS, DP > 64 ? 1 : 2) attn_simt_dq_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) float sm[];
   float* Q = sm;
   float* G = Q + Cfg<DP>::TILE;
@@ -369,6 +418,7 @@ __global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_dq_kernel
   float* pq = P + B * LDP;
   float* pk = pq + kMaxAxes * B;
   float* dl = pk + kMaxAxes * B;
+  constexpr int R = Cfg<DP>::R;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   grid_dep_launch();
   grid_dep_wait();
@@ -387,49 +437,61 @@ __global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_dq_kernel
     load_tile<DP>(K, p.o, p.os, qh, r0, hi, p.D, 1.f);   // o, for delta
     load_tile<DP>(G, p.go, p.gos, qh, r0, hi, p.D, 1.f);
     load_tile<DP>(Q, p.q, p.qs, qh, r0, hi, p.D, p.scale);
-    load_pos(pq, p, r0, hi);
+    Side<DP, false> side;
+    side.read(p, w.head, r0, hi);
+    side.write(pq, nullptr);
     __syncthreads();
-    {   // delta of row t / 4, four threads a row
-      const int r = threadIdx.x >> 2;
+    {   // delta, TR threads a row
+      constexpr int TR = Cfg<DP>::THREADS / B;
+      const int r = threadIdx.x / TR;
       float d = 0.f;
-      for (int c = (threadIdx.x & 3); c < DP; c += 4) d = fmaf(G[r * Cfg<DP>::LD + c], K[r * Cfg<DP>::LD + c], d);
-      d += __shfl_xor_sync(0xffffffffu, d, 1);
-      d += __shfl_xor_sync(0xffffffffu, d, 2);
-      if ((threadIdx.x & 3) == 0) {
+      for (int c = threadIdx.x % TR; c < DP; c += TR) d = fmaf(G[r * Cfg<DP>::LD + c], K[r * Cfg<DP>::LD + c], d);
+#pragma unroll
+      for (int x = 1; x < TR; x *= 2) d += __shfl_xor_sync(0xffffffffu, d, x);
+      if (threadIdx.x % TR == 0) {
         dl[r] = d;
         if (r0 + r < hi) p.delta[(int64_t)w.head * p.N + r0 + r] = d;
       }
     }
     __syncthreads();
-    const bool busy = r0 + 8 * (threadIdx.x >> 5) < hi;
-    float lse[4], delta[4];
-    uint64_t acc[4][Cfg<DP>::DC][2];
+    const bool busy = r0 + 2 * R * (threadIdx.x >> 5) < hi;
+    float lse[R], delta[R];
+    uint64_t acc[R][Cfg<DP>::DC][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t r = r0 + 4 * ty + i;
+    for (int i = 0; i < R; ++i) {
+      const int64_t r = r0 + R * ty + i;
       lse[i] = r < hi ? p.lse[(int64_t)w.head * p.N + r] : 0.f;
-      delta[i] = dl[4 * ty + i];
+      delta[i] = dl[R * ty + i];
 #pragma unroll
       for (int c = 0; c < Cfg<DP>::DC; ++c) acc[i][c][0] = acc[i][c][1] = 0;
     }
+    Rows<DP> kr, vr;                       // the next moving tile
+    auto read = [&](int64_t c0) {
+      kr.read(p.k, p.ks, kh, c0, hi, p.D);
+      vr.read(p.v, p.vs, kh, c0, hi, p.D);
+      side.read(p, w.head, c0, hi);
+    };
+    if (Cfg<DP>::AHEAD) read(lo);
     for (int64_t c0 = lo; c0 < hi; c0 += B) {
       __syncthreads();
-      load_tile<DP>(K, p.k, p.ks, kh, c0, hi, p.D, 1.f);
-      load_tile<DP>(V, p.v, p.vs, kh, c0, hi, p.D, 1.f);
-      load_pos(pk, p, c0, hi);
+      if (!Cfg<DP>::AHEAD) read(c0);
+      kr.write(K, 1.f);
+      vr.write(V, 1.f);
+      side.write(pk, nullptr);
       __syncthreads();
+      if (Cfg<DP>::AHEAD && c0 + B < hi) read(c0 + B);
       if (!busy) continue;
       const int nc = (int)(hi - c0 < B ? hi - c0 : B);
-      float u[4][4], dp[4][4];
+      float u[R][4], dp[R][4];
       mm_nt<DP>(Q, K, nc, u);
       mm_nt<DP>(G, V, nc, dp);
-      float bias[4][4];
+      float bias[R][4];
       distances(p, pq, pk, slope, bias);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < R; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-          const int c = tx + 16 * j, r = 4 * ty + i;
+          const int c = tx + 16 * j, r = R * ty + i;
           float prob, du;
           tile_grad(p, u[i][j], dp[i][j], bias[i][j], lse[i], delta[i], r0 + r < hi && c0 + c < hi, icap, prob, du);
           P[r * LDP + c] = du;
@@ -438,13 +500,15 @@ __global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_dq_kernel
       mm_nn<DP>(P, K, nc, acc);
       __syncwarp();
     }
-    const float mul[4] = {p.scale, p.scale, p.scale, p.scale};
+    float mul[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) mul[i] = p.scale;
     store_rows<DP>(p.dq, p.dqs, qh, r0, hi, p.D, acc, mul);
   }
 }
 
 template <int DP>
-__global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_dkv_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(Cfg<DP>::THREADS, DP > 64 ? 1 : 2) attn_simt_dkv_kernel(const __grid_constant__ Params p) {
   extern __shared__ __align__(16) float sm[];
   float* K = sm;
   float* V = K + Cfg<DP>::TILE;
@@ -454,6 +518,7 @@ __global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_dkv_kerne
   float* pq = P + B * LDP;
   float* pk = pq + kMaxAxes * B;
   float* stat = pk + kMaxAxes * B;         // lse [64], delta [64]
+  constexpr int R = Cfg<DP>::R;
   const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
   grid_dep_launch();
   grid_dep_wait();
@@ -474,42 +539,48 @@ __global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_dkv_kerne
     __syncthreads();
     load_tile<DP>(K, p.k, p.ks, kh, r0, hi, p.D, 1.f);
     load_tile<DP>(V, p.v, p.vs, kh, r0, hi, p.D, 1.f);
-    load_pos(pk, p, r0, hi);
-    const bool busy = r0 + 8 * (threadIdx.x >> 5) < hi;
-    uint64_t dk[4][Cfg<DP>::DC][2], dv[4][Cfg<DP>::DC][2];
+    Side<DP, true> side;
+    side.read(p, w.head * rep, r0, hi);
+    side.write(pk, stat);                  // stat comes with each moving tile
+    const bool busy = r0 + 2 * R * (threadIdx.x >> 5) < hi;
+    uint64_t dk[R][Cfg<DP>::DC][2], dv[R][Cfg<DP>::DC][2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
+    for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int c = 0; c < Cfg<DP>::DC; ++c)
 #pragma unroll
         for (int k = 0; k < 2; ++k) dk[i][c][k] = dv[i][c][k] = 0;
+    Rows<DP> qr, gr;                       // the next moving tile
+    auto read = [&](int head, int64_t c0) {
+      qr.read(p.q, p.qs, (int64_t)head * p.D, c0, hi, p.D);
+      gr.read(p.go, p.gos, (int64_t)head * p.D, c0, hi, p.D);
+      side.read(p, head, c0, hi);
+    };
+    if (Cfg<DP>::AHEAD) read(w.head * rep, lo);
     for (int g = 0; g < rep; ++g) {
       const int head = w.head * rep + g;
-      const int64_t qh = (int64_t)head * p.D;
       const float slope = p.axes ? p.slopes[head] : 0.f;
       for (int64_t c0 = lo; c0 < hi; c0 += B) {
         __syncthreads();
-        load_tile<DP>(Q, p.q, p.qs, qh, c0, hi, p.D, p.scale);
-        load_tile<DP>(G, p.go, p.gos, qh, c0, hi, p.D, 1.f);
-        load_pos(pq, p, c0, hi);
-        if (threadIdx.x < B) {
-          const bool on = c0 + threadIdx.x < hi;
-          stat[threadIdx.x] = on ? p.lse[(int64_t)head * p.N + c0 + threadIdx.x] : 0.f;
-          stat[B + threadIdx.x] = on ? p.delta[(int64_t)head * p.N + c0 + threadIdx.x] : 0.f;
-        }
+        if (!Cfg<DP>::AHEAD) read(head, c0);
+        qr.write(Q, p.scale);
+        gr.write(G, 1.f);
+        side.write(pq, stat);
         __syncthreads();
+        if (Cfg<DP>::AHEAD && c0 + B < hi) read(head, c0 + B);
+        else if (Cfg<DP>::AHEAD && g + 1 < rep) read(head + 1, lo);
         if (!busy) continue;
         const int nc = (int)(hi - c0 < B ? hi - c0 : B);
-        float u[4][4], dp[4][4];
+        float u[R][4], dp[R][4];
         mm_nt<DP>(K, Q, nc, u);
         mm_nt<DP>(V, G, nc, dp);
-        float bias[4][4];
+        float bias[R][4];
         distances(p, pk, pq, slope, bias);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const int c = tx + 16 * j, r = 4 * ty + i;
+            const int c = tx + 16 * j, r = R * ty + i;
             float prob, du;
             tile_grad(p, u[i][j], dp[i][j], bias[i][j], stat[c], stat[B + c], r0 + r < hi && c0 + c < hi, icap, prob,
                       du);
@@ -520,15 +591,17 @@ __global__ void __launch_bounds__(kThreads, DP > 64 ? 1 : 2) attn_simt_dkv_kerne
         mm_nn<DP>(P, G, nc, dv);
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int i = 0; i < R; ++i)
 #pragma unroll
-          for (int j = 0; j < 4; ++j) P[(4 * ty + i) * LDP + tx + 16 * j] = dp[i][j];
+          for (int j = 0; j < 4; ++j) P[(R * ty + i) * LDP + tx + 16 * j] = dp[i][j];
         __syncwarp();
         mm_nn<DP>(P, Q, nc, dk);           // Q carries the scale
         __syncwarp();
       }
     }
-    const float one[4] = {1.f, 1.f, 1.f, 1.f};
+    float one[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) one[i] = 1.f;
     store_rows<DP>(p.dk, p.dks, kh, r0, hi, p.D, dk, one);
     store_rows<DP>(p.dv, p.dvs, kh, r0, hi, p.D, dv, one);
   }
@@ -540,7 +613,7 @@ template <int DP> constexpr int smem_bytes(int tiles) {
   return (tiles * Cfg<DP>::TILE + B * LDP + 2 * kMaxAxes * B + 2 * B) * (int)sizeof(float);
 }
 
-cudaError_t run(void (*k)(Params), int smem, Params p, int heads, cudaStream_t st) {
+cudaError_t run(void (*k)(Params), int smem, int threads, Params p, int heads, cudaStream_t st) {
   const int64_t longest = p.len;           // the document length that sets the blocks per head
   int64_t tiles = (longest + B - 1) / B;
   if (tiles < 1) tiles = 1;
@@ -551,19 +624,19 @@ cudaError_t run(void (*k)(Params), int smem, Params p, int heads, cudaStream_t s
   p.hint = (int)(tiles < room ? tiles : room);
   p.items = (uint32_t)(items * p.hint);
   cudaError_t e = set_smem_limit(reinterpret_cast<const void*>(k), smem);
-  if (e == cudaSuccess) e = launch_pdl(k, dim3(p.items), dim3(kThreads), (size_t)smem, st, p);
+  if (e == cudaSuccess) e = launch_pdl(k, dim3(p.items), dim3(threads), (size_t)smem, st, p);
   if (e == cudaSuccess) count_launches(1);
   return e;
 }
 
 template <int DP>
 cudaError_t forward(const Params& p, cudaStream_t st) {
-  return run(attn_simt_fwd_kernel<DP>, smem_bytes<DP>(3), p, p.H, st);
+  return run(attn_simt_fwd_kernel<DP>, smem_bytes<DP>(3), Cfg<DP>::THREADS, p, p.H, st);
 }
 template <int DP>
 cudaError_t backward(const Params& p, cudaStream_t st) {
-  const cudaError_t e = run(attn_simt_dq_kernel<DP>, smem_bytes<DP>(4), p, p.H, st);
-  return e != cudaSuccess ? e : run(attn_simt_dkv_kernel<DP>, smem_bytes<DP>(4), p, p.K, st);
+  const cudaError_t e = run(attn_simt_dq_kernel<DP>, smem_bytes<DP>(4), Cfg<DP>::THREADS, p, p.H, st);
+  return e != cudaSuccess ? e : run(attn_simt_dkv_kernel<DP>, smem_bytes<DP>(4), Cfg<DP>::THREADS, p, p.K, st);
 }
 
 cudaError_t dispatch(const Params& p, bool bwd, cudaStream_t st) {

@@ -212,9 +212,9 @@ class EQViTBlock(nn.Module):
         g = torch.Generator().manual_seed(seed)
         self.Cp, self.T, self.heads, self.native, self.cap = Cp, T, heads, bool(native), float(cap)
         self.rope = None if rope_sections is None else eqlin.Rope(T, Cp // heads, rope_sections, rope_base)
-        self.register_buffer("slopes", torch.tensor([2.0 ** (-8.0 * (h + 1) / heads) for h in range(heads)],
-                                                    dtype=torch.float32, device=device) if distance else None,
-                             persistent=False)
+        # a plain attribute: a buffer would follow the module into 16 bits
+        self.slopes = torch.tensor([2.0 ** (-8.0 * (h + 1) / heads) for h in range(heads)], dtype=torch.float32,
+                                   device=device) if distance else None
         self.norm1 = GroupLayerNorm(Cp, T, dtype=dtype, device=device, native=native)
         self.qkv = EQLinear(Cp, (heads + 2 * self.kv_heads) * (Cp // heads), T, dtype=dtype, device=device, generator=g)
         self.proj = EQLinear(Cp, Cp, T, dtype=dtype, device=device, generator=g)
@@ -233,10 +233,12 @@ class EQViTBlock(nn.Module):
             raise ValueError("x must be [B, L, C'*T], or [N, C'*T] with offsets")
         if pos is None and (self.rope is not None or self.slopes is not None):
             raise ValueError("rotary positions and the distance bias need pos")
+        if self.slopes is not None and self.slopes.device != x.device:
+            self.slopes = self.slopes.to(x.device)
         h = self.qkv(self.norm1(x))
         o = ops.qkv_attention(h.reshape(-1, self.heads + 2 * self.kv_heads, (self.Cp // self.heads) * self.T), self.heads,
                               self.kv_heads, plan=self.rope, pos=pos,
-                              slopes=None if self.slopes is None else self.slopes.float(),
+                              slopes=self.slopes,
                               docs=x.shape[0] if offsets is None else 1, offsets=offsets, max_len=max_len, cap=self.cap)
         y, x = self.norm2(x, self.proj(o.reshape(x.shape)))
         return x + self.fc2(F.gelu(self.fc1(y)))

@@ -8,6 +8,7 @@ using namespace eqlin;
 namespace {
 
 bool bad16(const void* p) { return ((uintptr_t)p & 15u) != 0; }
+bool bad4(const void* p) { return ((uintptr_t)p & 3u) != 0; }
 
 // Checks common to both directions; fills what they share.
 eqlin_status_t describe(const eqlin_attention_t* a, eqlin_dtype_t dtype, attn::Params& p) {
@@ -25,7 +26,8 @@ eqlin_status_t describe(const eqlin_attention_t* a, eqlin_dtype_t dtype, attn::P
   if (!a->offsets) {
     if (a->tokens > 0 && (a->docs < 1 || a->tokens % a->docs)) return EQLIN_ERR_INVALID_ARG;
   }
-  if ((a->docs + 1) * a->heads > 0x7fffffff) return EQLIN_ERR_UNSUPPORTED;
+  if (a->docs > 0x7fffffff || (a->docs + 1) * a->heads > 0x7fffffff) return EQLIN_ERR_UNSUPPORTED;
+  if (bad4(a->offsets) || bad4(a->pos) || bad4(a->slopes) || bad4(a->err)) return EQLIN_ERR_MISALIGNED;
   p = attn::Params{};
   p.N = a->tokens;
   p.H = (int)a->heads;
@@ -71,7 +73,7 @@ extern "C" eqlin_status_t eqlin_attention_forward(const eqlin_attention_t* a, eq
   if ((st = stride_ok(a->o_stride, p.H, p, dtype)) != EQLIN_OK) return st;
   if (p.N == 0) return EQLIN_OK;
   if (!q || !k || !v || !o || !lse || (p.axes && !p.pos)) return EQLIN_ERR_INVALID_ARG;
-  if (bad16(q) || bad16(k) || bad16(v) || bad16(o)) return EQLIN_ERR_MISALIGNED;
+  if (bad16(q) || bad16(k) || bad16(v) || bad16(o) || bad4(lse)) return EQLIN_ERR_MISALIGNED;
   p.q = q;
   p.k = k;
   p.v = v;
@@ -102,7 +104,8 @@ extern "C" eqlin_status_t eqlin_attention_backward(const eqlin_attention_t* a, e
   if (p.N == 0) return EQLIN_OK;
   if (!go || !q || !k || !v || !o || !lse || !dq || !dk || !dv || !delta || (p.axes && !p.pos))
     return EQLIN_ERR_INVALID_ARG;
-  if (bad16(go) || bad16(q) || bad16(k) || bad16(v) || bad16(o) || bad16(dq) || bad16(dk) || bad16(dv))
+  if (bad16(go) || bad16(q) || bad16(k) || bad16(v) || bad16(o) || bad16(dq) || bad16(dk) || bad16(dv) ||
+      bad4(lse) || bad4(delta))
     return EQLIN_ERR_MISALIGNED;
   p.q = q;
   p.k = k;

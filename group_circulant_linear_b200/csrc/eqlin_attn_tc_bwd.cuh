@@ -65,9 +65,9 @@ template <int DP, bool KEYS> struct BwdCfg {
 // halves), bias 2 + axes, the rest 5.  Two signs cancel to save two more: diff
 // is delta - dP and gain tanh^2 - 1, so that du is right, while eps and P g
 // (KEYS = false) come out negated, and so does not their product.
-template <int AXES, bool CAP, bool KEYS, bool SMALL, int CW, typename E>
+template <int AXES, bool CAP, bool KEYS, bool SMALL, bool EDGE, int CW, typename E>
 __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, const float* side, int c0, const float* own,
-                                       float lse2, float delta, const Score& sc, uint64_t& eps, uint32_t* pp,
+                                       float lse2, float delta, const Score& sc, int left, uint64_t& eps, uint32_t* pp,
                                        uint32_t* pd) {
   constexpr bool F16 = Pair<E>::fmt == 0;
   constexpr float kDown = F16 ? 1.f / 256.f : 1.f;
@@ -107,6 +107,10 @@ __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, c
       unpk2(fma2(x, k2, off), a, b);
       a = ex2(a);
       b = ex2(b);
+      if (EDGE) {                                    // no probability past the document's end
+        if (i >= left) a = 0.f;
+        if (i + 1 >= left) b = 0.f;
+      }
       // delta - dP under a cap, else dP - delta
       uint64_t diff;
       if (KEYS) {
@@ -364,21 +368,24 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
               tmem_wait_ld();
               tie32(rs);
               tie32(rd);
-              // Past the document's end: P = 0 and dP = delta, so that nothing adds to eps or du.  Under a cap
-              // P is what -cap gives, at most 1, and its product with g is 0.  KEYS: lse is +inf there, so any
-              // finite score will do.
-              if ((!KEYS || CAP) && c * 32 + 32 > nc) {
+              // Past the document's end dP = delta, and P = 0 by a raw score of -inf or, where a cap would bring that
+              // back to -cap, by EDGE.  KEYS: lse is +inf there, so any finite score will do.
+              const int left = nc - c * 32;
+              if ((!KEYS || CAP) && left < 32) {
 #pragma unroll
                 for (int k = 0; k < 32; ++k)
-                  if (c * 32 + k >= nc) {
-                    rs[k] = KEYS ? 0u : __float_as_uint(-INFINITY);
+                  if (k >= left) {
+                    rs[k] = KEYS || CAP ? 0u : __float_as_uint(-INFINITY);
                     if (!KEYS) rd[k] = __float_as_uint(delta);
                   }
               }
-              if (CAP && all_small<32>(reinterpret_cast<const float*>(rs), sc, live))
-                grad32<AXES, CAP, KEYS, true, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);
+              if (CAP && !KEYS && left < 32)
+                grad32<AXES, CAP, KEYS, false, CAP && !KEYS, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, left, eps2,
+                                                                    pp, pd);
+              else if (CAP && all_small<32>(reinterpret_cast<const float*>(rs), sc, live))
+                grad32<AXES, CAP, KEYS, true, false, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, 32, eps2, pp, pd);
               else
-                grad32<AXES, CAP, KEYS, false, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, eps2, pp, pd);
+                grad32<AXES, CAP, KEYS, false, false, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, 32, eps2, pp, pd);
               tmem_st_32x32b_x16(my + C::S_COL + c * 32, pp);
               tmem_st_32x32b_x16(my + C::DP_COL + c * 32, pd);
             }

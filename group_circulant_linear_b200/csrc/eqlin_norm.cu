@@ -477,6 +477,8 @@ cudaError_t dispatch(eqlin_dtype_t dt, const Params& p, const Shape& s, bool bwd
 }
 
 bool bad16(const void* p) { return ((uintptr_t)p & 15u) != 0; }
+bool bad4(const void* p) { return ((uintptr_t)p & 3u) != 0; }
+bool bad_elem(const void* p, eqlin_dtype_t dt) { return ((uintptr_t)p & (dt == EQLIN_F32 ? 3u : 1u)) != 0; }
 
 eqlin_status_t check(int T, int64_t Cp, eqlin_dtype_t dt, int64_t N) {
   if (dt != EQLIN_F32 && dt != EQLIN_F16 && dt != EQLIN_BF16) return EQLIN_ERR_INVALID_ARG;
@@ -511,7 +513,9 @@ extern "C" eqlin_status_t eqlin_norm_forward(int T, int64_t Cp, eqlin_dtype_t dt
   if (!w || !b || !(eps >= 0.f) || (res == nullptr) != (sum == nullptr)) return EQLIN_ERR_INVALID_ARG;
   if (N == 0) return EQLIN_OK;
   if (!x || !y || !mean || !rstd) return EQLIN_ERR_INVALID_ARG;
-  if (norm::bad16(x) || norm::bad16(res) || norm::bad16(sum) || norm::bad16(y)) return EQLIN_ERR_MISALIGNED;
+  if (norm::bad16(x) || norm::bad16(res) || norm::bad16(sum) || norm::bad16(y) || norm::bad_elem(w, dtype) ||
+      norm::bad_elem(b, dtype) || norm::bad4(mean) || norm::bad4(rstd))
+    return EQLIN_ERR_MISALIGNED;
   norm::Params p = norm::describe(T, Cp, dtype, N);
   p.x = x;
   p.res = res;
@@ -533,7 +537,7 @@ extern "C" eqlin_status_t eqlin_norm_forward(int T, int64_t Cp, eqlin_dtype_t dt
 }
 
 extern "C" int64_t eqlin_norm_workspace_bytes(int T, int64_t Cp, int64_t N) {
-  if (T < 1 || T > 16 || Cp < 1 || Cp * T > norm::kMaxF || N < 0) return -1;
+  if (T < 1 || T > 16 || Cp < 1 || Cp > norm::kMaxF || Cp * T > norm::kMaxF || N < 0) return -1;
   return norm::parts_of(N) * 2 * Cp * (int64_t)sizeof(float);
 }
 
@@ -544,6 +548,7 @@ extern "C" eqlin_status_t eqlin_norm_backward(int T, int64_t Cp, eqlin_dtype_t d
   const eqlin_status_t st = norm::check(T, Cp, dtype, N);
   if (st != EQLIN_OK) return st;
   if (!w || !dw || !db) return EQLIN_ERR_INVALID_ARG;
+  if (norm::bad_elem(w, dtype) || norm::bad4(dw) || norm::bad4(db)) return EQLIN_ERR_MISALIGNED;
   cudaStream_t cs = static_cast<cudaStream_t>(stream);
   if (N == 0) {
     cudaError_t e = cudaMemsetAsync(dw, 0, (size_t)Cp * sizeof(float), cs);
@@ -551,7 +556,8 @@ extern "C" eqlin_status_t eqlin_norm_backward(int T, int64_t Cp, eqlin_dtype_t d
     return e == cudaSuccess ? EQLIN_OK : EQLIN_ERR_CUDA;
   }
   if (!gy || !x || !mean || !rstd || !dx || !workspace) return EQLIN_ERR_INVALID_ARG;
-  if (norm::bad16(gy) || norm::bad16(gsum) || norm::bad16(x) || norm::bad16(res) || norm::bad16(dx) || norm::bad16(workspace))
+  if (norm::bad16(gy) || norm::bad16(gsum) || norm::bad16(x) || norm::bad16(res) || norm::bad16(dx) || norm::bad16(workspace) ||
+      norm::bad4(mean) || norm::bad4(rstd))
     return EQLIN_ERR_MISALIGNED;
   norm::Params p = norm::describe(T, Cp, dtype, N);
   p.x = x;

@@ -201,8 +201,8 @@ extern "C" eqlin_status_t eqlin_rope_apply(eqlin_rope_t r, eqlin_dtype_t dtype, 
                                            int inverse, int64_t N, void* stream) {
   if (!r || (dtype != EQLIN_F32 && dtype != EQLIN_F16 && dtype != EQLIN_BF16)) return EQLIN_ERR_INVALID_ARG;
   if (N < 0 || heads < 1) return EQLIN_ERR_INVALID_ARG;
-  const int64_t width = heads * r->plan.Ch * r->plan.T;
   if (heads > 65536) return EQLIN_ERR_UNSUPPORTED;
+  const int64_t width = heads * r->plan.Ch * r->plan.T;
   if (src_stride < width || dst_stride < width) return EQLIN_ERR_INVALID_ARG;
   if (N == 0) return EQLIN_OK;
   if (!pos || !src || !dst) return EQLIN_ERR_INVALID_ARG;

@@ -356,7 +356,11 @@ EQLIN_API eqlin_status_t eqlin_rope_apply(eqlin_rope_t r, eqlin_dtype_t dtype, c
  * n * stride, so q, k and v may be parts of one packed projection; strides and
  * head_dim are multiples of 16 bytes, head_dim <= 128.  lse is [heads, tokens]
  * float32.  Rows outside every document get o = 0, lse = 0 and zero gradients;
- * what the inputs hold there is not looked at.
+ * what the inputs hold there is not looked at.  Outputs must not overlap inputs
+ * or one another.  q, k, v, o and their gradients are 16-byte aligned.
+ * f16 and bf16 run on the tensor cores (probabilities and score gradients pass
+ * through the inputs' type on their way into a product, all sums are FP32), f32
+ * on the CUDA cores.
  */
 typedef struct {
     int64_t tokens, heads, kv_heads, head_dim;

@@ -283,3 +283,24 @@ def test_attention_on_another_stream_and_wait_limit():
     eqlin.attention_forward(q, k, v, o2, l2)
     torch.cuda.synchronize()
     assert torch.equal(o1, o2)
+
+
+@pytest.mark.gpu
+def test_block_command_times_the_native_block(capsys):
+    import json
+
+    from group_circulant_linear_b200 import block
+    block.main(["--native", "--model", "eq-vit-s", "--batch", "2", "--iters", "2", "--warmup", "1"])
+    out = json.loads(capsys.readouterr().out)
+    assert out["native_fwd_ms"] > 0 and out["native_fwd_bwd_ms"] > 0
+
+
+@pytest.mark.gpu
+def test_native_block_deepcopy_and_16_bit_cast():
+    import copy
+    blk = make(torch.bfloat16)
+    twin = copy.deepcopy(blk).to(torch.bfloat16)
+    assert twin.slopes.dtype == torch.float32 and torch.equal(twin.slopes, blk.slopes)
+    x = torch.randn((1, 20, 128), generator=torch.Generator().manual_seed(0)).bfloat16().cuda()
+    with torch.no_grad():
+        assert torch.equal(blk(x, grid_positions(4, 5)), twin(x, grid_positions(4, 5)))

@@ -309,7 +309,7 @@ def attention_bounds(q, k, v, go, lens, lead, cap, pos, slopes, scale, dt, p16):
 
 
 def run_attention(lens, lead, tail, H, K, D, cap, axes, dtype, seed=0, uniform=False, packed=True, scale=None,
-                  q_std=2.0, poison=True, max_len="max"):
+                  q_std=2.0, poison=True, max_len="max", slope=0.3):
     dt = DT[dtype]
     g = torch.Generator().manual_seed(seed)
     N = lead + sum(lens) + tail
@@ -318,7 +318,7 @@ def run_attention(lens, lead, tail, H, K, D, cap, axes, dtype, seed=0, uniform=F
     qkv = qkv.to(dt)
     go = torch.randn((N, H, D), generator=g).to(dt)
     pos = torch.randint(0, 30, (N, axes), generator=g).float() if axes else None
-    slopes = torch.rand(H, generator=g) * 0.3 if axes else None
+    slopes = torch.rand(H, generator=g) * slope if axes else None
     scale = D ** -0.5 if scale is None else scale
     val, tol = attention_bounds(qkv[:, :H], qkv[:, H:H + K], qkv[:, H + K:], go, lens, lead, cap, pos, slopes, scale, dt,
                                 dtype != "f32")
@@ -447,6 +447,16 @@ def test_attention_documents_do_not_see_each_other(dtype, cap):
 
 @pytest.mark.gpu
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("cap", [0.0, 8.0])
+@pytest.mark.parametrize("slope,scale", [(-0.5, None), (0.0, 0.01), (4.0, 1.5)])
+def test_attention_any_slopes_and_scales(slope, scale, cap, dtype):
+    # a bias that grows with the distance, none at all, and one that leaves next to nothing
+    run_attention([70, 33, 101], 1, 2, 2, 2, 64, cap, 2, dtype, slope=slope, scale=scale)
+    run_attention([70, 33, 101], 1, 2, 2, 1, 128, cap, 3, dtype, slope=slope, scale=scale)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 def test_attention_large_scores(dtype):
     # scores of several hundred units: the running maximum moves far, capped and not
     run_attention([190, 300], 0, 0, 2, 2, 64, 0.0, 0, dtype, q_std=60.0, seed=4)
@@ -567,6 +577,11 @@ def test_norm_refusals():
 
     for name in ("gy", "x", "w", "mean", "rstd", "dx", "dw", "db", "ws"):
         assert bwd(**{name: None}) == -1, name
+    for name in ("mean", "rstd", "dw", "db"):
+        assert bwd(**{name: ctypes.c_void_p(4098)}) == -3, name
+    for name in ("w", "b", "mean", "rstd"):
+        assert fwd(**{name: ctypes.c_void_p(4097)}) == -3, name
+    assert L.eqlin_norm_workspace_bytes(4, 2 ** 62, 2) == -1
     for name in ("gy", "gs", "x", "res", "dx", "ws"):
         assert bwd(**{name: ctypes.c_void_p(4100)}) == -3, name
     assert bwd(T=17) == -2 and bwd(Cp=3) == -3 and bwd(N=-2) == -1
@@ -599,6 +614,7 @@ def test_rope_refusals():
     assert call(r=None) == -1 and call(dt=5) == -1 and call(heads=0) == -1 and call(N=-1) == -1
     assert call(ss=63) == -1 and call(ds=63) == -1 and call(pos=None) == -1 and call(src=None) == -1
     assert call(dst=None) == -1 and call(src=ctypes.c_void_p(4097)) == -3 and call(heads=70000, ss=2 ** 40, ds=2 ** 40) == -2
+    assert call(heads=2 ** 62) == -2
     assert call(N=0) == 0
     import copy
     import pickle
@@ -628,7 +644,9 @@ def test_attention_refusals():
     assert call(q_stride=33) == -3 and call(tokens=2 ** 31, docs=1) == -2 and call(docs=2 ** 30, offsets=4096) == -2
     for name in ("q", "k", "v", "o"):
         assert call(**{name: None}) == -1 and call(**{name: ctypes.c_void_p(4098)}) == -3, name
-    assert call(lse=None) == -1
+    assert call(lse=None) == -1 and call(lse=ctypes.c_void_p(4098)) == -3 and call(docs=2 ** 62, offsets=4096) == -2
+    for name in ("offsets", "err", "pos", "slopes"):
+        assert call(**{name: 4097}) == -3, name
     assert call(tokens=0) == 0 and call(tokens=0, docs=0) == 0
 
     def back(dt=eqlin.BF16, go=one, gs=32, dq=one, dqs=32, dk=one, dks=16, dv=one, dvs=16, delta=one, **kw):

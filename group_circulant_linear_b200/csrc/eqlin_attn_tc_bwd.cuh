@@ -330,23 +330,32 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
     const uint32_t my = tmem + ((uint32_t)(quarter * 32) << 16);
     uint32_t item = 0;
     bool ok = true;
+    // A tile's own rows: positions and, where queries own, lse (base 2) and the
+    // first guess of delta.  Read while the tile before ends.
+    Tile w;
+    float own[AXES ? AXES : 1], lse2 = 0.f, delta = 0.f;
+    auto enter = [&](uint32_t i) {
+      w = tile_at(p, heads, list, i);
+      const int r0 = w.first + quarter * 32;
+      const int64_t row = (int64_t)r0 + lane;
+      const bool live = row < w.hi;
+#pragma unroll
+      for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
+      if (!KEYS && r0 < w.hi) {
+        const int64_t at = (int64_t)w.head * p.D;
+        delta = row_dots(static_cast<const E*>(p.go) + (int64_t)r0 * p.gos + at, p.gos,
+                         static_cast<const E*>(p.o) + (int64_t)r0 * p.os + at, p.os, w.hi - r0, p.D, lane);
+        lse2 = live ? p.lse[(int64_t)w.head * p.N + row] * kLog2e : 0.f;
+      }
+    };
+    enter(0);
     for (uint32_t i = 0; ok && i < count; ++i) {
-      const Tile w = tile_at(p, heads, list, i);
       const int kv_head = KEYS ? w.head : w.head / rep, q_head = KEYS ? w.head * rep : w.head;
       const int64_t kh = (int64_t)kv_head * p.D, qh0 = (int64_t)q_head * p.D;
       const int lo = w.lo, hi = w.hi, tiles = (hi - lo - 1) / CW + 1;   // moving tiles of one head
       const int r0 = w.first + quarter * 32;
       const bool any = r0 < hi, live = lane < hi - r0;
       const int64_t row = (int64_t)r0 + lane;
-      float own[AXES ? AXES : 1];
-#pragma unroll
-      for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
-      float lse2 = 0.f, delta = 0.f;                 // of the own row (queries own)
-      if (!KEYS && any) {
-        delta = row_dots(static_cast<const E*>(p.go) + (int64_t)r0 * p.gos + qh0, p.gos,
-                         static_cast<const E*>(p.o) + (int64_t)r0 * p.os + qh0, p.os, hi - r0, p.D, lane);
-        if (live) lse2 = p.lse[(int64_t)w.head * p.N + row] * kLog2e;
-      }
       uint64_t eps2 = 0;
       for (int g = 0; ok && g < passes; ++g) {
         const Score sc = score_of(p, q_head + g);
@@ -396,6 +405,8 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
         }
       }
       if (!ok) break;
+      const float guess = delta;
+      if (i + 1 < count) enter(i + 1);
       ok = wwait_all(acc_full, (item - 1) & 1, limit, abort_flag, err, site(KID, 0, 3), item);
       if (!ok) break;
       tc_fence_after();
@@ -410,7 +421,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
           eps = eps_sum[quarter * 32 + lane] + eps_sum[ROWS + quarter * 32 + lane];
           named_bar_sync(1, NWG * 128);
         }
-        if (live && wg == 0) p.delta[(int64_t)w.head * p.N + row] = CAP ? delta - eps : delta + eps;
+        if (live && wg == 0) p.delta[(int64_t)q_head * p.N + row] = CAP ? guess - eps : guess + eps;
       }
       if (any) {
 #pragma unroll

@@ -51,7 +51,7 @@ template <int DP, bool KEYS> struct BwdCfg {
   static constexpr int MOV = DP / 64 * MOV_PANEL;               // bytes of one moving tile
   static constexpr int SLOTS = DP > 64 ? 2 : 4;
   static constexpr int SIDE = (kMaxAxes + (KEYS ? 2 : 0)) * CW * 4;            // positions, lse, delta of a slot
-  static constexpr int NBAR = 2 + 3 * SLOTS + 4;
+  static constexpr int NBAR = 2 + 3 * SLOTS + 5;
   static constexpr int EPS = NWG == 2 ? 2 * ROWS * 4 : 0;       // eps of the two warpgroups
   static constexpr int SMEM = 2 * OWN + SLOTS * (2 * MOV + SIDE) + EPS + NWG * 4 * STAGE + NBAR * 8 + 32 + kListInts * 4 + 1024;
   static_assert(ACC1 + DP <= TMEM, "TMEM columns");
@@ -159,7 +159,8 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
   uint64_t* s_full = land + C::SLOTS;
   uint64_t* p_full = s_full + 1;
   uint64_t* acc_full = p_full + 1;
-  uint64_t* drain = acc_full + 1;
+  uint64_t* eps_full = acc_full + 1;
+  uint64_t* drain = eps_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
   int* local_err = abort_word + 1;
@@ -193,6 +194,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
     mbar_init(s_full, 1);
     mbar_init(p_full, NWG * 128);
     mbar_init(acc_full, 1);
+    mbar_init(eps_full, NWG * 128);
     mbar_init(drain, 1);
     *abort_word = 0;
     for (int i = 0; i < 4; ++i) local_err[i] = 0;
@@ -416,10 +418,13 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
         unpk2(eps2, a, b);
         eps = a + b;
         if (NWG == 2) {                              // the two halves of the row's columns
+          // (a bounded wait, not a block barrier: a warp that gave up does not come here; the next tile's sums are
+          // written after every warp has passed this one's scores, and so this)
           eps_sum[wg * ROWS + quarter * 32 + lane] = eps;
-          named_bar_sync(1, NWG * 128);
+          mbar_arrive(eps_full);
+          ok = wwait_all(eps_full, i & 1, limit, abort_flag, err, site(KID, 0, 4), item);
+          if (!ok) break;
           eps = eps_sum[quarter * 32 + lane] + eps_sum[ROWS + quarter * 32 + lane];
-          named_bar_sync(1, NWG * 128);
         }
         if (live && wg == 0) p.delta[(int64_t)q_head * p.N + row] = CAP ? guess - eps : guess + eps;
       }

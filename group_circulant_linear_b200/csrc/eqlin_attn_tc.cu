@@ -417,7 +417,8 @@ cudaError_t forward_axes(const Params& p, const Maps& maps, cudaStream_t st) {
 template <int DP, int CW, typename E>
 cudaError_t forward_cap(const Params& p, cudaStream_t st) {
   Maps maps;
-  cudaError_t e = make_map(&maps.m[0], p.q, Pair<E>::fmt, p, p.H, p.qs, ROWS);
+  cudaError_t e = enter_context();
+  if (e == cudaSuccess) e = make_map(&maps.m[0], p.q, Pair<E>::fmt, p, p.H, p.qs, ROWS);
   if (e == cudaSuccess) e = make_map(&maps.m[1], p.k, Pair<E>::fmt, p, p.K, p.ks, CW);
   if (e == cudaSuccess) e = make_map(&maps.m[2], p.v, Pair<E>::fmt, p, p.K, p.vs, CW);
   if (e != cudaSuccess) return e;

@@ -2,7 +2,7 @@
 //
 // All of them have one shape: 128 rows stay ("own" rows: queries, or keys in
 // the kernel for dk and dv), the other side passes by in tiles of up to 128
-// ("moving" rows).  A block is six warps:
+// ("moving" rows).  A block is six warps, or ten with two threads per own row:
 //
 //   warps 0-3   one thread per own row: scores out of TMEM, softmax (or its
 //               gradient) in FP32 registers, 16-bit probabilities back into
@@ -436,6 +436,15 @@ __device__ __forceinline__ void transform32(float* s, const float* pos, int c0, 
 struct Maps {
   CUtensorMap m[4];
 };
+
+// Make the current device's context current in this host thread, too: one that
+// has only selected the device (an autograd worker, say) may not have it yet,
+// and encoding a tensor map needs it.
+inline cudaError_t enter_context() {
+  int dev = 0;
+  const cudaError_t e = cudaGetDevice(&dev);
+  return e != cudaSuccess ? e : cudaSetDevice(dev);
+}
 
 // A map over [N][heads][D] for boxes of 64 features x one head x `rows` tokens.
 inline cudaError_t make_map(CUtensorMap* map, const void* base, uint32_t fmt, const Params& p, int heads, int64_t stride,

@@ -28,7 +28,10 @@
 // A thread owns one row and 64 columns of a tile (NWG warpgroups of rows, the
 // 32-column chunks dealt out in turn).  P and du lie over the scores they came
 // from, chunk by chunk: the accumulators take the rest of the columns, and the
-// SM's other block fills the gap until the next scores.
+// SM's other block fills the gap until the next scores.  Measured, bf16, both
+// kernels: 12544 tokens, 6 heads of 64, 1.23 ms (490 TFLOP/s of the formula's five
+// products); 64 x 197 tokens, 12 heads, capped, two-axis bias, 173 us; one tile of
+// 64 moving rows takes an SM about 1550 cycles, 512 of them exponentials.
 #pragma once
 
 #include "eqlin_attn_tc.cuh"
@@ -61,10 +64,11 @@ template <int DP, bool KEYS> struct BwdCfg {
 // One 32-column chunk of a row: raw scores rs and dP rd in, packed P and du out.
 //   KEYS: -lse and delta belong to the columns (in shared memory, in base 2 and
 //   scaled), else to the row.
-// In FMA-pipe operations per element, which bound this under a cap: tanh 8 (16
-// halves), bias 2 + axes, the rest 5.  Two signs cancel to save two more: diff
-// is delta - dP and gain tanh^2 - 1, so that du is right, while eps and P g
-// (KEYS = false) come out negated, and so does not their product.
+// FMA-pipe operations per element, which bound this under a cap: 8 for the tanh
+// and its derivative, 2 axes for the bias, 5 for the rest.  Two signs cancel to
+// save two more: under a cap diff is delta - dP and gain tanh^2 - 1, so that du
+// is right, while eps and P g (KEYS = false) come out negated, and so does not
+// their product.
 template <int AXES, bool CAP, bool KEYS, bool SMALL, bool EDGE, int CW, typename E>
 __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, const float* side, int c0, const float* own,
                                        float lse2, float delta, const Score& sc, int left, uint64_t& eps, uint32_t* pp,
@@ -484,7 +488,8 @@ cudaError_t backward_cap(const Params& p, cudaStream_t st) {
   constexpr uint32_t fmt = Pair<E>::fmt;
   constexpr int CW = BwdCfg<DP, KEYS>::CW;
   Maps maps;                                         // own tiles A0, A1, moving tiles X, Y
-  cudaError_t e = make_map(&maps.m[KEYS ? 2 : 0], p.q, fmt, p, p.H, p.qs, KEYS ? CW : ROWS);
+  cudaError_t e = enter_context();
+  if (e == cudaSuccess) e = make_map(&maps.m[KEYS ? 2 : 0], p.q, fmt, p, p.H, p.qs, KEYS ? CW : ROWS);
   if (e == cudaSuccess) e = make_map(&maps.m[KEYS ? 3 : 1], p.go, fmt, p, p.H, p.gos, KEYS ? CW : ROWS);
   if (e == cudaSuccess) e = make_map(&maps.m[KEYS ? 0 : 2], p.k, fmt, p, p.K, p.ks, KEYS ? ROWS : CW);
   if (e == cudaSuccess) e = make_map(&maps.m[KEYS ? 1 : 3], p.v, fmt, p, p.K, p.vs, KEYS ? ROWS : CW);

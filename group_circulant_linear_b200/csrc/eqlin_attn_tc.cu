@@ -17,12 +17,14 @@
 //   CW = 64    S, then P in its place, then the next S.
 //   CW = 128   P has columns of its own and the next S is issued while P is
 //              formed; half the hand-overs, but its 128 scores per thread only
-//              stay in registers for whole tiles away from the cap.
+//              stay in registers in whole tiles away from the cap and, without a
+//              cap and a bias, in a document's last tile.
 // CW = 128 is taken for heads of up to 64 features (its columns need them) in
-// documents of 512 tokens and more on average.  CW 128 against 64, heads of 64:
-// 12544 tokens, 6 heads 379 us against 534 (595 against 786 capped); 30 x 600
-// tokens, 6 heads 47 against 57 (96 against 93 capped and biased); 64 x 197
-// tokens, 12 heads 48 against 40 (103 against 65); windows of 49 127 against 64.
+// documents that are long on average: from 384 tokens, with a cap or a bias from
+// 768.  CW 128 against 64, heads of 64, us: 12544 tokens, 6 heads 359 : 531
+// (biased 618 : 746, capped 625 : 761); 30 x 900 tokens, 6 heads 92 : 110 (capped
+// and biased 191 : 190); 30 x 500, 12 heads 61 : 66 (137 : 111); 30 x 384, 12 heads
+// 36 : 41 (62 : 68); 30 x 300, 12 heads 37 : 34; 64 x 197, 12 heads 42 : 41 (90 : 65).
 #include "eqlin_attn_tc.cuh"
 
 namespace eqlin {
@@ -45,7 +47,7 @@ template <int DP, int CW_> struct FwdCfg {
   static_assert(O_COL + DP <= TMEM, "TMEM columns");
   static_assert(2 * (SMEM + 1024) <= 228 * 1024, "shared memory");
 };
-constexpr int kWideFrom = 512;                                // average tokens of a document
+constexpr int kWideFrom = 384, kWideFromBiased = 768;         // average tokens of a document
 
 template <int DP, int CW, typename E, int AXES, bool CAP>
 __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_constant__ Params p,
@@ -271,9 +273,15 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
             for (int c = 0; c < CW / 32; ++c)
               if (c * 32 < nc) chunk(s + c * 32, c, nc - c * 32);
           } else {
-            bool fast = nc == CW;
+            constexpr bool PLAIN = !CAP && AXES == 0;
+            bool fast = PLAIN || nc == CW;
             if (fast) {
               load();
+              if (PLAIN && nc < CW) {                       // the document ends in this tile
+#pragma unroll
+                for (int i = 0; i < CW; ++i)
+                  if (i >= nc) s[i] = -INFINITY;
+              }
               if (CAP) fast = all_small<CW>(s, sc, live);
             }
             if (fast) {
@@ -429,7 +437,8 @@ template <typename E>
 cudaError_t forward_dim(const Params& p, cudaStream_t st) {
   if (p.D > 64) return forward_cap<128, 64, E>(p, st);
   // by the average length, not by max_len: results do not depend on that
-  return p.N >= kWideFrom * p.docs ? forward_cap<64, 128, E>(p, st) : forward_cap<64, 64, E>(p, st);
+  const int64_t from = p.cap > 0.f || p.axes ? kWideFromBiased : kWideFrom;
+  return p.N >= from * p.docs ? forward_cap<64, 128, E>(p, st) : forward_cap<64, 64, E>(p, st);
 }
 
 }  // namespace attn_tc

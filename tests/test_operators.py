@@ -375,7 +375,7 @@ ATTN_CASES = [  # lens, lead, tail, H, K, D, cap, axes
     # many documents in a block's 128 tokens, runs of empty ones, whole blocks outside
     ([1] * 150 + [0] * 70 + [3] * 20 + [0] * 3 + [130, 0, 1], 140, 150, 2, 1, 64, 0.0, 1),
     ([0] * 40 + [127, 1, 128, 129], 128, 1, 1, 1, 32, 9.0, 0),
-    # documents of 512 tokens and more on average: the forward's wide form
+    # documents of 384 (768 with a cap or bias) tokens and more on average: the forward's wide form
     ([1100], 0, 0, 1, 1, 64, 20.0, 2),
     ([2177, 150], 3, 5, 1, 1, 32, 0.0, 3),
     ([1024 + 65], 0, 0, 2, 1, 56, 0.0, 0),

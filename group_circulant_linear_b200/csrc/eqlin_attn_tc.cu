@@ -25,6 +25,8 @@
 // (biased 618 : 746, capped 625 : 761); 30 x 900 tokens, 6 heads 92 : 110 (capped
 // and biased 191 : 190); 30 x 500, 12 heads 61 : 66 (137 : 111); 30 x 384, 12 heads
 // 36 : 41 (62 : 68); 30 x 300, 12 heads 37 : 34; 64 x 197, 12 heads 42 : 41 (90 : 65).
+#include <float.h>
+
 #include "eqlin_attn_tc.cuh"
 
 namespace eqlin {
@@ -324,6 +326,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
             top = fmaxf(fmaxf(t0, t1), v[31]);
           }
           top *= sc.scale2;                                 // scale > 0
+          if (AXES) top = fmaxf(top, -FLT_MAX);             // where every key of the tile is infinitely far away
         }
         if (C::SEP && j > 0) {                              // P's columns, and O, are free once the last product is done
           ok = wwait_all(o_full, (step - 1) & 1, limit, abort_flag, err, site(K_ATTN_FWD, 0, 2), step);

@@ -466,6 +466,31 @@ def test_attention_large_scores(dtype):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("lead,rest,cap", [(1, 60, 0.0), (130, 90, 5.0), (300, 900, 0.0), (300, 900, 5.0)])
+def test_attention_keys_infinitely_far_away(lead, rest, cap, dtype):
+    # whole tiles of keys at an infinite distance come first: the others must not notice
+    H, D, N = 2, 64, lead + rest
+    dt = DT[dtype]
+    g = torch.Generator().manual_seed(6)
+    q, k, v = (torch.randn((N, H, D), generator=g).to(dt).cuda() for _ in range(3))
+    pos = torch.randint(0, 20, (N, 2), generator=g).float().cuda()
+    pos[:lead, 1] = math.inf
+    slopes = torch.tensor([0.5, 0.125], device="cuda")
+    o, lse = torch.empty_like(q), torch.empty((H, N), device="cuda")
+    eqlin.attention_forward(q, k, v, o, lse, pos=pos, slopes=slopes, cap=cap)
+    near = [t[lead:].contiguous() for t in (q, k, v)]
+    o2, lse2 = torch.empty_like(near[0]), torch.empty((H, rest), device="cuda")
+    eqlin.attention_forward(*near, o2, lse2, pos=pos[lead:].contiguous(), slopes=slopes, cap=cap)
+    # either result: P and o rounded to the type, half a step each (f32: neither), sums of up to N
+    # terms in another order, 2^-21 for each exponential and score
+    half = 0.0 if dtype == "f32" else torch.finfo(dt).eps / 2
+    tol = 2 * (2 * half + N * 2.0 ** -24 + 2.0 ** -20 * (8 + float(lse2.abs().max())))
+    assert float((o[lead:].float() - o2.float()).abs().max()) <= tol * float(v.float().abs().max())
+    assert float((lse[:, lead:] - lse2).abs().max()) <= 2 * (N * 2.0 ** -24 + 2.0 ** -20 * (8 + float(lse2.abs().max())))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("N", [700, 1200])
 def test_attention_rising_scores(N):
     # keys ordered so that each tile's maximum is above the last one's

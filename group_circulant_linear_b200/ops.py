@@ -138,6 +138,16 @@ def _aligned(x):
     return x
 
 
+_SHARED = ("offsets", "pos", "slopes")        # tensors that both directions read
+
+
+def _read_again(ctx, kw, *tensors):
+    """Save a call's tensors, the shared ones with them: changed in place before
+    the backward, they would be read as something else, which torch refuses."""
+    ctx.save_for_backward(*tensors, *(kw[n] for n in _SHARED))
+    ctx.kw = {n: v for n, v in kw.items() if n not in _SHARED}
+
+
 class _Attention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, kw):
@@ -146,17 +156,17 @@ class _Attention(torch.autograd.Function):
         o = torch.empty(q.shape, dtype=q.dtype, device=q.device)
         lse = torch.empty((H, N), dtype=torch.float32, device=q.device)
         eqlin.attention_forward(q, k, v, o, lse, **kw)
-        ctx.save_for_backward(q, k, v, o, lse)
-        ctx.kw = kw
+        _read_again(ctx, kw, q, k, v, o, lse)
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, go):
-        q, k, v, o, lse = ctx.saved_tensors
+        q, k, v, o, lse, *shared = ctx.saved_tensors
         go = _aligned(go)
         dq, dk, dv = (torch.empty(t.shape, dtype=t.dtype, device=t.device) for t in (q, k, v))
-        eqlin.attention_backward(go, q, k, v, o, lse, dq, dk, dv, torch.empty_like(lse), **ctx.kw)
+        eqlin.attention_backward(go, q, k, v, o, lse, dq, dk, dv, torch.empty_like(lse), **ctx.kw,
+                                 **dict(zip(_SHARED, shared)))
         return dq, dk, dv, None
 
 
@@ -192,19 +202,19 @@ class _QkvAttention(torch.autograd.Function):
         o = torch.empty((N, H, D), dtype=qkv.dtype, device=qkv.device)
         lse = torch.empty((H, N), dtype=torch.float32, device=qkv.device)
         eqlin.attention_forward(qk[:, :H], qk[:, H:], qkv[:, H + K:], o, lse, **kw)
-        ctx.save_for_backward(qkv, qk if plan is not None else None, o, lse, rope_pos)
-        ctx.heads, ctx.kv_heads, ctx.plan, ctx.kw = H, K, plan, kw
+        _read_again(ctx, kw, qkv, qk if plan is not None else None, o, lse, rope_pos)
+        ctx.heads, ctx.kv_heads, ctx.plan = H, K, plan
         return o
 
     @staticmethod
     @once_differentiable
     def backward(ctx, go):
-        qkv, qk, o, lse, rope_pos = ctx.saved_tensors
+        qkv, qk, o, lse, rope_pos, *shared = ctx.saved_tensors
         H, K = ctx.heads, ctx.kv_heads
         qk = qkv[:, :H + K] if qk is None else qk
         d = torch.empty(qkv.shape, dtype=qkv.dtype, device=qkv.device)
         eqlin.attention_backward(_aligned(go), qk[:, :H], qk[:, H:], qkv[:, H + K:], o, lse, d[:, :H], d[:, H:H + K],
-                                 d[:, H + K:], torch.empty_like(lse), **ctx.kw)
+                                 d[:, H + K:], torch.empty_like(lse), **ctx.kw, **dict(zip(_SHARED, shared)))
         if ctx.plan is not None:
             eqlin.rope(ctx.plan, rope_pos, d[:, :H + K], d[:, :H + K], inverse=True)
         return d, None, None, None, None, None
@@ -216,8 +226,8 @@ def qkv_attention(qkv: torch.Tensor, heads: int, kv_heads: int | None = None, *,
                   cap: float = 0.0) -> torch.Tensor:
     """Attention of a packed projection qkv [N, heads + 2 kv_heads, D] (queries,
     keys, values), whose queries and keys ``plan`` turns first.  ``pos`` [N,
-    axes] (or the same grid for every one of ``docs`` documents) serves both the plan and, with ``slopes``
-    [heads], the distance bias."""
+    axes] (or one grid for each of ``docs`` documents) serves both the plan
+    and, with ``slopes`` [heads], the distance bias."""
     kv_heads = heads if kv_heads is None else kv_heads
     _no_grad_for(pos=pos, slopes=slopes)
     if qkv.dim() != 3 or qkv.shape[1] != heads + 2 * kv_heads:

@@ -269,6 +269,21 @@ def test_rotary_and_attention_functions_take_any_strides():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("changed", ["offsets", "pos", "slopes"])
+def test_shared_tensors_changed_before_the_backward_are_refused(changed):
+    g = torch.Generator().manual_seed(4)
+    t = dict(offsets=torch.tensor([0, 20, 50], dtype=torch.int32, device="cuda"), pos=grid_positions(5, 10),
+             slopes=torch.tensor([0.5, 0.25], device="cuda"))
+    qkv = torch.randn((50, 6, 32), generator=g).bfloat16().cuda().requires_grad_(True)
+    for run in (lambda: ops.qkv_attention(qkv, 2, **t), lambda: ops.attention(qkv[:, :2], qkv[:, 2:4], qkv[:, 4:], **t)):
+        o = run()
+        o.sum().backward(retain_graph=True)
+        t[changed].mul_(1)
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            o.sum().backward()
+
+
+@pytest.mark.gpu
 def test_attention_on_another_stream_and_wait_limit():
     N, H, D = 300, 2, 64
     g = torch.Generator().manual_seed(0)

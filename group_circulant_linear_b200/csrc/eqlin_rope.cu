@@ -206,7 +206,7 @@ extern "C" eqlin_status_t eqlin_rope_apply(eqlin_rope_t r, eqlin_dtype_t dtype, 
   const int64_t width = heads * r->plan.Ch * r->plan.T;
   if (src_stride < width || dst_stride < width) return EQLIN_ERR_INVALID_ARG;
   if (N == 0) return EQLIN_OK;
-  if (!pos || !src || !dst) return EQLIN_ERR_INVALID_ARG;
+  if (!pos || !src || !dst || (src == dst && src_stride != dst_stride)) return EQLIN_ERR_INVALID_ARG;
   const int64_t es = dtype == EQLIN_F32 ? 4 : 2;
   if ((uintptr_t)src % es || (uintptr_t)dst % es || (uintptr_t)pos % 4) return EQLIN_ERR_MISALIGNED;
   rope::Params p = {};

@@ -640,6 +640,7 @@ def test_rope_refusals():
     assert call(ss=63) == -1 and call(ds=63) == -1 and call(pos=None) == -1 and call(src=None) == -1
     assert call(dst=None) == -1 and call(src=ctypes.c_void_p(4097)) == -3 and call(heads=70000, ss=2 ** 40, ds=2 ** 40) == -2
     assert call(heads=2 ** 62) == -2
+    assert call(ds=72) == -1                     # in place, but to other rows
     assert call(N=0) == 0
     import copy
     import pickle

@@ -269,6 +269,63 @@ def test_rotary_and_attention_functions_take_any_strides():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_more_than_2_to_the_31_elements(dtype):
+    # images are independent: the last ones of a long batch come out as they do alone, bit for bit
+    T, Ch, H, L, images, tail = 4, 16, 12, 197, 4800, 3
+    D = Ch * T
+    assert images * L * 3 * H * D > 2 ** 31
+    g = torch.Generator(device="cuda").manual_seed(8)
+    plan = eqlin.Rope(T, Ch, (4, 4))
+    kw = dict(plan=plan, pos=grid_positions(14, 14, lead=1), slopes=torch.full((H,), 0.1, device="cuda"), cap=20.0)
+    qkv = torch.randn((images * L, 3 * H, D), generator=g, device="cuda", dtype=dtype)
+    last = qkv[-tail * L:].clone()
+    outs = []
+    for x, n in ((qkv, images), (last, tail)):
+        x.requires_grad_(True)
+        o = ops.qkv_attention(x, H, docs=n, **kw)
+        go = torch.zeros_like(o)
+        go[-tail * L:] = torch.linspace(-1, 1, D, device="cuda")
+        o.backward(go)
+        outs.append([o[-tail * L:].detach().clone(), x.grad[-tail * L:].clone()])
+        x.grad = None
+    assert all(torch.equal(a, b) for a, b in zip(*outs)) and torch.isfinite(outs[0][1]).all()
+    del x, o, go
+    Cp, rows = H * 3 * Ch, 50
+    w, b = (torch.randn(Cp, generator=g, device="cuda", dtype=dtype) for _ in range(2))
+    feats = qkv.detach().view(images * L, Cp * T)
+    y = ops.group_layer_norm(feats, w, b, T)
+    assert torch.equal(y[-rows:], ops.group_layer_norm(feats[-rows:].clone(), w, b, T))
+
+
+@pytest.mark.gpu
+def test_two_threads_on_two_streams():
+    from concurrent.futures import ThreadPoolExecutor
+    plan = eqlin.Rope(4, 8, (2, 2))
+    g = torch.Generator().manual_seed(2)
+    pos, slopes = grid_positions(9, 11), torch.tensor([0.5, 0.25, 0.125], device="cuda")
+    w, c = (torch.randn(72, generator=g).bfloat16().cuda().requires_grad_(True) for _ in range(2))
+    xs = [torch.randn((b, 99, 288), generator=g).bfloat16().cuda() for b in (2, 5)]
+    torch.cuda.synchronize()
+
+    def run(x):
+        with torch.cuda.stream(torch.cuda.Stream()):
+            outs = []
+            for _ in range(20):
+                x = x.detach().requires_grad_(True)
+                h = ops.group_layer_norm(x, w, c, 4).reshape(-1, 9, 32)
+                y = ops.qkv_attention(h, 3, plan=plan, pos=pos, slopes=slopes, docs=x.shape[0], cap=20.0)
+                outs.append((y.detach(), *torch.autograd.grad(y.float().square().sum(), (x, w, c))))
+            torch.cuda.current_stream().synchronize()
+            return outs
+
+    alone = [run(x)[0] for x in xs]
+    with ThreadPoolExecutor(2) as pool:
+        for want, got in zip(alone, pool.map(run, xs)):
+            assert all(torch.equal(a, b) for once in got for a, b in zip(once, want))
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("changed", ["offsets", "pos", "slopes"])
 def test_shared_tensors_changed_before_the_backward_are_refused(changed):
     g = torch.Generator().manual_seed(4)

@@ -148,7 +148,7 @@ def _grid_positions(n, axes, device):
     i = torch.arange(n, device=device)
     if axes == 1:
         return i[:, None].float()
-    frames = 1 if axes == 2 else max(1, min(16, n))
+    frames = 1 if axes == 2 else min(16, n)
     per = max(1, -(-n // frames))
     side = max(1, math.isqrt(per))
     p = [i % per // side, i % per % side]

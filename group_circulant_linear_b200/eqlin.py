@@ -411,7 +411,8 @@ def norm_workspace(T: int, Cp: int, N: int, device=None) -> torch.Tensor:
 def norm_backward(gy: torch.Tensor, x: torch.Tensor, w: torch.Tensor, mean: torch.Tensor, rstd: torch.Tensor,
                   dx: torch.Tensor, dw: torch.Tensor, db: torch.Tensor, T: int, gsum: torch.Tensor | None = None,
                   res: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None):
-    """Gradients of the norm of x (or of x + res); see eqlin_norm_backward."""
+    """Gradients of the norm of x (or of x + res), both as the forward had them: not
+    xsum, whose rounding would go into dw.  See eqlin_norm_backward."""
     N, F = _shape2(gy, "gy")
     dt, dev, Cp = gy.dtype, gy.get_device(), w.shape[0]
     if Cp * T != F:

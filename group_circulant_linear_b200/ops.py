@@ -66,7 +66,8 @@ class _Norm(torch.autograd.Function):
 def group_layer_norm(x: torch.Tensor, w: torch.Tensor, b: torch.Tensor, T: int, eps: float = 1e-6,
                      res: torch.Tensor | None = None):
     """y [..., C'*T] from x and w, b [C']; with ``res`` the pair (y, x + res),
-    where y is the norm of the sum."""
+    where y is the norm of the sum.  The backward keeps both x and ``res``
+    rather than the sum, so that the weight's gradient is free of its rounding."""
     if res is not None and res.shape != x.shape:
         raise ValueError(f"res must have the shape of x, {tuple(x.shape)}, got {tuple(res.shape)}")
     return _Norm.apply(x, res, w, b, int(T), float(eps))

@@ -304,6 +304,11 @@ EQLIN_API int64_t eqlin_norm_workspace_bytes(int T, int64_t Cp, int64_t N);
  * and g = gy w,
  *   dx = rstd (g - mean_f g - xh mean_f(g xh)) + gsum     (the gradient of x and of res)
  *   dw[c] = sum_n sum_t gy xh,    db[c] = sum_n sum_t gy
+ * x, res, mean and rstd are those of the forward.  The stored sum must not
+ * stand in for x: mean and rstd belong to the unrounded one, and the rounding
+ * of the stored one goes into dw (2e-3 of it, in bf16, for a batch of 12608
+ * rows of 768, where the sums' own roundings are 2e-7).  So a training step
+ * keeps x and res until the backward, one tensor more than the sum alone.
  * gsum [N, F], the gradient of sum, may be NULL.  dx may be gy, gsum, x or res.  dw
  * and db [C'] are float32 and overwritten; sums run in a fixed order, without
  * atomics.  workspace: eqlin_norm_workspace_bytes, 16-byte aligned; calls that

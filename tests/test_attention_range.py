@@ -1,0 +1,149 @@
+"""Attention's gradients over the range of magnitudes that training meets.
+
+An f16 gradient is small (a mean over a long batch), or large (a loss scale),
+and so are the score gradients du that pass through 16 bits on their way into
+a product.  What the results may be off, in the root mean square over a
+tensor's values: every rounding to 16 bits is off by at most half a step, u
+relative, hence u / sqrt(3) in the mean of values spread over a step, and half
+the subnormals' spacing z where the output itself is that small.  Roundings
+are independent, so those of a sum's terms add up as their squares.  A quarter
+on top is room for the sample.  The FP32 part (scores, exponentials, sums)
+counts in full."""
+from __future__ import annotations
+
+import math
+
+import pytest
+import torch
+
+from group_circulant_linear_b200 import eqlin
+
+W = 2.0 ** -24
+
+
+def formula(q, k, v, go, lens, cap, scale):
+    """dq, dk, dv in 64 bits, and for each the mean squares that 16-bit operands add (in u^2), and the FP32 part."""
+    N, H, D = q.shape
+    K = k.shape[1]
+    val, sq, lin = ({n: torch.zeros(s, dtype=torch.float64, device=q.device) for n, s in
+                     dict(dq=(N, H, D), dk=(N, K, D), dv=(N, K, D)).items()} for _ in range(3))
+    lo = 0
+    for n in lens:
+        r = slice(lo, lo + n)
+        lo += n
+        for h in range(H):
+            kh = h // (H // K)
+            Q, Kh, V, G = q[r, h].double(), k[r, kh].double(), v[r, kh].double(), go[r, h].double()
+            s = scale * Q @ Kh.T
+            mag = scale * Q.abs() @ Kh.abs().T
+            g = torch.ones_like(s)
+            if cap:
+                t = torch.tanh(s / cap)
+                s, g = cap * t, 1 - t * t
+            P = torch.softmax(s, 1)
+            dP = G @ V.T
+            du = P * (dP - (P * dP).sum(1, keepdim=True)) * g
+            # relative error of P: D + 4 roundings of the score's products, a dozen of the score, the exponential's
+            # 2^-21; twice, for lse has them too; and a sum's n roundings
+            e = 2 * float(((D + 4) * W * mag + 12 * W * (s.abs() + cap) + 2.0 ** -21).max()) + math.sqrt(n) * W
+            e = e + 2 * D * W + (16 * W if cap else 0.0)              # dP, delta; 1 - tanh^2
+            val["dq"][r, h] = scale * du @ Kh
+            sq["dq"][r, h] = scale ** 2 * (du ** 2 @ Kh ** 2)
+            lin["dq"][r, h] = e * scale * (du ** 2 @ Kh ** 2).sqrt() + e * scale * (du @ Kh).abs()
+            val["dk"][r, kh] += scale * du.T @ Q
+            sq["dk"][r, kh] += scale ** 2 * (du.T ** 2 @ Q ** 2)
+            lin["dk"][r, kh] += e * scale * (du.T ** 2 @ Q ** 2).sqrt() + e * scale * (du.T @ Q).abs()
+            val["dv"][r, kh] += P.T @ G
+            sq["dv"][r, kh] += P.T ** 2 @ G ** 2
+            lin["dv"][r, kh] += e * (P.T ** 2 @ G ** 2).sqrt() + e * (P.T @ G).abs()
+    return val, sq, lin
+
+
+def gradients(q, k, v, go, lens, cap, scale):
+    N, H, _ = q.shape
+    off = torch.tensor([0] + list(torch.tensor(lens).cumsum(0)), dtype=torch.int32, device="cuda")
+    o, lse, delta = torch.empty_like(q), torch.empty((H, N), device="cuda"), torch.empty((H, N), device="cuda")
+    d = dict(dq=torch.empty_like(q), dk=torch.empty_like(k), dv=torch.empty_like(v))
+    eqlin.attention_forward(q, k, v, o, lse, offsets=off, cap=cap, scale=scale)
+    eqlin.attention_backward(go, q, k, v, o, lse, d["dq"], d["dk"], d["dv"], delta, offsets=off, cap=cap, scale=scale)
+    return d
+
+
+def compare(got, val, sq, lin, dt, weight=None):
+    u = torch.finfo(dt).eps / 2
+    z = torch.finfo(dt).smallest_normal * torch.finfo(dt).eps / 2
+    for n in val:
+        w = 1.0 if weight is None else weight[n]
+        assert torch.isfinite(got[n]).all(), n
+        off = float((w * (got[n].double() - val[n])).norm())
+        room = 1.25 * math.sqrt(float((w ** 2 * (u * u * (val[n] ** 2 + sq[n]) + z * z) / 3).sum())) + float((w * lin[n]).norm())
+        assert off <= room, f"{n}: off by {off}, {room} allowed, norm {float((w * val[n]).norm())}"
+
+
+def inputs(lens, H, K, D, dt, seed, spread, v_std=1.0, per_token=None):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    N = sum(lens)
+
+    def rnd(heads, std):
+        return (torch.randn((N, heads, D), generator=g, device="cuda") * std).to(dt)
+
+    q, k, v = rnd(H, 0.7), rnd(K, 0.7), rnd(K, v_std)
+    go = torch.randn((N, H, D), generator=g, device="cuda") * spread
+    if per_token is not None:
+        scale = 10.0 ** (torch.rand((N, 1, 1), generator=g, device="cuda") * per_token)
+        return q, k, v, (go * scale).to(dt), scale.double()
+    return q, k, v, go.to(dt), None
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("spread", [1.0, 1e-2, 1e-3, 1e-4])
+@pytest.mark.parametrize("lens,H,K,D,cap", [([8192], 1, 1, 64, 0.0), ([2048], 2, 1, 128, 0.0), ([1500, 37, 700], 2, 2, 64, 6.0),
+                                            ([3001], 1, 1, 32, 0.0), ([1500, 37, 700], 2, 1, 104, 6.0)])
+def test_small_gradients_keep_their_bits(lens, H, K, D, cap, spread, dtype):
+    q, k, v, go, _ = inputs(lens, H, K, D, dtype, D + len(lens), spread)
+    scale = D ** -0.5
+    compare(gradients(q, k, v, go, lens, cap, scale), *formula(q, k, v, go, lens, cap, scale), dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[2, 3, 5, 1, 40], [150, 300]])
+def test_large_f16_gradients_stay_finite(lens, D):
+    # a loss scale: dP is past f16's largest number, the results are not
+    dt, scale = torch.float16, D ** -0.5
+    q, k, v, go, _ = inputs(lens, 2, 2, D, dt, 5, 3.0e3, v_std=4.0)
+    val, sq, lin = formula(q, k, v, go, lens, 0.0, scale)
+    assert all(float(t.abs().max()) < 6.0e4 for t in val.values())
+    compare(gradients(q, k, v, go, lens, 0.0, scale), val, sq, lin, dt)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_f16_gradients_of_tokens_of_very_different_weight(D):
+    # each token's dq by its own measure: go spans four decades between tokens
+    lens, dt, scale = [1200, 900], torch.float16, D ** -0.5
+    q, k, v, go, by = inputs(lens, 2, 1, D, dt, 6, 1e-4, per_token=4.0)
+    val, sq, lin = formula(q, k, v, go, lens, 0.0, scale)
+    got = gradients(q, k, v, go, lens, 0.0, scale)
+    compare(got, val, sq, lin, dt)
+    compare({"dq": got["dq"]}, {"dq": val["dq"]}, sq, lin, dt, weight={"dq": 1 / by})
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("D", [64, 128])
+def test_f16_gradients_that_grow_along_a_document(D):
+    # the factor of a row follows what passes by: values (queries' gradients) grow from 1e-4 to 1e4 and fall again
+    n, dt, scale = 1300, torch.float16, D ** -0.5
+    up = 10.0 ** torch.linspace(-4, 4, n // 2, device="cuda")
+    for turn in (torch.cat([up, up.flip(0)]), torch.cat([up.flip(0), up])):
+        q, k, v, go, _ = inputs([n], 1, 1, D, dt, 7, 1.0)
+        v = (v.float() * turn[:, None, None].sqrt()).to(dt)
+        go = (go.float() * turn[:, None, None].sqrt() * 0.01).to(dt)
+        val, sq, lin = formula(q, k, v, go, [n], 0.0, scale)
+        compare(gradients(q, k, v, go, [n], 0.0, scale), val, sq, lin, dt)
+        zero = torch.zeros_like(go)
+        zero[-3:] = go[-3:]                      # gradients of the last tokens only, nothing but zeros before
+        val, sq, lin = formula(q, k, v, zero, [n], 0.0, scale)
+        compare(gradients(q, k, v, zero, [n], 0.0, scale), val, sq, lin, dt)
+    assert not any(t.any() for t in gradients(q, k, v, torch.zeros_like(go), [n], 0.0, scale).values())

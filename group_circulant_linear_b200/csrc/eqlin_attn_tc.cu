@@ -147,7 +147,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
           if (!ok) break;
           // positions go with V: its slot is free once the softmax has used them
           if (AXES && kv) {
-            sidev.store(spos + (slot >> 1) * kMaxAxes * CW, 0.f, 0.f, lane);
+            sidev.store(spos + (slot >> 1) * kMaxAxes * CW, 0.f, lane);
             if (j + 1 < key_tiles) sidev.fetch(p, w.head, c0 + CW, hi, lane);
           }
           ok = bring<DP, CW, 1>(tails, slot, ring, land, kv_full, &maps.m[1 + kv], kv_head, c0, nc, wait,

@@ -161,7 +161,15 @@ template <int AXES, bool STAT, int TILE_ROWS> struct Side {
       }
     }
   }
-  __device__ __forceinline__ void store(float* dst, float up, float down, int lane) const {
+  // delta's largest magnitude, behind the rest
+  __device__ __forceinline__ void store_top(float* dst, int lane) const {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) m = max(m, __float_as_uint(fabsf(delta[i])));   // ordered as the floats are
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) dst[(kMaxAxes + 2) * TILE_ROWS] = __uint_as_float(m);
+  }
+  __device__ __forceinline__ void store(float* dst, float up, int lane) const {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
 #pragma unroll
@@ -169,7 +177,7 @@ template <int AXES, bool STAT, int TILE_ROWS> struct Side {
       if (STAT) {
         // past the document's end lse is +inf: P = 0 there
         dst[kMaxAxes * TILE_ROWS + lane + 32 * i] = fmaf(lse[i], -kLog2e, up);
-        dst[(kMaxAxes + 1) * TILE_ROWS + lane + 32 * i] = delta[i] * down;
+        dst[(kMaxAxes + 1) * TILE_ROWS + lane + 32 * i] = delta[i];
       }
     }
   }

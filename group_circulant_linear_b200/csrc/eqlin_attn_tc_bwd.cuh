@@ -13,9 +13,20 @@
 //   else:  e += (P g) X,  dq += du X
 //
 // P and du are rounded to the inputs' type as operands of those products, half
-// a step each; sums are FP32 in TMEM.  In f16 P carries a factor 2^8 on its
-// way to dv, so that probabilities of long documents (1e-5 and less) stay out
-// of the subnormals.
+// a step each; sums are FP32 in TMEM.  f16's range is narrow: du is about the
+// gradient over the document's length, below 6e-5 it loses bits, and under a
+// loss scale dP alone can pass 65504.  So in f16 both carry powers of two, which
+// the FP32 results are freed of.  P, at most 1, has 2^12.  A row of du has its
+// own, f: with top the row's largest |dP| + |delta| in a tile, f top is brought
+// to 2^12 .. 2^13 in the first tile and again in any tile where it passes 2^14
+// (so is du f then, with room for a P that rounding puts above 1), and what the
+// row has summed up follows.  A row's results are then off by at most 2^-37 of
+// its largest top for each of its du, beside the roundings.  The other look at dP
+// costs an f16 backward 9 to 14 % (12544 tokens, 6 heads of 64: 1.24 to 1.38 ms;
+// 64 x 197 tokens, 12 heads, capped, two-axis bias: 175 to 191 us; 2048 windows of
+// 49 tokens, 3 heads of 32: 161 to 183 us).  Bounds from max|do| and max|v|, found
+// in shared memory before the scores, cost long documents 2 to 6 % and short ones
+// up to 25 %.
 //
 // delta = do.o from the stored o would carry o's rounding (its own and that of
 // P in the forward) into every du; for short documents that is more than all
@@ -53,9 +64,10 @@ template <int DP, bool KEYS> struct BwdCfg {
   static constexpr int MOV_PANEL = CW * 128;
   static constexpr int MOV = DP / 64 * MOV_PANEL;               // bytes of one moving tile
   static constexpr int SLOTS = DP > 64 ? 2 : 4;
-  static constexpr int SIDE = (kMaxAxes + (KEYS ? 2 : 0)) * CW * 4;            // positions, lse, delta of a slot
-  static constexpr int NBAR = 2 + 3 * SLOTS + 5;
-  static constexpr int EPS = NWG == 2 ? 2 * ROWS * 4 : 0;       // eps of the two warpgroups
+  // positions, lse, delta and the largest |delta| (in 16 bytes) of a slot
+  static constexpr int SIDE = (kMaxAxes + (KEYS ? 2 : 0)) * CW * 4 + (KEYS ? 16 : 0);
+  static constexpr int NBAR = 2 + 3 * SLOTS + 6;
+  static constexpr int EPS = NWG == 2 ? 4 * ROWS * 4 : 0;       // eps and top of the two warpgroups
   static constexpr int SMEM = 2 * OWN + SLOTS * (2 * MOV + SIDE) + EPS + NWG * 4 * STAGE + NBAR * 8 + 32 + kListInts * 4 + 1024;
   static_assert(ACC1 + DP <= TMEM, "TMEM columns");
   static_assert(BLOCKS * SMEM <= 227 * 1024, "shared memory");
@@ -69,16 +81,20 @@ template <int DP, bool KEYS> struct BwdCfg {
 // save two more: under a cap diff is delta - dP and gain tanh^2 - 1, so that du
 // is right, while eps and P g (KEYS = false) come out negated, and so does not
 // their product.
+// In f16 P comes out times 2^kUp, du and the terms of eps times the row's f.
+constexpr float kUp16 = 12.f, kDown16 = 1.f / 4096.f;     // P's power of two in f16, and its inverse
 template <int AXES, bool CAP, bool KEYS, bool SMALL, bool EDGE, int CW, typename E>
 __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, const float* side, int c0, const float* own,
-                                       float lse2, float delta, const Score& sc, int left, uint64_t& eps, uint32_t* pp,
-                                       uint32_t* pd) {
+                                       float lse2, float delta, float f, const Score& sc, int left, uint64_t& eps,
+                                       uint32_t* pp, uint32_t* pd) {
   constexpr bool F16 = Pair<E>::fmt == 0;
-  constexpr float kDown = F16 ? 1.f / 256.f : 1.f;
+  const float fd = F16 ? f * kDown16 : 1.f;          // of dP and delta: P brings the rest
+  const uint64_t plus_f = pk2(fd, fd), minus_f = pk2(-fd, -fd);
   const uint64_t k2 = CAP ? pk2(sc.cap2, sc.cap2) : pk2(sc.scale2, sc.scale2);
   const uint64_t in = pk2(sc.in, sc.in), slope = pk2(-sc.slope2, -sc.slope2);
-  const uint64_t minus = pk2(-1.f, -1.f), down = pk2(-kDown, -kDown);
-  const uint64_t row_off = pk2(-lse2, -lse2), row_delta = pk2(CAP ? delta : -delta, CAP ? delta : -delta);
+  const uint64_t minus = pk2(-1.f, -1.f);
+  const float off_row = F16 ? kUp16 - lse2 : -lse2, delta_row = CAP ? delta * fd : -delta * fd;
+  const uint64_t row_off = pk2(off_row, off_row), row_delta = pk2(delta_row, delta_row);
 #pragma unroll
   for (int j = 0; j < 32; j += 4) {
     float d[4];
@@ -115,11 +131,14 @@ __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, c
         if (i >= left) a = 0.f;
         if (i + 1 >= left) b = 0.f;
       }
-      // delta - dP under a cap, else dP - delta
+      // delta - dP under a cap, else dP - delta (the factors are powers of two: their products are exact)
       uint64_t diff;
       if (KEYS) {
-        if (CAP) diff = F16 ? fma2(dp, down, h ? dl.y : dl.x) : fma2(dp, minus, h ? dl.y : dl.x);
-        else diff = fma2(h ? dl.y : dl.x, minus, F16 ? mul2(dp, mul2(down, minus)) : dp);
+        const uint64_t de = h ? dl.y : dl.x;
+        if (CAP) diff = F16 ? fma2(de, plus_f, mul2(dp, minus_f)) : fma2(dp, minus, de);
+        else diff = F16 ? fma2(de, minus_f, mul2(dp, plus_f)) : fma2(de, minus, dp);
+      } else if (F16) {
+        diff = fma2(dp, CAP ? minus_f : plus_f, row_delta);
       } else {
         diff = CAP ? fma2(dp, minus, row_delta) : add2(dp, row_delta);
       }
@@ -137,6 +156,30 @@ __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, c
   }
 }
 
+// The largest magnitude of a row's 64 values x, y, of which `left` and `left` - `apart` are inside.
+__device__ __forceinline__ float top64(uint32_t* x, uint32_t* y, int left, int apart) {
+  if (left < 32 + apart) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (i >= left) x[i] = 0u;
+      if (i >= left - apart) y[i] = 0u;
+    }
+  }
+  float a = 0.f, b = 0.f, c = 0.f, d = 0.f;
+#pragma unroll
+  for (int i = 0; i < 32; i += 4) {
+    a = fmaxf(fmaxf(a, fabsf(__uint_as_float(x[i]))), fabsf(__uint_as_float(x[i + 1])));
+    b = fmaxf(fmaxf(b, fabsf(__uint_as_float(x[i + 2]))), fabsf(__uint_as_float(x[i + 3])));
+    c = fmaxf(fmaxf(c, fabsf(__uint_as_float(y[i]))), fabsf(__uint_as_float(y[i + 1])));
+    d = fmaxf(fmaxf(d, fabsf(__uint_as_float(y[i + 2]))), fabsf(__uint_as_float(y[i + 3])));
+  }
+  return fmaxf(fmaxf(a, b), fmaxf(c, d));
+}
+// The power of two that brings top into [2^12, 2^13), at most 2^100, and its inverse.
+__device__ __forceinline__ uint32_t top_exponent(float top) { return max((__float_as_uint(top) >> 23) & 255u, 39u); }
+__device__ __forceinline__ float factor_of(uint32_t e) { return __uint_as_float((266u - e) << 23); }
+__device__ __forceinline__ float inverse_of(uint32_t e) { return __uint_as_float((e - 12u) << 23); }
+
 template <int DP, typename E, int AXES, bool CAP, bool KEYS>
 __global__ void __launch_bounds__(BwdCfg<DP, KEYS>::THREADS, BwdCfg<DP, KEYS>::BLOCKS)
 attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Maps maps) {
@@ -144,15 +187,15 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
   constexpr int CW = C::CW, NWG = C::NWG;
   constexpr uint32_t KID = KEYS ? K_ATTN_DKV : K_ATTN_DQ;
   constexpr bool F16 = Pair<E>::fmt == 0;
-  constexpr float kUp = F16 ? 8.f : 0.f;             // P's factor, as an exponent (KEYS)
-  constexpr float kDown = F16 ? 1.f / 256.f : 1.f;
+  constexpr float kUp = F16 ? kUp16 : 0.f, kDown = F16 ? kDown16 : 1.f;   // P's factor (as an exponent), its inverse
   constexpr int MMA = NWG * 4, LOAD = NWG * 4 + 1;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
   uint8_t* ring = smem + 2 * C::OWN;
   float* side = reinterpret_cast<float*>(ring + C::SLOTS * 2 * C::MOV);
   constexpr int SIDE_F = C::SIDE / 4;
-  float* eps_sum = side + C::SLOTS * SIDE_F;
+  float* eps_sum = side + C::SLOTS * SIDE_F;         // [2][ROWS]
+  float* tops = eps_sum + 2 * ROWS;                  // [2][ROWS]
   uint8_t* stage = reinterpret_cast<uint8_t*>(eps_sum + C::EPS / 4);
   uint64_t* bars = reinterpret_cast<uint64_t*>(stage + NWG * 4 * STAGE);
   uint64_t* own_full = bars;
@@ -164,7 +207,8 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
   uint64_t* p_full = s_full + 1;
   uint64_t* acc_full = p_full + 1;
   uint64_t* eps_full = acc_full + 1;
-  uint64_t* drain = eps_full + 1;
+  uint64_t* top_full = eps_full + 1;
+  uint64_t* drain = top_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(bars + C::NBAR);
   int* abort_word = reinterpret_cast<int*>(tmem_slot + 1);
   int* local_err = abort_word + 1;
@@ -199,6 +243,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
     mbar_init(p_full, NWG * 128);
     mbar_init(acc_full, 1);
     mbar_init(eps_full, NWG * 128);
+    mbar_init(top_full, NWG * 128);
     mbar_init(drain, 1);
     *abort_word = 0;
     for (int i = 0; i < 4; ++i) local_err[i] = 0;
@@ -247,7 +292,8 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
                                 site(KID, 2, 1), item, lane);
           if (!ok) break;
           if (AXES || KEYS) {
-            sides.store(side + slot * SIDE_F, kUp, kDown, lane);
+            sides.store(side + slot * SIDE_F, kUp, lane);
+            if constexpr (KEYS && F16) sides.store_top(side + slot * SIDE_F, lane);
             const bool last = j + 1 == tiles;
             if (!last || g + 1 < passes) sides.fetch(p, q_head + g + (last ? 1 : 0), last ? lo : c0 + CW, hi, lane);
           }
@@ -363,17 +409,61 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
       const bool any = r0 < hi, live = lane < hi - r0;
       const int64_t row = (int64_t)r0 + lane;
       uint64_t eps2 = 0;
+      uint32_t fe = 0;                               // the row's factor in f16: factor_of(fe)
       for (int g = 0; ok && g < passes; ++g) {
         const Score sc = score_of(p, q_head + g);
         for (int j = 0; j < tiles; ++j, ++item) {
           const int nc = min(hi - lo - j * CW, CW), slot = item % C::SLOTS;
+          const float* sd = side + slot * SIDE_F;
           ok = wwait_all(s_full, item & 1, limit, abort_flag, err, site(KID, 0, 0), item);
           if ((AXES || KEYS) && ok)
             ok = wwait_all(full + slot, (item / C::SLOTS) & 1, limit, abort_flag, err, site(KID, 0, 1), item);
           if (!ok) break;
           tc_fence_after();
+          if constexpr (F16) {
+            float top = 0.f;
+            if (any) {                               // this warpgroup's two chunks
+              uint32_t x[32], y[32];
+              tmem_ld32(my + C::DP_COL + wg * 32, x);
+              tmem_ld32(my + C::DP_COL + (wg + NWG) * 32, y);
+              tmem_wait_ld();
+              tie32(x);
+              tie32(y);
+              top = top64(x, y, nc - wg * 32, NWG * 32);
+            }
+            if (NWG == 2) {                          // and the other's, as with eps below
+              tops[wg * ROWS + quarter * 32 + lane] = top;
+              mbar_arrive(top_full);
+              ok = wwait_all(top_full, item & 1, limit, abort_flag, err, site(KID, 0, 5), item);
+              if (!ok) break;
+              top = fmaxf(tops[quarter * 32 + lane], tops[ROWS + quarter * 32 + lane]);
+            }
+            top += KEYS ? sd[(kMaxAxes + 2) * CW] : fabsf(delta);
+            if (g == 0 && j == 0) {
+              fe = top_exponent(top);
+            } else if (any) {
+              const bool grow = top * factor_of(fe) > 16384.f;
+              if (__any_sync(0xffffffffu, grow)) {
+                // every product before these scores is done: the sums may be changed
+                const uint32_t now = grow ? top_exponent(top) : fe;
+                const float fix = factor_of(now) * inverse_of(fe);
+                fe = now;
+                eps2 = mul2(eps2, pk2(fix, fix));
+#pragma unroll 1
+                for (int c = wg; c < d16; c += NWG) {
+                  uint32_t x[16];
+                  tmem_ld_32x32b_x16(my + C::ACC1 + c * 16, x);
+                  tmem_wait_ld();
+                  tie16(x);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__uint_as_float(x[k]) * fix);
+                  tmem_st_32x32b_x16(my + C::ACC1 + c * 16, x);
+                }
+              }
+            }
+          }
           if (any) {
-            const float* sd = side + slot * SIDE_F;
+            const float f = F16 ? factor_of(fe) : 1.f;
             // this warpgroup's chunks: wg, wg + NWG
 #pragma unroll 1
             for (int c = wg; c * 32 < nc; c += NWG) {
@@ -395,12 +485,12 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
                   }
               }
               if (CAP && !KEYS && left < 32)
-                grad32<AXES, CAP, KEYS, false, CAP && !KEYS, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, left, eps2,
+                grad32<AXES, CAP, KEYS, false, CAP && !KEYS, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, f, sc, left, eps2,
                                                                     pp, pd);
               else if (CAP && all_small<32>(reinterpret_cast<const float*>(rs), sc, live))
-                grad32<AXES, CAP, KEYS, true, false, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, 32, eps2, pp, pd);
+                grad32<AXES, CAP, KEYS, true, false, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, f, sc, 32, eps2, pp, pd);
               else
-                grad32<AXES, CAP, KEYS, false, false, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, sc, 32, eps2, pp, pd);
+                grad32<AXES, CAP, KEYS, false, false, CW, E>(rs, rd, sd, c * 32, own, lse2, delta, f, sc, 32, eps2, pp, pd);
               tmem_st_32x32b_x16(my + C::S_COL + c * 32, pp);
               tmem_st_32x32b_x16(my + C::DP_COL + c * 32, pd);
             }
@@ -411,7 +501,7 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
         }
       }
       if (!ok) break;
-      const float guess = delta;
+      const float guess = delta, inv_f = F16 ? inverse_of(fe) : 1.f;
       if (i + 1 < count) enter(i + 1);
       ok = wwait_all(acc_full, (item - 1) & 1, limit, abort_flag, err, site(KID, 0, 3), item);
       if (!ok) break;
@@ -430,12 +520,13 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
           if (!ok) break;
           eps = eps_sum[quarter * 32 + lane] + eps_sum[ROWS + quarter * 32 + lane];
         }
-        if (live && wg == 0) p.delta[(int64_t)q_head * p.N + row] = CAP ? guess - eps : guess + eps;
+        if (live && wg == 0) p.delta[(int64_t)q_head * p.N + row] = CAP ? guess - eps * inv_f : guess + eps * inv_f;
       }
       if (any) {
 #pragma unroll
         for (int c = 0; c < DP / 32; ++c) {
           if (c * 32 >= p.D || c % NWG != wg) continue;
+          const float fix = p.scale * inv_f;
           uint32_t x[32], y[32], pk[16];
           tmem_ld32(my + C::ACC0 + c * 32, x);
           tmem_ld32(my + C::ACC1 + c * 32, y);
@@ -453,10 +544,10 @@ attn_tc_bwd_kernel(const __grid_constant__ Params p, const __grid_constant__ Map
           for (int i = 0; i < 32; i += 2) {
             float a = __uint_as_float(y[i]), b = __uint_as_float(y[i + 1]);
             if (!KEYS) {
-              a = fmaf(-eps, __uint_as_float(x[i]), a);
-              b = fmaf(-eps, __uint_as_float(x[i + 1]), b);
+              a = fmaf(-eps * kDown, __uint_as_float(x[i]), a);
+              b = fmaf(-eps * kDown, __uint_as_float(x[i + 1]), b);
             }
-            pk[i / 2] = Pair<E>::pack(a * p.scale, b * p.scale);
+            pk[i / 2] = Pair<E>::pack(a * fix, b * fix);
           }
           if (KEYS) store32(st, pk, static_cast<E*>(p.dk) + (int64_t)r0 * p.dks + kh, p.dks, hi - r0, c * 32, p.D, lane);
           else store32(st, pk, static_cast<E*>(p.dq) + (int64_t)r0 * p.dqs + qh0, p.dqs, hi - r0, c * 32, p.D, lane);

@@ -265,10 +265,14 @@ def expand_dense(W: torch.Tensor) -> torch.Tensor:
 class DenseEQViTBlock(nn.Module):
     """The same block with every EQ-Linear applied as the expanded dense
     matrix (``F.linear``), sharing the parameters of ``src``.  Context only:
-    the naive layer the pages measure against."""
+    the naive layer the pages measure against.  It has plain attention: a
+    block with rotary positions, a cap, a distance bias or shared key heads is
+    refused."""
 
     def __init__(self, src: EQViTBlock, dtype=None):
         super().__init__()
+        if src.rope is not None or src.cap or src.slopes is not None or src.kv_heads != src.heads:
+            raise ValueError("the dense block has no rotary positions, cap, distance bias or shared key heads")
         self.src, self.dtype = src, dtype
 
     def _lin(self, layer: EQLinear, x: torch.Tensor) -> torch.Tensor:

@@ -110,6 +110,8 @@ def _flat_pos(pos, N, axes, period):
     grid for every image of a batch)."""
     if axes and pos.shape[-1] != axes:
         raise ValueError(f"pos must have {axes} axes, got {pos.shape[-1]}")
+    if N == 0:                                # the grid of every image of an empty batch
+        return pos.new_empty((0, pos.shape[-1]), dtype=torch.float32)
     p = pos.reshape(-1, pos.shape[-1]).to(torch.float32)
     if p.shape[0] != N:
         if p.shape[0] != period or period == 0 or N % period:

@@ -5,7 +5,8 @@ import pytest
 import torch
 import torch.nn as nn
 
-from group_circulant_linear_b200.block import DenseEQViTBlock, EQViTBlock
+from group_circulant_linear_b200 import ops
+from group_circulant_linear_b200.block import DenseEQViTBlock, EQViTBlock, grid_positions
 
 
 def bare(**kw):
@@ -23,3 +24,24 @@ def test_dense_block_refuses_what_it_does_not_compute(option):
         DenseEQViTBlock(bare(**option))
     DenseEQViTBlock(bare())
     DenseEQViTBlock(bare(native=False))
+
+
+def test_positions_of_an_empty_batch():
+    grid = torch.zeros((49, 2))
+    for pos in (grid, grid.expand(0, 49, 2), grid[:0]):
+        assert ops._flat_pos(pos, 0, 2, 0).shape == (0, 2)
+    with pytest.raises(ValueError, match="axes"):
+        ops._flat_pos(grid, 0, 3, 0)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lead", [(0, 49), (3, 0), (0,)])
+def test_an_empty_batch_runs_both_ways(lead, dtype):
+    blk = EQViTBlock(32, 4, 4, dtype=dtype, native=True, kv_heads=2, rope_sections=(2, 2), cap=8.0, distance=True)
+    x = torch.empty((*lead, 128), dtype=dtype, device="cuda", requires_grad=True)
+    kw = dict(offsets=torch.zeros(1, dtype=torch.int32, device="cuda")) if len(lead) == 1 else {}
+    y = blk(x, grid_positions(7, lead[-1] // 7) if len(lead) == 2 else torch.empty((0, 2), device="cuda"), **kw)
+    assert y.shape == x.shape
+    grads = torch.autograd.grad(y, [x, *blk.parameters()], torch.empty_like(y))
+    assert grads[0].shape == x.shape and not any(g.any() for g in grads[1:])

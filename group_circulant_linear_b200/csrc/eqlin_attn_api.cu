@@ -48,7 +48,7 @@ eqlin_status_t describe(const eqlin_attention_t* a, eqlin_dtype_t dtype, attn::P
   p.scale = a->scale;
   p.cap = a->cap;
   p.err = a->err;
-  p.wait_limit = a->wait_limit ? a->wait_limit : kDefaultWaitLimit;
+  p.wait_limit = a->wait_limit == 0 ? kDefaultWaitLimit : a->wait_limit == UINT32_MAX ? 0 : a->wait_limit;
   return EQLIN_OK;
 }
 

@@ -336,6 +336,9 @@ def destroy(h: Handle):
 # These calls belong to no handle.  They run on the tensors' device (all on one)
 # and, unless told otherwise, on its current stream.
 
+NO_POLLS = 0xFFFFFFFF             # wait_limit: a wait that is not over when it begins runs out
+
+
 class _On:
     """Make the tensors' device current for a call and find the stream."""
 

@@ -381,7 +381,8 @@ typedef struct {
     int32_t *err;             /* device, 4 words as in eqlin_error_detail, zeroed by the caller: a
                                  wait that ran out is recorded here (outputs are then undefined);
                                  or NULL */
-    uint32_t wait_limit;      /* as in eqlin_set_wait_limit; 0 for the default */
+    uint32_t wait_limit;      /* as in eqlin_set_wait_limit; 0 for the default, UINT32_MAX for no polls:
+                                 a wait that is not over when it begins runs out */
 } eqlin_attention_t;
 
 EQLIN_API eqlin_status_t eqlin_attention_forward(const eqlin_attention_t *a, eqlin_dtype_t dtype,

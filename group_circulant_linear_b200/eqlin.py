@@ -592,6 +592,18 @@ def attention_backward(go: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: to
             _ptr(delta, torch.float32, (q.shape[1], q.shape[0]), "delta", dev), st), "eqlin_attention_backward")
 
 
+def attention_error(err: torch.Tensor) -> int:
+    """What the attention calls that were given ``err`` recorded: 0, or -6 for a
+    wait that timed out; clears it.  Waits for the current stream: synchronise
+    others that the calls ran on before."""
+    if not isinstance(err, torch.Tensor) or err.dtype != torch.int32 or tuple(err.shape) != (4,):
+        raise TypeError("err must be an int32 tensor of 4")
+    if err.tolist()[0] == 0:
+        return 0
+    err.zero_()
+    return -6
+
+
 # ------------------------------------------------------- allocating helpers
 
 class EQLinear:

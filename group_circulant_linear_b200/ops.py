@@ -11,6 +11,11 @@
 They run the kernels of ``include/eqlin.h`` on the tensors' device and current
 stream, in the tensors' type (float16, bfloat16 or float32), and have first
 derivatives only.  Positions, slopes and offsets are not differentiated.
+
+In float16 and bfloat16 attention's kernels wait for their copies and products
+within bounds.  ``err``, an int32 tensor of four zeros, records a wait that ran
+out in either direction (results are then undefined); read it with
+``eqlin.attention_error``.  Without one it goes unnoticed.
 """
 from __future__ import annotations
 
@@ -180,13 +185,13 @@ def _period(N, docs, offsets):
 
 def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *, docs: int = 1, offsets: torch.Tensor | None = None,
               max_len: int | None = None, pos: torch.Tensor | None = None, slopes: torch.Tensor | None = None,
-              scale: float | None = None, cap: float = 0.0) -> torch.Tensor:
+              scale: float | None = None, cap: float = 0.0, err: torch.Tensor | None = None) -> torch.Tensor:
     """Attention within documents on packed tokens: q [N, heads, D], k and v
     [N, kv_heads, D] -> [N, heads, D]; see ``eqlin.attention_forward``."""
     _no_grad_for(pos=pos, slopes=slopes)
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must be [N, heads, D]")
-    kw = dict(docs=docs, offsets=offsets, max_len=max_len, slopes=slopes, scale=scale, cap=cap,
+    kw = dict(docs=docs, offsets=offsets, max_len=max_len, slopes=slopes, scale=scale, cap=cap, err=err,
               pos=None if pos is None else _flat_pos(pos, q.shape[0], 0, _period(q.shape[0], docs, offsets)))
     return _Attention.apply(q, k, v, kw)
 
@@ -226,7 +231,7 @@ class _QkvAttention(torch.autograd.Function):
 def qkv_attention(qkv: torch.Tensor, heads: int, kv_heads: int | None = None, *, plan: eqlin.Rope | None = None,
                   pos: torch.Tensor | None = None, slopes: torch.Tensor | None = None, docs: int = 1,
                   offsets: torch.Tensor | None = None, max_len: int | None = None, scale: float | None = None,
-                  cap: float = 0.0) -> torch.Tensor:
+                  cap: float = 0.0, err: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of a packed projection qkv [N, heads + 2 kv_heads, D] (queries,
     keys, values), whose queries and keys ``plan`` turns first.  ``pos`` [N,
     axes] (or one grid for each of ``docs`` documents) serves both the plan
@@ -242,5 +247,5 @@ def qkv_attention(qkv: torch.Tensor, heads: int, kv_heads: int | None = None, *,
     p = None if pos is None else _flat_pos(pos, qkv.shape[0], plan.axes if plan is not None else 0,
                                              _period(qkv.shape[0], docs, offsets))
     kw = dict(docs=docs, offsets=offsets, max_len=max_len, slopes=slopes, pos=p if slopes is not None else None,
-              scale=scale, cap=cap)
+              scale=scale, cap=cap, err=err)
     return _QkvAttention.apply(qkv, int(heads), int(kv_heads), plan, p if plan is not None else None, kw)

@@ -5,7 +5,8 @@ from __future__ import annotations
 import pytest
 import torch
 
-from group_circulant_linear_b200 import eqlin
+from group_circulant_linear_b200 import block, eqlin, ops
+from group_circulant_linear_b200.block import EQViTBlock
 
 FWD, DQ = 4, 5                            # kernels in the record
 
@@ -80,3 +81,58 @@ def test_waits_of_calls_that_give_up_do_not_disturb_others():
         eqlin.attention_forward(q, k, v, mine, l3, err=e3, **kw)
     torch.cuda.synchronize()
     assert int(e[0]) == 1 and not e3.any() and torch.equal(o, mine) and torch.equal(lse, l3)
+
+
+def without_polls(monkeypatch):
+    """Give every attention call no polls for its waits."""
+    desc = eqlin._attention_desc
+    monkeypatch.setattr(eqlin, "_attention_desc", lambda *a: desc(*a[:-1], eqlin.NO_POLLS))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("packed", [False, True])
+def test_functions_record_a_wait_that_runs_out(packed, monkeypatch):
+    err = torch.zeros(4, dtype=torch.int32, device="cuda")
+    x = torch.randn((90, 6, 32), device="cuda").bfloat16().requires_grad_(True)
+    run = (lambda: ops.qkv_attention(x, 2, err=err)) if packed else \
+        (lambda: ops.attention(x[:, :2], x[:, 2:4], x[:, 4:], err=err))
+    o = run()
+    o.sum().backward()
+    assert eqlin.attention_error(err) == 0
+    with monkeypatch.context() as m:
+        without_polls(m)
+        run()
+        assert eqlin.attention_error(err) == -6 and eqlin.attention_error(err) == 0
+        o = run()
+        assert eqlin.attention_error(err) == -6
+        o.sum().backward()                # the backward records it, too
+        assert eqlin.attention_error(err) == -6
+    assert torch.equal(run(), run()) and eqlin.attention_error(err) == 0
+
+
+@pytest.mark.gpu
+def test_the_block_reports_a_wait_that_runs_out(monkeypatch):
+    import copy
+
+    blk = EQViTBlock(32, 4, 4, native=True)
+    twin = copy.deepcopy(blk)
+    x = torch.randn((2, 60, 128), device="cuda").bfloat16()
+    blk(x)
+    assert blk.get_error() == 0
+    with monkeypatch.context() as m:
+        without_polls(m)
+        blk(x)
+        assert twin.get_error() == 0 and blk.get_error() == -6 and blk.get_error() == 0
+        with pytest.raises(RuntimeError, match="timeout"):
+            block.main(["--native", "--model", "eq-vit-s", "--batch", "2", "--iters", "1", "--warmup", "1"])
+    blk(x)
+    assert blk.get_error() == 0 and EQViTBlock(32, 4, 4).get_error() == 0
+
+
+def test_attention_error_takes_a_record():
+    assert eqlin.attention_error(torch.zeros(4, dtype=torch.int32)) == 0
+    err = torch.tensor([1, 1040, 0, 0], dtype=torch.int32)
+    assert eqlin.attention_error(err) == -6 and not err.any()
+    for bad in (None, torch.zeros(3, dtype=torch.int32), torch.zeros(4)):
+        with pytest.raises(TypeError):
+            eqlin.attention_error(bad)

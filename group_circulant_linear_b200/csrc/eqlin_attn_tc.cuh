@@ -361,8 +361,9 @@ __device__ __forceinline__ Score score_of(const Params& p, int head) {
 }
 
 // tanh, for two arguments.  Where all of a warp's arguments are small (|x| <=
-// kSmall, the usual case below a cap) an odd polynomial, x q(x^2): 2e-8 off at
-// most, a third of a score's own rounding under a cap of 30 (coefficients: a
+// kSmall, the usual case below a cap) an odd polynomial, x q(x^2): 2.8e-8 off at
+// most, the FP32 roundings apart (with them 4.5e-7 relative), which under a cap of
+// 30 is less than the FP32 step of a score of 8 to 16 (coefficients: a
 // weighted least-squares fit of tanh(x)/x refined to equal ripple), 3
 // instructions per score on the FMA pipes.  Otherwise 1 - 2 / (1 + e^{2x}), a
 // few 2^-24 off in absolute terms everywhere, which is what a score needs; its

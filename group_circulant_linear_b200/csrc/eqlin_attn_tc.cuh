@@ -365,12 +365,16 @@ __device__ __forceinline__ Score score_of(const Params& p, int head) {
 // most, the FP32 roundings apart (with them 4.5e-7 relative), which under a cap of
 // 30 is less than the FP32 step of a score of 8 to 16 (coefficients: a
 // weighted least-squares fit of tanh(x)/x refined to equal ripple), 3
-// instructions per score on the FMA pipes.  Otherwise 1 - 2 / (1 + e^{2x}), a
-// few 2^-24 off in absolute terms everywhere, which is what a score needs; its
-// two MUFU operations (8 cycles of a scheduler each) would otherwise be two
-// thirds of the softmax's time.  tanh.approx would be one, but is only good to
-// 2^-11.
-constexpr float kSmall = 0.6f;
+// instructions per score on the FMA pipes.  Otherwise 1 - 2 / (1 + e^{2x}) for
+// the arguments that are not: a few 2^-24 off in absolute terms, which cap times
+// over would be too much for a small one (under a cap of 1e6 a score of 1 would be
+// off by 0.2).  The forward makes the difference above kLargeCap alone: at that
+// cap it is 6e-5 of a score, an eighth of f16's half step in P (12544 tokens, 6
+// heads of 64, scores of spread 2 under a cap of 3: 1.18 ms, 1.67 below it, too; the
+// backward 2.09 and 2.22, which is not worth a third form there).  Its two MUFU operations (8 cycles of a scheduler each) would be
+// two thirds of the softmax's time.  tanh.approx would be one, but is only good
+// to 2^-11.
+constexpr float kSmall = 0.6f, kLargeCap = 256.f;
 __device__ __forceinline__ uint64_t q_small2(uint64_t x) {      // tanh(x) / x
   const uint64_t z = mul2(x, x);
   uint64_t q = pk2(0.01497695967555046f, 0.01497695967555046f);
@@ -379,8 +383,16 @@ __device__ __forceinline__ uint64_t q_small2(uint64_t x) {      // tanh(x) / x
   q = fma2(q, z, pk2(-0.33331209421157837f, -0.33331209421157837f));
   return fma2(q, z, pk2(0.9999996423721313f, 0.9999996423721313f));
 }
-__device__ __forceinline__ float tanh_any(float raw, const Score& s) {
+__device__ __forceinline__ float tanh_large(float raw, const Score& s) {
   return fmaf(-2.f, rcp(1.f + ex2(raw * s.twoin)), 1.f);
+}
+__device__ __forceinline__ void tanh_any2(float& a, float& b, const Score& s) {      // raw scores in
+  const uint64_t x = mul2(pk2(a, b), pk2(s.in, s.in));
+  float xa, xb, pa, pb;
+  unpk2(x, xa, xb);
+  unpk2(mul2(x, q_small2(x)), pa, pb);
+  a = fabsf(xa) <= kSmall ? pa : tanh_large(a, s);
+  b = fabsf(xb) <= kSmall ? pb : tanh_large(b, s);
 }
 // Are all of the warp's raw scores, N per row, small enough for the polynomial?
 // Only live rows count: results must not depend on what lies behind a document.
@@ -423,9 +435,16 @@ __device__ __forceinline__ void transform32(float* s, const float* pos, int c0, 
         const uint64_t v = pk2(s[i], s[i + 1]);
         unpk2(mul2(v, q_small2(mul2(v, in))), s[i], s[i + 1]);
       }
+    } else if (sc.cap2 <= kLargeCap * kLog2e) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) s[i] = sc.out * tanh_large(s[i], sc);
     } else {
 #pragma unroll
-      for (int i = 0; i < 32; ++i) s[i] = sc.out * tanh_any(s[i], sc);
+      for (int i = 0; i < 32; i += 2) {
+        tanh_any2(s[i], s[i + 1], sc);
+        s[i] *= sc.out;
+        s[i + 1] *= sc.out;
+      }
     }
   }
   if constexpr (AXES > 0) {

@@ -117,7 +117,8 @@ __device__ __forceinline__ void grad32(const uint32_t* rs, const uint32_t* rd, c
         } else {
           float a, b;
           unpk2(x, a, b);
-          x = pk2(tanh_any(a, sc), tanh_any(b, sc));
+          tanh_any2(a, b, sc);
+          x = pk2(a, b);
         }
         gain = fma2(x, x, minus);
       }

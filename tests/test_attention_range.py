@@ -147,3 +147,50 @@ def test_f16_gradients_that_grow_along_a_document(D):
         val, sq, lin = formula(q, k, v, zero, [n], 0.0, scale)
         compare(gradients(q, k, v, zero, [n], 0.0, scale), val, sq, lin, dt)
     assert not any(t.any() for t in gradients(q, k, v, torch.zeros_like(go), [n], 0.0, scale).values())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap", [1.0e4, 1.0e6])
+def test_a_cap_far_above_the_scores_is_as_good_as_none(cap, D, dtype):
+    # cap tanh(u / cap) is u (1 - (u / cap)^2 / 3), and u is 30 at most: nothing beside the roundings.  Short documents:
+    # all of their columns lie in a last, partial tile.
+    lens, scale = [31, 20, 7, 100, 1000], D ** -0.5
+    q, k, v, go, _ = inputs(lens, 2, 1, D, dtype, 8, 1.0)
+    q = q * 4
+    val, sq, lin = formula(q, k, v, go, lens, 0.0, scale)
+    compare(gradients(q, k, v, go, lens, cap, scale), val, sq, lin, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n", [40, 1000])
+def test_scores_far_below_a_cap_beside_one_near_it(n, dtype):
+    # one query's scores come near a large cap; the others' must not take its form of the tanh
+    D, cap, odd = 64, 3.0e4, 3
+    scale = D ** -0.5
+    q, k, v, go, _ = inputs([n], 1, 1, D, dtype, 9, 1.0)
+    q[odd] *= 4.0e3 / float(q[odd].abs().max())
+    k[5] = q[odd, 0] / 4.0e3 * 50.0                    # u = 0.125 |q| |k|, of the order of the cap
+    assert 0.7 * cap < float(scale * (q[odd, 0].double() @ k[5, 0].double())) < 30 * cap
+    go[odd] = 0                                        # its own gradients, one-hot, are another matter
+    keep = torch.arange(n, device="cuda") != odd
+    o, lse = torch.empty_like(q), torch.empty((1, n), device="cuda")
+    eqlin.attention_forward(q, k, v, o, lse, cap=cap, scale=scale)
+    val, sq, lin = formula(q, k, v, go, [n], cap, scale)
+    # formula's bound of the FP32 part, of the rows that are looked at; a dozen roundings of the score, not of the cap
+    u = scale * q[keep, 0].double() @ k[:, 0].double().T
+    mag = scale * q[keep, 0].double().abs() @ k[:, 0].double().abs().T
+    e = 2 * float(((D + 4) * W * mag + 12 * W * u.abs() + 2.0 ** -21).max()) + math.sqrt(n) * W + 2 * D * W
+    P = torch.softmax(cap * torch.tanh(u / cap), 1)
+    V = v[:, 0].double()
+    half = torch.finfo(dtype).eps / 2
+    want = P @ V
+    room = 1.25 * half * math.sqrt(float((want ** 2).sum() + (P ** 2 @ V ** 2).sum()) / 3) \
+        + e * float((P ** 2 @ V ** 2).sqrt().norm() + want.norm())
+    assert float((o[keep, 0].double() - want).norm()) <= room
+    got = gradients(q, k, v, go, [n], cap, scale)["dq"][keep]
+    room = 1.25 * half * math.sqrt(float((val["dq"][keep] ** 2).sum() + sq["dq"][keep].sum()) / 3) \
+        + e * float(sq["dq"][keep].sqrt().norm() + val["dq"][keep].norm())
+    assert float((got.double() - val["dq"][keep]).norm()) <= room

@@ -9,7 +9,11 @@
 //
 // The output is rescaled only when a row's maximum grows by more than 2^8
 // (kLag): until then P is at most 256, far inside both types, and O and l
-// share the older m, so the quotient is the same.
+// share the older m, so the quotient is the same.  (A refinement, published
+// since, of the online softmax of Milakov and Gimelshein, 2018.)  In f16 P and l
+// carry 2^7 more: P is then at most 2^15, and what f16's smallest step loses of a
+// small P is 2^-32 of the row's largest, so that a hundred thousand keys which
+// share little of a row still count.
 //
 // Bound by the exponentials (128 x 128 of them take the four schedulers' MUFU
 // pipes 1024 cycles, the products 512) and by latency: TMEM and the registers
@@ -33,6 +37,7 @@ namespace eqlin {
 namespace attn_tc {
 
 constexpr float kLag = 8.f;
+template <typename E> constexpr float kLift = Pair<E>::fmt == 0 ? 7.f : 0.f;
 
 template <int DP, int CW_> struct FwdCfg {
   static constexpr int CW = CW_;                              // keys of a tile
@@ -233,7 +238,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
       float own[AXES ? AXES : 1];
 #pragma unroll
       for (int a = 0; a < AXES; ++a) own[a] = live ? p.pos[row * AXES + a] : 0.f;
-      float m = -INFINITY, l = 0.f;                           // m in base-2 units
+      float m = -INFINITY, l = 0.f;                           // m in base-2 units, kLift below the maximum
       for (int j = 0; j < key_tiles; ++j, ++step) {
         const int nc = min(hi - lo - j * CW, CW);
         // S is there; without SEP with it, in order, every earlier product
@@ -325,7 +330,7 @@ __global__ void __launch_bounds__(kThreads, 2) attn_tc_fwd_kernel(const __grid_c
             }
             top = fmaxf(fmaxf(t0, t1), v[31]);
           }
-          top *= sc.scale2;                                 // scale > 0
+          top = kLift<E> > 0.f ? fmaf(top, sc.scale2, -kLift<E>) : top * sc.scale2;          // scale > 0
           if (AXES) top = fmaxf(top, -FLT_MAX);             // where every key of the tile is infinitely far away
         }
         if (C::SEP && j > 0) {                              // P's columns, and O, are free once the last product is done

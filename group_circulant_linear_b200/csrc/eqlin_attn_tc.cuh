@@ -363,17 +363,18 @@ __device__ __forceinline__ Score score_of(const Params& p, int head) {
 // tanh, for two arguments.  Where all of a warp's arguments are small (|x| <=
 // kSmall, the usual case below a cap) an odd polynomial, x q(x^2): 2.8e-8 off at
 // most, the FP32 roundings apart (with them 4.5e-7 relative), which under a cap of
-// 30 is less than the FP32 step of a score of 8 to 16 (coefficients: a
-// weighted least-squares fit of tanh(x)/x refined to equal ripple), 3
-// instructions per score on the FMA pipes.  Otherwise 1 - 2 / (1 + e^{2x}) for
-// the arguments that are not: a few 2^-24 off in absolute terms, which cap times
-// over would be too much for a small one (under a cap of 1e6 a score of 1 would be
-// off by 0.2).  The forward makes the difference above kLargeCap alone: at that
-// cap it is 6e-5 of a score, an eighth of f16's half step in P (12544 tokens, 6
-// heads of 64, scores of spread 2 under a cap of 3: 1.18 ms, 1.67 below it, too; the
-// backward 2.09 and 2.22, which is not worth a third form there).  Its two MUFU operations (8 cycles of a scheduler each) would be
-// two thirds of the softmax's time.  tanh.approx would be one, but is only good
-// to 2^-11.
+// 30 is less than the FP32 step of a score of 8 to 16 (coefficients: a weighted
+// least-squares fit of tanh(x)/x refined to equal ripple), 3 instructions per
+// score on the FMA pipes.  Otherwise 1 - 2 / (1 + e^{2x}) for the arguments that
+// are not: a few 2^-24 off in absolute terms, which cap times over would be too
+// much for a small one (under a cap of 1e6 a score of 1 would be off by 0.2).  The
+// forward makes the difference above kLargeCap alone: at that cap it is 6e-5 of a
+// score, an eighth of f16's half step in P (12544 tokens, 6 heads of 64, scores of
+// spread 2 under a cap of 3: 1.18 ms, 1.67 below it, too; the backward takes 2.22
+// ms, 2.09 without the difference, which is not worth a third form there).  The
+// two MUFU operations (8 cycles of a scheduler each) for every score would be two
+// thirds of the softmax's time.  tanh.approx would be one, but is only good to
+// 2^-11.
 constexpr float kSmall = 0.6f, kLargeCap = 256.f;
 __device__ __forceinline__ uint64_t q_small2(uint64_t x) {      // tanh(x) / x
   const uint64_t z = mul2(x, x);

@@ -194,3 +194,32 @@ def test_scores_far_below_a_cap_beside_one_near_it(n, dtype):
     room = 1.25 * half * math.sqrt(float((val["dq"][keep] ** 2).sum() + sq["dq"][keep].sum()) / 3) \
         + e * float(sq["dq"][keep].sqrt().norm() + val["dq"][keep].norm())
     assert float((got.double() - val["dq"][keep]).norm()) <= room
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+@pytest.mark.parametrize("n,D", [(300, 64), (4096, 64), (65536, 64), (4096, 128)])
+def test_many_small_probabilities_beside_a_large_one(n, D, dtype):
+    # one key takes nearly all of each query's attention, and its value is 0: what is left are the other keys'
+    # probabilities, e^-17.4 each, below f16's smallest number
+    g = torch.Generator(device="cuda").manual_seed(n + D)
+    scale = D ** -0.5
+    q = torch.full((n, 1, D), 1.0, device="cuda", dtype=dtype)
+    k = torch.zeros((n, 1, D), device="cuda", dtype=dtype)
+    at = n // 3
+    k[at] = 17.4 / (scale * D)
+    v = (1 + torch.rand((n, 1, D), generator=g, device="cuda")).to(dtype)
+    v[at] = 0
+    o, lse = torch.empty_like(q), torch.empty((1, n), device="cuda")
+    eqlin.attention_forward(q, k, v, o, lse, scale=scale)
+    s = scale * q[:1, 0].double() @ k[:, 0].double().T              # every query is the same
+    P = torch.softmax(s, 1)
+    want, mass = P @ v[:, 0].double(), P @ v[:, 0].double().abs()
+    u = torch.finfo(dtype).eps / 2
+    z = torch.finfo(dtype).smallest_normal * u
+    # the output's rounding, P's, and in f16 half a step of its subnormals, 2^-25, on a P that carries 2^7; the FP32 part:
+    # score and exponential (as in formula), sums of n terms
+    e = 2 * ((D + 4) * W * 17.4 + 12 * W * 17.4 + 2.0 ** -21) + n * W
+    tol = u * want + z + (u + e) * mass + (2.0 ** -32 if dtype == torch.float16 else 0.0) * v[:, 0].double().sum(0)
+    assert bool(((o[:, 0].double() - want).abs() <= tol).all())
+    assert float((lse.double() - torch.logsumexp(s, 1)).abs().max()) <= e + 4 * W * 17.4

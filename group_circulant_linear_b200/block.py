@@ -152,7 +152,8 @@ class GroupLayerNorm(nn.Module):
     c shared by its T group positions (so it commutes with a cyclic shift).
 
     ``native`` runs the library's kernel, which also takes a residual: then
-    ``norm(x, res)`` is the pair of the normalised sum and the sum itself."""
+    ``norm(x, res)`` is the pair of the normalised sum and the sum itself.  It
+    takes inputs of the parameters' type, and does not promote others."""
 
     def __init__(self, Cp: int, T: int, eps: float = 1e-6, dtype=torch.bfloat16, device="cuda", native: bool = False):
         super().__init__()

@@ -235,7 +235,11 @@ def qkv_attention(qkv: torch.Tensor, heads: int, kv_heads: int | None = None, *,
     """Attention of a packed projection qkv [N, heads + 2 kv_heads, D] (queries,
     keys, values), whose queries and keys ``plan`` turns first.  ``pos`` [N,
     axes] (or one grid for each of ``docs`` documents) serves both the plan
-    and, with ``slopes`` [heads], the distance bias."""
+    and, with ``slopes`` [heads], the distance bias.
+
+    In float16 and bfloat16 the turned queries and keys are rounded to the type,
+    as ``rotary`` rounds them, and so are their gradients before they are turned
+    back: two roundings of half a step each where the others have one."""
     kv_heads = heads if kv_heads is None else kv_heads
     _no_grad_for(pos=pos, slopes=slopes)
     if qkv.dim() != 3 or qkv.shape[1] != heads + 2 * kv_heads:

@@ -5,7 +5,9 @@ of what the arithmetic may lose, element by element: half a step of the
 output's type (``u``), half a step for each operand that the tensor cores take
 in 16 bits (the probabilities P and the score gradients), and FP32 roundings
 along the longest chain of additions (2^-24 each) on the sums of absolute
-values.  They were fixed before the kernels first ran.
+values.  They were fixed before the kernels first ran, and narrowed twice with
+them since: where the norm's backward and the attention's no longer read a sum
+or an output as stored (x + res, and o for delta).
 """
 from __future__ import annotations
 

@@ -223,3 +223,21 @@ def test_many_small_probabilities_beside_a_large_one(n, D, dtype):
     tol = u * want + z + (u + e) * mass + (2.0 ** -32 if dtype == torch.float16 else 0.0) * v[:, 0].double().sum(0)
     assert bool(((o[:, 0].double() - want).abs() <= tol).all())
     assert float((lse.double() - torch.logsumexp(s, 1)).abs().max()) <= e + 4 * W * 17.4
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cap", [0.0, 6.0])
+@pytest.mark.parametrize("D", [40, 64, 128])
+def test_f16_gradients_scale_exactly_with_powers_of_two(D, cap):
+    # go times 2^s leaves every f16 operand's bits as they are: so are the results', times 2^s
+    lens, scale = [700, 1, 64, 300], D ** -0.5
+    q, k, v, go, by = inputs(lens, 4, 2, D, torch.float16, 10, 0.05, per_token=1.5)
+    # only what has all its bits times 2^-7, too: an f16 below 2^-7 would fall among the subnormals (2^-14 and less) there
+    go = (go.float() * 2.0 ** -7).half().float().mul(2.0 ** 7).half()
+    base = gradients(q, k, v, go, lens, cap, scale)
+    for s in (-7, -3, 4, 8):
+        for n, got in gradients(q, k, v, go * 2.0 ** s, lens, cap, scale).items():
+            # 2^-14 itself may come of a subnormal, which has fewer bits
+            normal = (got.abs() > 2.0 ** -14) & (base[n].abs() > 2.0 ** -14)
+            assert int(normal.sum()) > normal.numel() // 4
+            assert torch.equal(got.double()[normal], base[n].double()[normal] * 2.0 ** s), (n, s)

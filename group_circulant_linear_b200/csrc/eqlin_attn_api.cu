@@ -19,6 +19,10 @@ eqlin_status_t describe(const eqlin_attention_t* a, eqlin_dtype_t dtype, attn::P
   if (!isfinite(a->scale) || !(a->scale > 0.f) || !isfinite(a->cap) || a->cap < 0.f) return EQLIN_ERR_INVALID_ARG;
   if (a->axes < 0 || (a->axes > 0 && !a->slopes)) return EQLIN_ERR_INVALID_ARG;
   if (a->axes > attn::kMaxAxes) return EQLIN_ERR_UNSUPPORTED;
+  // what the kernels scale scores by stays a normal FP32 number
+  auto far = [](float x) { return x < 0x1p-120f || x > 0x1p120f; };
+  if (far(a->scale) || (a->cap > 0.f && (far(a->cap) || far(a->scale / a->cap) || far(a->cap / a->scale))))
+    return EQLIN_ERR_UNSUPPORTED;
   if (a->heads > 65536 || a->head_dim > attn::kMaxHeadDim || a->tokens > 0x7fffff00)   // a tile's end fits 32 bits
     return EQLIN_ERR_UNSUPPORTED;
   const int64_t es = dtype == EQLIN_F32 ? 4 : 2;

@@ -380,7 +380,8 @@ typedef struct {
     const float *pos;         /* device, [tokens, axes], or NULL with axes = 0 */
     const float *slopes;      /* device, [heads] */
     int axes;                 /* 0 (no bias) to 3 */
-    float scale, cap;         /* scale > 0; cap >= 0, 0: scores are not capped */
+    float scale, cap;         /* scale > 0; cap >= 0, 0: scores are not capped; each, and scale / cap,
+                                 within 2^-120 .. 2^120 */
     int32_t *err;             /* device, 4 words as in eqlin_error_detail, zeroed by the caller: a
                                  wait that ran out is recorded here (outputs are then undefined);
                                  or NULL */

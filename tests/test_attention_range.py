@@ -11,6 +11,7 @@ on top is room for the sample.  The FP32 part (scores, exponentials, sums)
 counts in full."""
 from __future__ import annotations
 
+import ctypes
 import math
 
 import pytest
@@ -241,3 +242,27 @@ def test_f16_gradients_scale_exactly_with_powers_of_two(D, cap):
             normal = (got.abs() > 2.0 ** -14) & (base[n].abs() > 2.0 ** -14)
             assert int(normal.sum()) > normal.numel() // 4
             assert torch.equal(got.double()[normal], base[n].double()[normal] * 2.0 ** s), (n, s)
+
+
+def test_scales_and_caps_beyond_fp32_are_refused():
+    L, one = eqlin.lib(), ctypes.c_void_p(4096)      # never followed: each call is refused first
+
+    def call(scale, cap):
+        d = eqlin.AttentionDesc(tokens=6, heads=2, kv_heads=2, head_dim=8, q_stride=16, k_stride=16, v_stride=16, o_stride=16,
+                                docs=2, scale=scale, cap=cap)
+        fwd = L.eqlin_attention_forward(ctypes.byref(d), eqlin.BF16, one, one, one, one, one, None)
+        bwd = L.eqlin_attention_backward(ctypes.byref(d), eqlin.BF16, one, 16, one, one, one, one, one, one, 16, one, 16, one,
+                                         16, one, None)
+        assert fwd == bwd
+        return fwd
+
+    assert call(0.125, 1.0e38) == -2 and call(0.125, 1.0e-38) == -2 and call(1.0e-38, 0.0) == -2 and call(1.0e38, 0.0) == -2
+    assert call(2.0 ** -70, 2.0 ** 70) == -2 and call(2.0 ** 70, 2.0 ** -70) == -2
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16, torch.float32])
+def test_the_largest_cap(dtype):
+    lens, scale = [31, 100, 200], 0.125
+    q, k, v, go, _ = inputs(lens, 2, 1, 64, dtype, 8, 1.0)
+    compare(gradients(q, k, v, go, lens, 2.0 ** 116, scale), *formula(q, k, v, go, lens, 0.0, scale), dtype)

@@ -33,11 +33,17 @@ def _no_grad_for(**tensors):
 
 # -------------------------------------------------------------------- norm
 
+def _rows(x, F):
+    """[..., F] as the norm's kernels read it: [N, F], one row after the other from a 16-byte boundary on."""
+    x = x.reshape(-1, F).contiguous()
+    return x.clone() if x.data_ptr() % 16 else x
+
+
 class _Norm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, res, w, b, T, eps):
-        x2 = x.reshape(-1, x.shape[-1]).contiguous()
-        r2 = None if res is None else res.reshape(x2.shape).contiguous()
+        x2 = _rows(x, x.shape[-1])
+        r2 = None if res is None else _rows(res, x.shape[-1])
         y = torch.empty_like(x2)
         s = None if res is None else torch.empty_like(x2)
         mean = torch.empty(x2.shape[0], dtype=torch.float32, device=x.device)
@@ -58,8 +64,8 @@ class _Norm(torch.autograd.Function):
         shape = (gy if gy is not None else gs).shape
         if gy is None:                        # only the sum was used
             return gs, (gs if r is not None else None), torch.zeros_like(w), torch.zeros_like(w), None, None
-        gy = gy.reshape(x.shape).contiguous()
-        gs = None if gs is None else gs.reshape(x.shape).contiguous()
+        gy = _rows(gy, x.shape[1])
+        gs = None if gs is None else _rows(gs, x.shape[1])
         dx = torch.empty_like(x)
         dw = torch.empty(w.shape, dtype=torch.float32, device=w.device)
         db = torch.empty_like(dw)

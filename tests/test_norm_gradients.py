@@ -59,3 +59,25 @@ def test_weight_gradient_of_a_sum_has_no_16_bit_rounding(call, dtype):
     assert float((gb.double() - db).norm()) <= tol * float(rss_b) + out * float(db.norm())
     half = torch.finfo(dtype).eps / 2
     assert float((gx.double() - dx).norm()) <= (half + tol) * float(dx.norm())
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_rows_that_start_anywhere(dtype):
+    # contiguous tensors at an odd element of a larger buffer, as attention takes them
+    N, Cp, T = 37, 24, 4
+    gen = torch.Generator(device="cuda").manual_seed(1)
+
+    def odd(t):
+        buf = torch.empty(t.numel() + 1, dtype=dtype, device="cuda")
+        buf[1:] = t.flatten()
+        return buf[1:].view(t.shape)
+
+    x, r, gy, gs = (torch.randn((N, Cp * T), generator=gen, device="cuda").to(dtype) for _ in range(4))
+    w, b = (torch.randn(Cp, generator=gen, device="cuda").to(dtype) for _ in range(2))
+    outs = []
+    for place in (lambda t: t.clone(), odd):
+        leaves = [place(t).requires_grad_(True) for t in (x, r, w, b)]
+        y, s = ops.group_layer_norm(leaves[0], leaves[2], leaves[3], T, res=leaves[1])
+        outs.append([y, s, *torch.autograd.grad((y, s), leaves, (place(gy), place(gs)))])
+    assert all(torch.equal(p, q) for p, q in zip(*outs))

@@ -25,10 +25,11 @@
 //              cap and a bias, in a document's last tile.
 // CW = 128 is taken for heads of up to 64 features (its columns need them) in
 // documents that are long on average: from 384 tokens, with a cap or a bias from
-// 768.  CW 128 against 64, heads of 64, us: 12544 tokens, 6 heads 359 : 531
-// (biased 618 : 746, capped 625 : 761); 30 x 900 tokens, 6 heads 92 : 110 (capped
-// and biased 191 : 190); 30 x 500, 12 heads 61 : 66 (137 : 111); 30 x 384, 12 heads
-// 36 : 41 (62 : 68); 30 x 300, 12 heads 37 : 34; 64 x 197, 12 heads 42 : 41 (90 : 65).
+// 768.  CW 128 against 64, heads of 64, us, inputs cold: 12544 tokens, 6 heads 373 :
+// 539 (two-axis bias 542 : 701, capped 634 : 758); 30 x 900 tokens, 6 heads 100 :
+// 118 (capped and biased 206 : 197); 30 x 500, 12 heads 70 : 74 (150 : 120); 30 x
+// 384, 12 heads 44 : 48 (77 : 79); 30 x 300, 12 heads 45 : 41; 64 x 197, 12 heads
+// 49 : 47 (105 : 74).
 #include <float.h>
 
 #include "eqlin_attn_tc.cuh"

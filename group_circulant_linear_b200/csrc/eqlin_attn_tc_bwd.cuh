@@ -23,8 +23,8 @@
 // row has summed up follows.  A row's results are then off by at most 2^-37 of
 // its largest top for each of its du, beside the roundings.  The other look at dP
 // costs an f16 backward 9 to 14 % (12544 tokens, 6 heads of 64: 1.24 to 1.38 ms;
-// 64 x 197 tokens, 12 heads, capped, two-axis bias: 175 to 191 us; 2048 windows of
-// 49 tokens, 3 heads of 32: 161 to 183 us).  Bounds from max|do| and max|v|, found
+// 64 x 197 tokens, 12 heads, capped, two-axis bias: 175 to 193 us; 2048 windows of
+// 49 tokens, 3 heads of 32: 161 to 181 us).  Bounds from max|do| and max|v|, found
 // in shared memory before the scores, cost long documents 2 to 6 % and short ones
 // up to 25 %.
 //
@@ -41,7 +41,7 @@
 // from, chunk by chunk: the accumulators take the rest of the columns, and the
 // SM's other block fills the gap until the next scores.  Measured, bf16, both
 // kernels: 12544 tokens, 6 heads of 64, 1.23 ms (490 TFLOP/s of the formula's five
-// products); 64 x 197 tokens, 12 heads, capped, two-axis bias, 173 us; one tile of
+// products); 64 x 197 tokens, 12 heads, capped, two-axis bias, 179 us; one tile of
 // 64 moving rows takes an SM about 1550 cycles, 512 of them exponentials.
 #pragma once
 

@@ -216,7 +216,9 @@ class EQViTBlock(nn.Module):
         # a plain attribute: a buffer would follow the module into 16 bits
         self.slopes = torch.tensor([2.0 ** (-8.0 * (h + 1) / heads) for h in range(heads)], dtype=torch.float32,
                                    device=device) if distance else None
-        self.err = torch.zeros(4, dtype=torch.int32, device=device) if native else None    # of the attention, see get_error
+        self.errs = {}                             # the attention's records by device, see get_error
+        if native:
+            self._err(torch.empty(0, device=device).device)
         self.norm1 = GroupLayerNorm(Cp, T, dtype=dtype, device=device, native=native)
         self.qkv = EQLinear(Cp, (heads + 2 * self.kv_heads) * (Cp // heads), T, dtype=dtype, device=device, generator=g)
         self.proj = EQLinear(Cp, Cp, T, dtype=dtype, device=device, generator=g)
@@ -237,16 +239,19 @@ class EQViTBlock(nn.Module):
             raise ValueError("rotary positions and the distance bias need pos")
         if self.slopes is not None and self.slopes.device != x.device:
             self.slopes = self.slopes.to(x.device)
-        if self.err.device != x.device:
-            self.err = torch.zeros(4, dtype=torch.int32, device=x.device)
         h = self.qkv(self.norm1(x))
         o = ops.qkv_attention(h.reshape(-1, self.heads + 2 * self.kv_heads, (self.Cp // self.heads) * self.T), self.heads,
                               self.kv_heads, plan=self.rope, pos=pos,
                               slopes=self.slopes,
                               docs=x.shape[0] if offsets is None else 1, offsets=offsets, max_len=max_len, cap=self.cap,
-                              err=self.err)
+                              err=self._err(x.device))
         y, x = self.norm2(x, self.proj(o.reshape(x.shape)))
         return x + self.fc2(F.gelu(self.fc1(y)))
+
+    def _err(self, device: torch.device) -> torch.Tensor:
+        if device not in self.errs:
+            self.errs[device] = torch.zeros(4, dtype=torch.int32, device=device)
+        return self.errs[device]
 
     def get_error(self) -> int:
         """Device-side status of the block's layers and, where it is native, its
@@ -254,9 +259,7 @@ class EQViTBlock(nn.Module):
         (results are then undefined); clears it.  Synchronise streams other than
         the current one before."""
         status = [eqlin.get_error(layer.h) for layer in (self.qkv, self.proj, self.fc1, self.fc2)]
-        if self.err is not None:
-            status.append(eqlin.attention_error(self.err))
-        return min(status)
+        return min(status + [eqlin.attention_error(err) for err in self.errs.values()])
 
 
 def grid_positions(height: int, width: int, frames: int | None = None, lead: int = 0, device="cuda") -> torch.Tensor:

@@ -365,10 +365,10 @@ EQLIN_API eqlin_status_t eqlin_rope_apply(eqlin_rope_t r, eqlin_dtype_t dtype, c
  * or one another.  q, k, v, o and their gradients are 16-byte aligned.
  * f16 and bf16 run on the tensor cores (probabilities and score gradients pass
  * through the inputs' type on their way into a product, all sums are FP32), f32
- * on the CUDA cores.  Their forward has two tile widths and takes one by the mean
- * length of a call's documents, tokens / docs: a document's o and lse may differ
- * in their last bits between calls that put it beside others.  The same call
- * gives the same bits every time.
+ * on the CUDA cores.  The f16 and bf16 forward has two tile widths and takes one
+ * by the mean length of a call's documents, tokens / docs: a document's o and lse
+ * may differ in their last bits between calls that put it beside others.  The
+ * same call gives the same bits every time.
  */
 typedef struct {
     int64_t tokens, heads, kv_heads, head_dim;

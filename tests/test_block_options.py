@@ -45,3 +45,22 @@ def test_an_empty_batch_runs_both_ways(lead, dtype):
     assert y.shape == x.shape
     grads = torch.autograd.grad(y, [x, *blk.parameters()], torch.empty_like(y))
     assert grads[0].shape == x.shape and not any(g.any() for g in grads[1:])
+
+
+def test_the_attention_record_is_kept_for_each_device(monkeypatch):
+    import copy
+
+    from group_circulant_linear_b200 import eqlin
+
+    blk = bare(errs={})
+    for name in ("qkv", "proj", "fc1", "fc2"):
+        object.__setattr__(blk, name, type("Layer", (), {"h": None}))
+    monkeypatch.setattr(eqlin, "get_error", lambda h: 0)
+    cpu, meta = torch.device("cpu"), torch.device("meta")
+    err = blk._err(cpu)
+    assert blk._err(cpu) is err and blk._err(meta) is not err and blk._err(cpu) is err
+    del blk.errs[meta]
+    assert blk.get_error() == 0
+    err[0] = 1
+    twin = copy.deepcopy(blk.errs)
+    assert blk.get_error() == -6 and blk.get_error() == 0 and int(twin[cpu][0]) == 1
